@@ -188,7 +188,7 @@ def _prepare_attn(c, seed):
         pages, shape = None, (S, nkv, cap, d)
     n = lambda *s, std=1.0: torch.empty(s, device="cuda").normal_(0.0, std, generator=g)
     st = dict(case=c, lens=lens, counts=counts, parent=_i32(parent), base=_i32(lens), cap=cap,
-              q=n(S * rows, nq * d, std=1.5).to(dt), kb=n(S, nkv, rows, d).to(dt), vb=n(S, nkv, rows, d).to(dt),
+              q=n(S * rows, nq * d, std=1.5).to(dt), kb=n(S, rows, nkv, d).to(dt), vb=n(S, rows, nkv, d).to(dt),
               out=torch.zeros(S * rows, nq * d, dtype=dt, device="cuda"),
               pages=None if pages is None else _i32(pages), pool=shape[0] if pages else 0)
     for x in "kv":
@@ -217,10 +217,10 @@ def _prepare_kv(c, seed):
     st = dict(case=c, base_l=base, valid_l=valid, index_l=index, cap=cap, base=_i32(base), valid=_i32(valid),
               index=None if index is None else _i32(index), pages=None if pages is None else _i32(pages), pool=pool)
     for x in "kv":
-        t = torch.empty((L, S, nkv, rows, d), device="cuda").normal_(0.0, 1.0, generator=g)
-        t *= torch.empty((L, S, nkv, rows, 1), device="cuda").uniform_(0.25, 4.0, generator=g)
+        t = torch.empty((L, S, rows, nkv, d), device="cuda").normal_(0.0, 1.0, generator=g)
+        t *= torch.empty((L, S, rows, nkv, 1), device="cuda").uniform_(0.25, 4.0, generator=g)
         st[x + "b"] = t.to(dt)
-        st[x + "o"] = torch.zeros((L, S, nkv, rows, d), dtype=dt, device="cuda")
+        st[x + "o"] = torch.zeros((L, S, rows, nkv, d), dtype=dt, device="cuda")
         st[x + "c"] = torch.zeros(shape, dtype=torch.uint8, device="cuda")
         st[x + "e"] = torch.full(shape[:-1], EXP_BIAS, dtype=torch.uint8, device="cuda")
     # each written slot's (page or sequence, offset), for the plain form
@@ -406,8 +406,8 @@ def _plain_attn(st):
     o = out.view(S, rows, nkv, nq // nkv, d)
     for s in range(S):
         n = st["lens"][s]
-        k = torch.cat([_context(st, "k", s, n), st["kb"][s].float()], 1)
-        v = torch.cat([_context(st, "v", s, n), st["vb"][s].float()], 1)
+        k = torch.cat([_context(st, "k", s, n), st["kb"][s].float().transpose(0, 1)], 1)
+        v = torch.cat([_context(st, "v", s, n), st["vb"][s].float().transpose(0, 1)], 1)
         see = _ancestors(st["parent"][s])
         sc = torch.matmul(q[s].permute(1, 2, 0, 3).reshape(nkv, -1, d), k.transpose(1, 2)) / math.sqrt(d)
         sc = sc.view(nkv, nq // nkv, rows, -1)
@@ -423,12 +423,12 @@ def _plain_attn(st):
 def _plain_kv(st):
     s, i, src, at, off = st["map"]
     for x in "kv":
-        codes, ex = _quantise(st[x + "b"][:, s, :, src])
-        st[x + "c"][:, at, :, off] = codes.view(torch.uint8)
-        st[x + "e"][:, at, :, off] = ex
+        codes, ex = _quantise(st[x + "b"][:, s, src])  # [layers][slots][nkv][d]
+        st[x + "c"][:, at, :, off] = codes.view(torch.uint8).transpose(0, 1)
+        st[x + "e"][:, at, :, off] = ex.transpose(0, 1)
     for x in "kv":
         codes, ex = st[x + "c"][:, at, :, off].view(torch.float8_e4m3fn), st[x + "e"][:, at, :, off]
-        st[x + "o"][:, s, :, i] = _values(codes, ex).to(st[x + "o"].dtype)
+        st[x + "o"][:, s, i] = _values(codes, ex).to(st[x + "o"].dtype).transpose(0, 1)
     return [st["ko"], st["vo"]]
 
 
@@ -515,7 +515,7 @@ def _exact_attn(st):
             if e is not None:
                 scales.append(torch.pow(2.0, e[at, :, :b - a].double() - EXP_BIAS))
         parts = [p * w[..., None] for p, w in zip(parts, scales)] if scales else parts
-        return torch.cat(parts + [st[x + "b"][s].double()], 1)
+        return torch.cat(parts + [st[x + "b"][s].double().transpose(0, 1)], 1)
 
     for s in range(S):
         n = st["lens"][s]
@@ -538,18 +538,19 @@ def _exact_attn(st):
 
 def _exact_kv(st):
     c = st["case"]
+    two_to = lambda e: ((e.long() + 1023) << 52).view(torch.float64)  # exact, so that ties stay ties
     res = []
     for x in "kv":
         src = st[x + "b"].double()
         out = torch.zeros_like(src)
         for s in range(c["S"]):
             for i in range(st["valid_l"][s]) if c["path"] else [slice(0, st["valid_l"][s])]:
-                y = src[:, s, :, st["index_l"][s][i] if c["path"] else i]
+                y = src[:, s, st["index_l"][s][i] if c["path"] else i]
                 # (1e-9: log2 may land just above the whole number that a power of two has)
                 e = torch.ceil(torch.log2(y.abs().amax(-1, keepdim=True) / E4M3_MAX) - 1e-9).clamp(-EXP_LIM, EXP_LIM)
-                y = y * torch.pow(2.0, -e)
-                ulp = torch.pow(2.0, torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
-                out[:, s, :, i] = torch.round(y / ulp) * ulp * torch.pow(2.0, e)
+                y = y * two_to(-e)
+                ulp = two_to(torch.frexp(y.abs().clamp(min=2.0 ** -6))[1] - 4)
+                out[:, s, i] = torch.round(y / ulp) * ulp * two_to(e)
         res.append(out)
     return res
 
