@@ -7,6 +7,8 @@
 
 #include <algorithm>
 
+#include "abi_common.h"
+#include "abi_tree.h"
 #include "common.cuh"
 #include "internal.h"
 #include "trace.h"
@@ -17,6 +19,10 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+}  // namespace
+
+namespace dfl {
+
 int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -25,74 +31,9 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-#define DF_CHECK(cond, ...)                                 \
-  do {                                                      \
-    if (!(cond)) return fail(DFLASH_ERR_INVALID_ARG, __VA_ARGS__); \
-  } while (0)
+}  // namespace dfl
 
-#define DF_CUDA(call)                                                                       \
-  do {                                                                                      \
-    cudaError_t e_ = (call);                                                                \
-    if (e_ != cudaSuccess) return fail(DFLASH_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
-
-// Launch with optional tracing (family, algorithmic bytes).
-#define DF_LAUNCH(st, fam, bytes, call)                                                     \
-  do {                                                                                      \
-    trace_pre((st), (fam));                                                                 \
-    cudaError_t e_ = (call);                                                                \
-    trace_post((st), (double)(bytes));                                                      \
-    if (e_ != cudaSuccess) return fail(DFLASH_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
-
-size_t elem_size(int dtype) { return dtype == DFLASH_BF16 ? 2 : 4; }
-
-// Carves a workspace into 256-byte aligned pieces; with base == nullptr it
-// only measures.
-struct Bump {
-  char* base;
-  size_t off = 0;
-  explicit Bump(void* b) : base(static_cast<char*>(b)) {}
-  void* take(size_t bytes) {
-    off = (off + 255) & ~size_t(255);
-    void* p = base ? base + off : nullptr;
-    off += bytes;
-    return p;
-  }
-};
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
-  return n;
-}
-
-int check_dims(const dflash_dims& d, const char* who) {
-  DF_CHECK(d.dtype == DFLASH_F32 || d.dtype == DFLASH_BF16, "%s: dtype %d not F32/BF16", who, d.dtype);
-  DF_CHECK(d.hidden > 0 && d.hidden % 8 == 0, "%s: hidden %d must be a positive multiple of 8", who, d.hidden);
-  DF_CHECK(d.head_dim == 64 || d.head_dim == 128, "%s: head_dim %d must be 64 or 128", who, d.head_dim);
-  DF_CHECK(d.n_q_heads > 0 && d.n_kv_heads > 0 && d.n_q_heads % d.n_kv_heads == 0,
-           "%s: n_q_heads %d must be a positive multiple of n_kv_heads %d", who, d.n_q_heads, d.n_kv_heads);
-  DF_CHECK(d.intermediate > 0 && d.intermediate % 8 == 0, "%s: intermediate %d must be a multiple of 8", who,
-           d.intermediate);
-  DF_CHECK((d.n_q_heads * d.head_dim) % 8 == 0, "%s: n_q_heads*head_dim must be a multiple of 8", who);
-  DF_CHECK(d.vocab > 0, "%s: vocab must be positive", who);
-  DF_CHECK(d.rms_eps >= 0.f && d.rope_theta > 0.f, "%s: rms_eps >= 0 and rope_theta > 0 required", who);
-  return DFLASH_OK;
-}
-
-struct Ctx {
-  uint32_t* status;
-  uint32_t* counters;
-};
-
-Ctx header(void* ws) {
-  Ctx c;
-  c.status = static_cast<uint32_t*>(ws);
-  c.counters = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kHeaderBytes);
-  return c;
-}
+namespace {
 
 // ------------------------------------------------------------------ GEMMs
 
@@ -161,6 +102,9 @@ struct LayerConv {
 struct LayerShape {
   dflash_dims d;
   int S, rows, mode, max_pos, cap, window;
+  dflash_kv kv;                // DFLASH_ATTN_TREE: the cache
+  const int32_t* tree_parent;  // DFLASH_ATTN_TREE (see dflash_layer_args)
+  const int32_t* tree_pos;
 };
 
 void layer_gemms(const LayerShape& L, const dflash_layer_weights* w, GemmDesc* g4) {
@@ -192,6 +136,11 @@ void layer_gemms(const LayerShape& L, const dflash_layer_weights* w, GemmDesc* g
   g4[1] = o;
   g4[2] = gu;
   g4[3] = dn;
+  // A tree's rows carry their own positions: every row is a sequence of one
+  // row to the projections (base_pos is then the row's position), and its
+  // keys and values land token-major.
+  if (L.mode == DFLASH_ATTN_TREE)
+    for (int j = 0; j < 4; ++j) g4[j].rows = 1;
 }
 
 AttnDesc attn_shape(const LayerShape& L) {
@@ -222,7 +171,10 @@ void carve_layer(Bump& b, const LayerShape& L, int sms, LayerScratch& s, int con
   s.vb = b.take((size_t)L.S * d.n_kv_heads * L.rows * d.head_dim * es);
   s.attn = b.take(M * QD * es);
   s.act = b.take(M * d.intermediate * es);
-  s.apart = static_cast<float*>(b.take(attn_workspace(attn_shape(L))));
+  s.apart = static_cast<float*>(b.take(
+      L.mode == DFLASH_ATTN_TREE
+          ? tree_attn_workspace(tree_attn_desc(d, L.S, L.rows, L.max_pos - L.rows, L.kv, 0.f), sms)
+          : attn_workspace(attn_shape(L))));
   GemmDesc g4[4];
   layer_gemms(L, nullptr, g4);
   size_t gp = 0;
@@ -267,9 +219,13 @@ static double conv_bytes(const LayerShape& L, const LayerConv& cv) {
 
 int check_layer_shape(const LayerShape& L, const char* who) {
   DF_CHECK(L.S > 0 && L.rows > 0, "%s: n_seqs and rows must be positive", who);
-  DF_CHECK(L.mode == DFLASH_ATTN_CAUSAL || L.mode == DFLASH_ATTN_BLOCK_BIDIR, "%s: bad attn_mode", who);
+  DF_CHECK(L.mode == DFLASH_ATTN_CAUSAL || L.mode == DFLASH_ATTN_BLOCK_BIDIR || L.mode == DFLASH_ATTN_TREE,
+           "%s: bad attn_mode", who);
   DF_CHECK(L.cap > 0, "%s: kv capacity must be positive", who);
   DF_CHECK(L.max_pos >= L.rows, "%s: max_pos must cover base_pos + rows", who);
+  if (L.mode == DFLASH_ATTN_TREE) return check_tree_shape(L.d, L.S, L.rows, L.max_pos - L.rows, L.kv, who);
+  if (L.kv.k_exp || L.kv.v_exp)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: an 8-bit cache is read in DFLASH_ATTN_TREE mode only", who);
   if (L.mode == DFLASH_ATTN_CAUSAL) {
     DF_CHECK(L.window == 0, "%s: causal layers take no window", who);
     DF_CHECK(L.max_pos <= L.cap, "%s: max_pos %d exceeds cache capacity %d", who, L.max_pos, L.cap);
@@ -319,7 +275,7 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   GemmDesc g4[4];
   layer_gemms(L, &w, g4);
   for (auto& g : g4) g.base_pos = base_pos;
-  const bool causal = L.mode == DFLASH_ATTN_CAUSAL;
+  const bool causal = L.mode == DFLASH_ATTN_CAUSAL, tree = L.mode == DFLASH_ATTN_TREE;
 
   DF_LAUNCH(st, TF_RMSNORM, 0, launch_rmsnorm(d.dtype, h, w.ln1, M, H, d.rms_eps, s.x, st));
   if (cv) DF_LAUNCH(st, TF_CONV, conv_bytes(L, *cv), layer_conv(L, *cv, 0, s.x, s.xc, 0, s, st));
@@ -332,7 +288,8 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   const bool direct = causal && kv.pages == nullptr;
   qkv.k_dst[0] = direct ? kv.k : s.kb;
   qkv.v_dst[0] = direct ? kv.v : s.vb;
-  qkv.kv_cap = direct ? kv.capacity : L.rows;
+  qkv.kv_cap = direct ? kv.capacity : qkv.rows;
+  if (tree) qkv.base_pos = L.tree_pos;
   qkv.kv_window = 0;
   qkv.kv_slot_mode = direct ? 1 : 0;
   qkv.rope_cs = rope_cs;
@@ -348,6 +305,18 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
     DF_LAUNCH(st, TF_PAGE, 0, launch_kv_page_scatter(ks, st));
   }
 
+  if (tree) {
+    TreeAttnDesc t = tree_attn_desc(d, L.S, L.rows, L.max_pos - L.rows, kv, 0.f);
+    t.base_pos = base_pos;
+    t.parent = L.tree_parent;
+    t.q = s.q;
+    t.kb = s.kb;
+    t.vb = s.vb;
+    t.out = s.attn;
+    t.work = s.apart;
+    t.status = c.status;
+    DF_LAUNCH(st, TF_ATTN, 0, launch_tree_attention(t, sms, st));
+  } else {
   AttnDesc a = attn_shape(L);
   a.base_pos = base_pos;
   a.q = s.q;
@@ -364,6 +333,7 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   a.counters = c.counters;
   a.status = c.status;
   DF_LAUNCH(st, TF_ATTN, 0, launch_attention(a, st));
+  }
 
   // With convolutions the O and down projections store their output, which
   // the convolution then adds to the residual.
@@ -389,26 +359,6 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   if (cv) DF_LAUNCH(st, TF_CONV, conv_bytes(L, *cv), layer_conv(L, *cv, 3, s.yc, h, 1, s, st));
 
   if (tap) DF_LAUNCH(st, TF_TAP, 0, launch_store_tap(d.dtype, h, M, H, tap, tap_stride, tap_offset, st));
-  return DFLASH_OK;
-}
-
-int check_ws(void* ws, size_t ws_bytes, size_t need, const char* who) {
-  if (!ws) return fail(DFLASH_ERR_INVALID_ARG, "%s: workspace is NULL", who);
-  if (ws_bytes < need)
-    return fail(DFLASH_ERR_WORKSPACE, "%s: workspace %zu bytes, %zu required", who, ws_bytes, need);
-  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0)
-    return fail(DFLASH_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
-  return DFLASH_OK;
-}
-
-// A paged cache: page size a multiple of the 128-key attention chunk,
-// capacity == max_pages * page_size.
-int check_kv_pages(const dflash_kv& kv, const char* who) {
-  if (!kv.pages) return DFLASH_OK;
-  DF_CHECK(kv.page_size > 0 && kv.page_size % 128 == 0, "%s: page_size must be a positive multiple of 128", who);
-  DF_CHECK(kv.max_pages > 0 && kv.pool_pages > 0, "%s: max_pages and pool_pages must be positive", who);
-  DF_CHECK((long)kv.max_pages * kv.page_size == kv.capacity, "%s: capacity must equal max_pages * page_size", who);
-  DF_CHECK((long)kv.pool_pages * kv.page_size <= (1L << 30), "%s: page pool too large", who);
   return DFLASH_OK;
 }
 
@@ -461,6 +411,9 @@ LayerShape draft_layer_shape(const dflash_draft_args* a, int j) {
   L.max_pos = a->max_pos;
   L.cap = a->kv_layers[j].capacity;
   L.window = a->kv_layers[j].window;
+  L.kv = a->kv_layers[j];
+  L.tree_parent = nullptr;
+  L.tree_pos = nullptr;
   return L;
 }
 
@@ -554,7 +507,7 @@ static int check_verify_shape(const dflash_verify_args* a, const char* who) {
 
 
 namespace dfl {
-// Sets the thread-local error text from another translation unit.
+// Sets the thread-local error text from a fixed message.
 int abi_fail(int code, const char* msg) { return fail(code, "%s", msg); }
 
 // Every host-side check of dflash_verify_accept (shapes, then pointers).
@@ -667,6 +620,9 @@ static LayerShape layer_shape_of(const dflash_layer_args* a) {
   L.max_pos = a->max_pos;
   L.cap = a->kv.capacity;
   L.window = a->kv.window;
+  L.kv = a->kv;
+  L.tree_parent = a->tree_parent;
+  L.tree_pos = a->tree_pos;
   return L;
 }
 
@@ -696,6 +652,12 @@ int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws
   if (rc) return rc;
   DF_CHECK(a->base_pos && a->h && a->kv.k && a->kv.v && a->rope_cs, "%s: NULL pointer", who);
   LayerShape L = layer_shape_of(a);
+  const bool tree = L.mode == DFLASH_ATTN_TREE;
+  if (tree) {
+    DF_CHECK(a->tree_pos, "%s: DFLASH_ATTN_TREE needs tree_pos", who);
+    rc = check_tree_kv(a->kv, who);
+    if (rc) return rc;
+  }
   DF_CHECK(a->max_pos <= a->rope_max_pos, "%s: max_pos %d beyond the RoPE table (%d)", who, a->max_pos,
            a->rope_max_pos);
   {
@@ -717,8 +679,8 @@ int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws
   if (a->out_x_attn) s.x = a->out_x_attn;
   if (a->out_x_mlp) s.x2 = a->out_x_mlp;
   if (a->out_q) s.q = a->out_q;
-  if (a->out_kb && L.mode == DFLASH_ATTN_BLOCK_BIDIR) s.kb = a->out_kb;
-  if (a->out_vb && L.mode == DFLASH_ATTN_BLOCK_BIDIR) s.vb = a->out_vb;
+  if (a->out_kb && L.mode != DFLASH_ATTN_CAUSAL) s.kb = a->out_kb;
+  if (a->out_vb && L.mode != DFLASH_ATTN_CAUSAL) s.vb = a->out_vb;
   if (a->out_attn) s.attn = a->out_attn;
   if (a->out_act) s.act = a->out_act;
   return run_layer(L, a->w, a->kv, a->h, a->base_pos, a->rope_cs, a->rope_max_pos, a->tap, a->tap_stride, a->tap_offset, s,
@@ -772,6 +734,8 @@ static int check_fuse_shape(const dflash_fuse_args* a, const char* who) {
   for (int j = 0; j < a->n_layers; ++j) {
     const int rc2 = check_kv_pages(a->kv_layers[j], who);
     if (rc2) return rc2;
+    if (a->kv_layers[j].k_exp || a->kv_layers[j].v_exp)
+      return fail(DFLASH_ERR_UNSUPPORTED, "%s: the context cache cannot be an 8-bit one", who);
     DF_CHECK((a->kv_layers[j].pages == nullptr) == (a->kv_layers[0].pages == nullptr) &&
                  a->kv_layers[j].page_size == a->kv_layers[0].page_size &&
                  a->kv_layers[j].max_pages == a->kv_layers[0].max_pages &&
@@ -1249,6 +1213,12 @@ size_t dflash_workspace_bytes(int32_t op, const void* args) {
       void *xf, *hp;
       return verify_ws(a, sms, &xf, &hp, nullptr);
     }
+    case DFLASH_OP_TREE_ATTENTION:
+    case DFLASH_OP_TREE_ACCEPT:
+    case DFLASH_OP_KV_WRITE:
+    case DFLASH_OP_KV_READ:
+    case DFLASH_OP_TREE_BUILD:
+      return tree_op_workspace(op, args, who);
     default:
       fail(DFLASH_ERR_INVALID_ARG, "dflash_workspace_bytes: unknown op %d", op);
       return 0;

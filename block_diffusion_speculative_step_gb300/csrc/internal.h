@@ -154,6 +154,91 @@ struct PathDesc {
   int32_t* cand_out;          // optional out [S][block-1][topk]: the candidate lists walked
 };
 
+// Attention of a tree's rows over the context and their ancestors
+// (k_tree_attn.cu; see dflash_tree_attention).
+struct TreeAttnDesc {
+  int dtype;
+  int n_seqs, rows, nq, nkv, d;
+  const int32_t* base_pos;
+  const int32_t* parent;      // [S][rows] or null (chain)
+  const void* q;              // [M][nq*d]
+  const void* kb;             // [M][nkv][d]
+  const void* vb;
+  const void* kc;             // cache [S][nkv][cap][d] or page pool [pool][nkv][ps][d]
+  const void* vc;
+  const uint8_t* k_exp;       // scale exponents of an 8-bit cache, or null
+  const uint8_t* v_exp;
+  int cap;
+  const int32_t* pages;
+  int ps, max_pages, pool;
+  int max_pos;                // bound on base_pos
+  float scale;                // times log2 e: scores in log2 units
+  void* out;                  // [M][nq*d]
+  void* work;                 // partials
+  uint32_t* status;
+};
+size_t tree_attn_workspace(const TreeAttnDesc& a, int num_sms);
+cudaError_t launch_tree_attention(const TreeAttnDesc& a, int num_sms, cudaStream_t st);
+
+// Cache rows written and read back (k_kv_cache.cu).
+constexpr int kKvMaxLayers = 64;
+struct KvRowsLayers {
+  const void* src_k[kKvMaxLayers];  // write: source rows; read: cache
+  const void* src_v[kKvMaxLayers];
+  void* dst_k[kKvMaxLayers];        // write: cache; read: output rows
+  void* dst_v[kKvMaxLayers];
+  uint8_t* k_exp[kKvMaxLayers];     // null: the cache holds the dtype
+  uint8_t* v_exp[kKvMaxLayers];
+  const int32_t* pages[kKvMaxLayers];
+};
+struct KvRowsDesc {
+  int dtype, n_layers, S, rows, nkv, d;
+  const int32_t* base_pos;
+  const int32_t* valid;
+  const int32_t* row_index;
+  int cap, window, ps, max_pages, pool;
+  uint32_t* status;
+};
+cudaError_t launch_kv_write(const KvRowsDesc& k, const KvRowsLayers& l, cudaStream_t st);
+cudaError_t launch_kv_read(const KvRowsDesc& k, const KvRowsLayers& l, cudaStream_t st);
+
+// Acceptance over a tree (k_tree_accept.cu; see dflash_tree_accept).
+struct TreeAcceptDesc {
+  int n_seqs, rows, levels, V;
+  float invT;                 // 0: greedy
+  const int32_t* parent;
+  const int32_t* tokens;
+  const float* target;
+  const int32_t* argmax;
+  const float* draft;
+  const float* u;
+  const float* noise;
+  int32_t* base_pos;
+  int update_base;
+  int32_t* accept_len;
+  int32_t* path;
+  int32_t* out_tokens;
+  int32_t* next_anchor;
+  int32_t* commit_base;
+  int32_t* commit_count;
+  uint32_t* status;
+};
+cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_t st);
+
+struct TreeBuildDesc {
+  int n_seqs, rows, levels, topk;
+  const int32_t* parent;
+  const int32_t* rank;
+  const int32_t* cand;
+  const int32_t* anchor;
+  const int32_t* base_pos;
+  int32_t* parent_out;
+  int32_t* tokens_out;
+  int32_t* pos_out;
+  uint32_t* status;
+};
+cudaError_t launch_tree_build(const TreeBuildDesc& d, cudaStream_t st);
+
 // Sampling-mode verification (k_sample.cu).
 // Kept set of one logit row under top-k / top-p: the entries up to (key,
 // idx) in the order (logit descending, index ascending); see k_sample.cu.

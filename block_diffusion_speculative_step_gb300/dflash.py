@@ -22,9 +22,14 @@ DFLASH_F32 = 0
 DFLASH_BF16 = 1
 DFLASH_ATTN_CAUSAL = 0
 DFLASH_ATTN_BLOCK_BIDIR = 1
+DFLASH_ATTN_TREE = 2
 (DFLASH_OP_EMBED, DFLASH_OP_LAYER, DFLASH_OP_FUSE, DFLASH_OP_DRAFT, DFLASH_OP_VERIFY, DFLASH_OP_PATH,
- DFLASH_OP_SAMPLE_DRAFTS, DFLASH_OP_SAMPLE_ACCEPT) = range(8)
+ DFLASH_OP_SAMPLE_DRAFTS, DFLASH_OP_SAMPLE_ACCEPT, DFLASH_OP_TREE_ATTENTION, DFLASH_OP_TREE_ACCEPT,
+ DFLASH_OP_KV_WRITE, DFLASH_OP_KV_READ, DFLASH_OP_TREE_BUILD) = range(13)
 DFLASH_MAX_LAYERS = 16
+DFLASH_KV_MAX_LAYERS = 64
+DFLASH_MAX_TREE = 128
+DFLASH_TREE_PAD = -2
 
 # Every symbol the header exports (checked by the CPU test suite).
 EXPORTS = ("dflash_rope_table", "dflash_embed", "dflash_decoder_layer_forward", "dflash_fuse_context",
@@ -32,7 +37,8 @@ EXPORTS = ("dflash_rope_table", "dflash_embed", "dflash_decoder_layer_forward", 
            "dflash_workspace_init", "dflash_read_status", "dflash_last_error", "dflash_abi_version",
            "dflash_trace_begin", "dflash_trace_pause", "dflash_trace_read", "dflash_trace_end",
            "dflash_verify_accept_noalloc", "dflash_trace_launches", "dflash_sample_drafts",
-           "dflash_sample_accept", "dflash_workspace_control", "dflash_build_flags")
+           "dflash_sample_accept", "dflash_workspace_control", "dflash_build_flags", "dflash_tree_attention",
+           "dflash_tree_build", "dflash_tree_accept", "dflash_kv_write", "dflash_kv_read")
 DFLASH_TRACE_FAMILIES = 13
 
 
@@ -56,7 +62,7 @@ class dflash_dims(C.Structure):
 
 class dflash_kv(C.Structure):
     _fields_ = [("k", vp), ("v", vp), ("capacity", i32), ("window", i32), ("pages", vp), ("page_size", i32),
-                ("max_pages", i32), ("pool_pages", i32)]
+                ("max_pages", i32), ("pool_pages", i32), ("k_exp", vp), ("v_exp", vp)]
 
 
 class dflash_layer_weights(C.Structure):
@@ -73,7 +79,7 @@ class dflash_layer_args(C.Structure):
                 ("base_pos", vp), ("h", vp), ("kv", dflash_kv), ("attn_mode", i32), ("max_pos", i32),
                 ("rope_cs", vp), ("rope_max_pos", i32), ("tap", vp), ("tap_stride", i32),
                 ("tap_offset", i32), ("out_x_attn", vp), ("out_q", vp), ("out_kb", vp), ("out_vb", vp),
-                ("out_attn", vp), ("out_x_mlp", vp), ("out_act", vp)]
+                ("out_attn", vp), ("out_x_mlp", vp), ("out_act", vp), ("tree_parent", vp), ("tree_pos", vp)]
 
 
 class dflash_fuse_args(C.Structure):
@@ -123,6 +129,36 @@ class dflash_sample_accept_args(C.Structure):
                 ("draft_cand", vp), ("draft_logq", vp)]
 
 
+class dflash_tree_attention_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_seqs", i32), ("rows", i32), ("base_pos", vp), ("parent", vp), ("q", vp),
+                ("kb", vp), ("vb", vp), ("kv", dflash_kv), ("max_pos", i32), ("scale", f32), ("out", vp)]
+
+
+class dflash_tree_build_args(C.Structure):
+    _fields_ = [("n_seqs", i32), ("rows", i32), ("levels", i32), ("topk", i32), ("parent", vp), ("rank", vp),
+                ("cand", vp), ("anchor", vp), ("base_pos", vp), ("parent_out", vp), ("tokens_out", vp),
+                ("pos_out", vp)]
+
+
+class dflash_tree_accept_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_seqs", i32), ("rows", i32), ("levels", i32), ("temperature", f32),
+                ("parent", vp), ("tokens", vp), ("target_logits", vp), ("target_argmax", vp), ("draft_logits", vp),
+                ("u", vp), ("noise", vp), ("base_pos", vp), ("update_base_pos", i32), ("accept_len", vp),
+                ("path", vp), ("out_tokens", vp), ("next_anchor", vp), ("commit_base", vp), ("commit_count", vp)]
+
+
+# kb, vb, k_out, v_out and kv_layers are addresses of HOST arrays with one
+# entry per layer (C.addressof of a ctypes array the caller keeps alive).
+class dflash_kv_write_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_layers", i32), ("kb", vp), ("vb", vp), ("kv_layers", vp), ("n_seqs", i32),
+                ("rows", i32), ("base_pos", vp), ("valid", vp), ("row_index", vp)]
+
+
+class dflash_kv_read_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_layers", i32), ("k_out", vp), ("v_out", vp), ("kv_layers", vp),
+                ("n_seqs", i32), ("rows", i32), ("base_pos", vp), ("valid", vp)]
+
+
 class dflash_trace_stat(C.Structure):
     _fields_ = [("name", C.c_char * 24), ("launches", i32), ("total_ms", C.c_double), ("bytes", C.c_double)]
 
@@ -140,7 +176,9 @@ def lib(path: str | None = None):
             raise RuntimeError(f"{path} is missing: build the CUDA library first (__graft_entry__.build())")
         L = C.CDLL(path)
         for name in ("dflash_embed", "dflash_decoder_layer_forward", "dflash_fuse_context", "dflash_draft_block",
-                     "dflash_verify_accept", "dflash_path_select", "dflash_sample_drafts", "dflash_sample_accept"):
+                     "dflash_verify_accept", "dflash_path_select", "dflash_sample_drafts", "dflash_sample_accept",
+                     "dflash_tree_attention", "dflash_tree_build", "dflash_tree_accept", "dflash_kv_write",
+                     "dflash_kv_read"):
             getattr(L, name).argtypes = [vp, vp, C.c_size_t, vp]
             getattr(L, name).restype = C.c_int
         L.dflash_rope_table.argtypes = [f32, i32, i32, vp, vp]
@@ -258,6 +296,26 @@ def dflash_sample_drafts(args: dflash_sample_drafts_args, ws_ptr: int, ws_bytes:
 
 def dflash_sample_accept(args: dflash_sample_accept_args, ws_ptr: int, ws_bytes: int, stream=None):
     _call("dflash_sample_accept", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_tree_attention(args: dflash_tree_attention_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_tree_attention", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_tree_build(args: dflash_tree_build_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_tree_build", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_tree_accept(args: dflash_tree_accept_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_tree_accept", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_kv_write(args: dflash_kv_write_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_kv_write", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_kv_read(args: dflash_kv_read_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_kv_read", args, ws_ptr, ws_bytes, stream)
 
 
 def dflash_trace_begin(max_launches: int = 4096):

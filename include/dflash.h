@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define DFLASH_ABI_VERSION 8
+#define DFLASH_ABI_VERSION 9
 #define DFLASH_MAX_LAYERS 16 /* draft layers handled by one fuse / draft call */
 
 typedef struct CUstream_st* dflash_stream_t; /* == cudaStream_t */
@@ -72,7 +72,8 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 } dflash_dtype;
 
 typedef enum {
   DFLASH_ATTN_CAUSAL = 0,     /* target verification: row i sees cache slots 0..pos_i */
-  DFLASH_ATTN_BLOCK_BIDIR = 1 /* draft block: every row sees the context and the whole block */
+  DFLASH_ATTN_BLOCK_BIDIR = 1, /* draft block: every row sees the context and the whole block */
+  DFLASH_ATTN_TREE = 2        /* target verification of a tree: a row sees the context, its ancestors and itself */
 } dflash_attn_mode;
 
 typedef enum {
@@ -83,7 +84,12 @@ typedef enum {
   DFLASH_OP_VERIFY = 4,
   DFLASH_OP_PATH = 5,
   DFLASH_OP_SAMPLE_DRAFTS = 6,
-  DFLASH_OP_SAMPLE_ACCEPT = 7
+  DFLASH_OP_SAMPLE_ACCEPT = 7,
+  DFLASH_OP_TREE_ATTENTION = 8,
+  DFLASH_OP_TREE_ACCEPT = 9,
+  DFLASH_OP_KV_WRITE = 10,
+  DFLASH_OP_KV_READ = 11,
+  DFLASH_OP_TREE_BUILD = 12
 } dflash_op;
 
 /* Shapes and arithmetic of one decoder stack. */
@@ -114,6 +120,14 @@ typedef struct {
  * With a window the ring slots (position % window) are paged the same way.
  * The arithmetic does not depend on the layout: a paged call returns what
  * the contiguous call returns, bit for bit.
+ *
+ * 8-bit (k_exp and v_exp not NULL): k and v hold e4m3 codes, one byte per
+ * element, and k_exp / v_exp one byte per (slot, KV head) -- [n_seqs][n_kv]
+ * [capacity], or [pool_pages][n_kv][page_size] when paged -- the biased
+ * exponent of that row's scale: an element stands for code * 2^(exp - 127).
+ * dflash_kv_write fills such a cache; dflash_kv_read, dflash_tree_attention
+ * and the layer in DFLASH_ATTN_TREE mode read it; every other call refuses
+ * it with DFLASH_ERR_UNSUPPORTED.  Both pointers are set or both NULL.
  */
 typedef struct {
   void* k;
@@ -126,6 +140,8 @@ typedef struct {
   int32_t page_size;
   int32_t max_pages;
   int32_t pool_pages;
+  uint8_t* k_exp;        /* NULL, or the scale exponents of an 8-bit cache */
+  uint8_t* v_exp;
 } dflash_kv;
 
 typedef struct {
@@ -177,6 +193,13 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *   injected context of positions < base_pos[s] (the last kv.window of them
  *   with a window); every row attends all of those plus every row of its own
  *   block, no mask.  The block's K/V are not stored in kv.
+ * DFLASH_ATTN_TREE: the rows are the nodes of a drafted tree (tree_parent,
+ *   see dflash_tree_attention) at the positions tree_pos[M] (base_pos[s] +
+ *   the node's depth; dflash_tree_build writes both).  A row attends the
+ *   cache slots below base_pos[s], its ancestors and itself; kv (also 8-bit)
+ *   is not written: the rows' rotated keys and values go to out_kb / out_vb,
+ *   here [M][n_kv][d], from which dflash_kv_write commits the accepted path.
+ *   kv.window must be 0; rows <= DFLASH_MAX_TREE; max_pos - rows <= capacity.
  * tap (optional): writes the layer's output residual, rounded to dims.dtype,
  *   to tap[row * tap_stride + tap_offset + j] (feature taps for fusion).
  * max_pos: host-side bound with base_pos[s] + rows <= max_pos for every s
@@ -189,8 +212,8 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *     x_attn [M][H]        RMSNorm(h; ln1), the QKV projection's input
  *     q      [M][n_q*d]    rotated queries
  *     kb, vb [n_seqs][n_kv][rows][d]  the block's rotated keys and values
- *                          (DFLASH_ATTN_BLOCK_BIDIR only; causal layers
- *                          write them into kv)
+ *                          (DFLASH_ATTN_BLOCK_BIDIR; [M][n_kv][d] with
+ *                          DFLASH_ATTN_TREE; causal layers write them into kv)
  *     attn   [M][n_q*d]    attention output, the O projection's input
  *     x_mlp  [M][H]        RMSNorm(h; ln2) after the attention residual
  *     act    [M][I]        SiLU(gate) * up, the down projection's input
@@ -215,6 +238,8 @@ typedef struct {
   void* out_attn;
   void* out_x_mlp;
   void* out_act;
+  const int32_t* tree_parent; /* DFLASH_ATTN_TREE: [n_seqs][rows], or NULL for a chain */
+  const int32_t* tree_pos;    /* DFLASH_ATTN_TREE: [M] absolute positions of the rows */
 } dflash_layer_args;
 int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws_bytes,
                                  dflash_stream_t stream);
@@ -464,6 +489,162 @@ typedef struct {
 } dflash_sample_accept_args;
 int dflash_sample_accept(const dflash_sample_accept_args* a, void* ws, size_t ws_bytes,
                          dflash_stream_t stream);
+
+/*
+ * Verification of a drafted TREE (DFLASH_ATTN_TREE): instead of one chain of
+ * drafts, the target verifies up to DFLASH_MAX_TREE nodes of a tree of
+ * candidates in one forward.  Row i of a sequence is node i; its parent is a
+ * row before it:
+ *   parent[s][i] in [0, i): that node;  -1: a root (row 0 holds the anchor);
+ *   DFLASH_TREE_PAD: the row holds no node (rows behind a tree's last node).
+ * parent == NULL is the chain parent[i] = i - 1.  A row whose chain of
+ * parents meets a padding row is padding itself; any other value raises
+ * DFLASH_ERR_INVALID_ARG in the status word and makes the row padding.
+ * Padding rows' outputs are left as they were.
+ *
+ * dflash_tree_attention: per query head, for every node row
+ *   out = softmax_j(scale * q . k_j) v_j  over the cache slots j < base_pos[s]
+ *   (<= max_pos) and the tree rows j that are the node's ancestors or itself.
+ * The softmax runs in fp32.  With bf16 the probabilities enter their product
+ * with the values rounded to bf16 (fp16 for an 8-bit cache).  A call's result
+ * is deterministic; in bf16 the context is cut into pieces that depend on all
+ * the lengths of the launch, so a sequence's last bits may differ with the
+ * batch it runs in (fp32: they do not).
+ */
+#define DFLASH_MAX_TREE 128
+#define DFLASH_TREE_PAD (-2)
+typedef struct {
+  dflash_dims dims;
+  int32_t n_seqs, rows;
+  const int32_t* base_pos; /* [n_seqs] cached positions of each sequence (may be 0) */
+  const int32_t* parent;   /* [n_seqs][rows] or NULL */
+  const void* q;           /* [M][n_q*d] rotated queries */
+  const void* kb;          /* [M][n_kv][d] rotated keys of the tree rows */
+  const void* vb;          /* [M][n_kv][d] */
+  dflash_kv kv;            /* the context; contiguous or paged, dims.dtype or 8-bit; window 0 */
+  int32_t max_pos;         /* host-side bound: base_pos[s] <= max_pos <= capacity */
+  float scale;             /* 0: 1 / sqrt(head_dim) */
+  void* out;               /* [M][n_q*d] */
+} dflash_tree_attention_args;
+int dflash_tree_attention(const dflash_tree_attention_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * The tree of one cycle from per-position candidates: node i of the template
+ * (parent[rows], shared by the sequences) at depth t >= 1 takes the token
+ * cand[s][t-1][rank[i]] (dflash_draft_block's path_cand_out lists them best
+ * first); a root takes anchor[s].  Writes each sequence's parent_out and
+ * tokens_out [n_seqs][rows] and pos_out [n_seqs*rows] = base_pos[s] + depth.
+ * A depth beyond `levels` or a rank outside [0, topk) raises
+ * DFLASH_ERR_INVALID_ARG in the status word and makes the row padding; a
+ * padding row gets the anchor's token and position base_pos[s].
+ */
+typedef struct {
+  int32_t n_seqs, rows, levels, topk;
+  const int32_t* parent;   /* [rows] */
+  const int32_t* rank;     /* [rows] */
+  const int32_t* cand;     /* [n_seqs][levels][topk] */
+  const int32_t* anchor;   /* [n_seqs] */
+  const int32_t* base_pos; /* [n_seqs] */
+  int32_t* parent_out;     /* [n_seqs][rows] */
+  int32_t* tokens_out;     /* [n_seqs][rows] */
+  int32_t* pos_out;        /* [n_seqs*rows] */
+} dflash_tree_build_args;
+int dflash_tree_build(const dflash_tree_build_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * Acceptance over a tree from given random numbers.  Starting at row 0 the
+ * walk looks at the current node's children in row order; with k tokens
+ * accepted so far, p = softmax(target_logits[node] / T) and q =
+ * softmax(draft_logits[s][k] / T):
+ *   child i (token x) is accepted iff u[s][i] * q(x) < p(x); the walk goes on
+ *   at i.  On rejection p becomes max(0, p - q) normalised (p itself when
+ *   nothing is left) and q loses x and is normalised again (siblings are
+ *   drawn without replacement), and the next child is tested.
+ *   draft_logits == NULL: the candidates are not draws; child x is accepted
+ *   iff u < p(x), and on rejection p loses x and is normalised again.
+ * When no child is accepted the last token is the argmax over v of
+ * p(v) / noise[s][v] (an exponential race: a draw from p when noise holds
+ * Exp(1) numbers; the lowest v on equal values), so the emitted tokens follow
+ * the target's distribution exactly.  Logits may be -inf (probability 0); a
+ * NaN or +inf in a visited row raises DFLASH_ERR_NUMERIC in the status word.
+ * temperature == 0: the accepted child is the first whose token equals
+ * target_argmax[node] (dflash_verify_accept's argmax), the last token is the
+ * last node's argmax; logits, u and noise are not read.
+ * A token outside [0, V), or children below depth `levels`, raise
+ * DFLASH_ERR_INVALID_ARG in the status word and are not accepted.
+ * Outputs: accept_len[s] = accepted tokens k; path[s][0..k] = the accepted
+ * rows (path[s][0] = 0), then -1: the row_index of dflash_kv_write;
+ * out_tokens[s] = the accepted tokens, the last token, then -1; state updates
+ * as in dflash_sample_accept.
+ */
+typedef struct {
+  dflash_dims dims;            /* vocab is used */
+  int32_t n_seqs, rows;
+  int32_t levels;              /* rows of draft_logits per sequence (0 without them) */
+  float temperature;           /* >= 0 */
+  const int32_t* parent;       /* [n_seqs][rows] or NULL: a chain */
+  const int32_t* tokens;       /* [n_seqs][rows]; row 0's is not read */
+  const float* target_logits;  /* [n_seqs][rows][V] */
+  const int32_t* target_argmax;/* [n_seqs][rows] (temperature 0) */
+  const float* draft_logits;   /* [n_seqs][levels][V] or NULL */
+  const float* u;              /* [n_seqs][rows] in [0, 1) */
+  const float* noise;          /* [n_seqs][V] > 0 */
+  int32_t* base_pos;           /* in: P; out: P + accept_len + 1 when update_base_pos */
+  int32_t update_base_pos;
+  int32_t* accept_len;         /* out [n_seqs] */
+  int32_t* path;               /* out [n_seqs][rows] */
+  int32_t* out_tokens;         /* out [n_seqs][rows] */
+  int32_t* next_anchor;        /* optional out [n_seqs]: the last token */
+  int32_t* commit_base;        /* optional out [n_seqs]: P */
+  int32_t* commit_count;       /* optional out [n_seqs]: accept_len + 1 */
+} dflash_tree_accept_args;
+int dflash_tree_accept(const dflash_tree_accept_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * Cache rows written and read back, for n_layers layers in one launch.
+ * dflash_kv_write: for i < valid[s], source row (row_index ?
+ * row_index[s*rows + i] : i) of sequence s goes to the slot of position
+ * base_pos[s] + i (modulo the window of a ring).  An 8-bit cache receives it
+ * quantised: e = the smallest exponent in [-60, 60] with max |x| <= 448 * 2^e,
+ * code = x * 2^-e rounded to e4m3 (nearest, ties to even; beyond 448 to 448).
+ * A NaN or infinite element becomes the e4m3 NaN, is left out of the maximum
+ * and raises DFLASH_ERR_NUMERIC in the status word.  Other caches receive a
+ * copy.  Of more valid rows than a ring holds, the last ones are kept.
+ * dflash_kv_read: the slot of position base_pos[s] + i, i < valid[s], comes
+ * back in dims.dtype as row i of k_out / v_out (an 8-bit element as code *
+ * 2^(exp - 127)).
+ * Rows i >= valid[s] are neither written nor read back.  A slot beyond the
+ * cache, an unmapped page or a source row outside [0, rows) raises
+ * DFLASH_ERR_INVALID_ARG in the status word; that row is skipped.
+ * The layers share the cache geometry (and 8 bits or not); the arrays kb, vb,
+ * k_out, v_out and kv_layers are HOST arrays of n_layers entries, read
+ * during the call.
+ */
+#define DFLASH_KV_MAX_LAYERS 64
+typedef struct {
+  dflash_dims dims;
+  int32_t n_layers;           /* <= DFLASH_KV_MAX_LAYERS */
+  const void* const* kb;      /* host array of [n_seqs*rows][n_kv][d] device buffers */
+  const void* const* vb;
+  const dflash_kv* kv_layers; /* host array */
+  int32_t n_seqs, rows;
+  const int32_t* base_pos;    /* [n_seqs] */
+  const int32_t* valid;       /* [n_seqs] or NULL: all rows */
+  const int32_t* row_index;   /* [n_seqs][rows] or NULL */
+} dflash_kv_write_args;
+int dflash_kv_write(const dflash_kv_write_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+typedef struct {
+  dflash_dims dims;
+  int32_t n_layers;
+  void* const* k_out;         /* host array of [n_seqs*rows][n_kv][d] device buffers */
+  void* const* v_out;
+  const dflash_kv* kv_layers; /* host array */
+  int32_t n_seqs, rows;
+  const int32_t* base_pos;    /* [n_seqs] */
+  const int32_t* valid;       /* [n_seqs] or NULL: all rows */
+} dflash_kv_read_args;
+int dflash_kv_read(const dflash_kv_read_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
 /* Bytes of workspace `op` needs for these arguments (args points to the
  * op's argument struct); 0 on invalid arguments. */
