@@ -179,6 +179,8 @@ struct TreeAttnDesc {
 };
 size_t tree_attn_workspace(const TreeAttnDesc& a, int num_sms);
 cudaError_t launch_tree_attention(const TreeAttnDesc& a, int num_sms, cudaStream_t st);
+size_t tree_tc_workspace(const TreeAttnDesc& a, int num_sms);  // the tensor-core path (bf16, k_tree_attn_tc.cu)
+cudaError_t launch_tree_tc(const TreeAttnDesc& a, int num_sms, cudaStream_t st);
 
 // Cache rows written and read back (k_kv_cache.cu).
 constexpr int kKvMaxLayers = 64;

@@ -278,17 +278,18 @@ static cudaError_t ts_launch(const TreeAttnDesc& a, cudaStream_t st) {
   return launch_pdl(tree_simt_merge_kernel<T, D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a);
 }
 
-template <typename T>
 static cudaError_t ts_dispatch(const TreeAttnDesc& a, cudaStream_t st) {
   const bool q8 = a.k_exp != nullptr;
-  if (a.d == 128) return q8 ? ts_launch<T, true, 128>(a, st) : ts_launch<T, false, 128>(a, st);
-  return q8 ? ts_launch<T, true, 64>(a, st) : ts_launch<T, false, 64>(a, st);
+  if (a.d == 128) return q8 ? ts_launch<float, true, 128>(a, st) : ts_launch<float, false, 128>(a, st);
+  return q8 ? ts_launch<float, true, 64>(a, st) : ts_launch<float, false, 64>(a, st);
 }
 
-size_t tree_attn_workspace(const TreeAttnDesc& a, int num_sms) { return ts_workspace(a); }
+size_t tree_attn_workspace(const TreeAttnDesc& a, int num_sms) {
+  return a.dtype == DFLASH_BF16 ? tree_tc_workspace(a, num_sms) : ts_workspace(a);
+}
 
 cudaError_t launch_tree_attention(const TreeAttnDesc& a, int num_sms, cudaStream_t st) {
-  return a.dtype == DFLASH_BF16 ? ts_dispatch<__nv_bfloat16>(a, st) : ts_dispatch<float>(a, st);
+  return a.dtype == DFLASH_BF16 ? launch_tree_tc(a, num_sms, st) : ts_dispatch(a, st);
 }
 
 }  // namespace dfl
