@@ -28,6 +28,9 @@ int check_tree_shape(const dflash_dims& d, int S, int rows, int max_pos, const d
       kv.pages ? (long long)kv.pool_pages * kv.page_size * d.n_kv_heads : (long long)S * kv.capacity * d.n_kv_heads;
   DF_CHECK(vecs < (1ll << 31), "%s: the cache holds 2^31 or more rows", who);
   DF_CHECK((long long)S * rows * d.n_q_heads < (1ll << 31) / 128, "%s: too many query vectors", who);
+  DF_CHECK((long long)S * d.n_kv_heads * ((rows * (d.n_q_heads / d.n_kv_heads) + 127) / 128) * (max_pos / 128 + 4) <
+               (1ll << 27),
+           "%s: too many (sequence, KV head, 128-slot chunk) pieces", who);
   DF_CHECK(S <= 65535 && d.n_q_heads <= 4096, "%s: n_seqs must be at most 65535, n_q_heads at most 4096", who);
   return DFLASH_OK;
 }

@@ -16,11 +16,20 @@
 // both hold the same tile and take chunks alternately, and are joined when
 // the segment ends.  Per chunk and stream (128 query vectors x 128 keys):
 //   S = Q K^T        tcgen05.mma, both operands in shared memory
-//   P = 2^(c S - m)  one thread per query vector; written over S as 16-bit
+//   P = 2^(c S - m)  one thread per query vector, written over S as 16-bit
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
-// While one stream's softmax runs, the other stream's products do.  The
-// reference maximum m moves only when a chunk exceeds it by more than 8 (a
-// factor 256 in P), so O is rarely rescaled.
+// With NT = 2 the streams' softmaxes take turns, so that one stream's products
+// run beside the other's softmax (left alone both fall in step and wait for
+// their products together).  The reference m stays while the weights' sum
+// suits the 16-bit type, so the usual chunk needs no maximum and no rescaling
+// of O: bf16, which has fp32's exponents, starts at m = 0 and takes sums of
+// 2^-60 .. 2^60; fp16 (8-bit cache) starts at the first chunk's maximum and
+// takes sums up to 2^15.  Otherwise the chunk is done again with its maximum:
+// the scores stay until the sum is known.
+//
+// Eight softmax warps with many registers (scores in flight while others are
+// exponentiated) measured faster than sixteen: two threads a row spend more
+// instructions on exchanging maxima and votes than they save.
 //
 // P is rounded to 16 bits for its product: bf16 next to a bf16 V (2^-8
 // relative per weight, as the output itself is rounded), fp16 with an 8-bit
@@ -57,26 +66,37 @@ constexpr int kTtRing = 8;      // chunks whose scale exponents and bad rows are
 struct TtTma {
   CUtensorMap kc, vc;  // cache rows [..][D]: bf16 boxes of 64 dims, or e4m3 boxes of D bytes, 128 rows
   CUtensorMap kb, vb;  // tree rows [M][nkv][D] (bf16 cache)
+  CUtensorMap q3;      // queries [M][nq][D], box 64 dims x group x 128 / group tokens (q_tma)
+  int q_tma;           // the group divides 128: a query tile is one box per 64 dims
   TreeAttnDesc a;
   int n_pt;            // query tile groups per KV head
+  uint32_t grp_mul;    // ceil(2^32 / group) for groups of 2 .. 256 query heads, else 0
 };
+
+// qv / grp.  For grp <= 256 and qv < 128 grp the product's error, qv (grp - 1)
+// 2^-32 at most, stays below 1 / grp.
+__device__ __forceinline__ int tt_div_grp(const TtTma& p, int qv, int grp) {
+  return p.grp_mul ? (int)__umulhi((uint32_t)qv, p.grp_mul) : qv / grp;
+}
 
 template <int D, int NT, bool Q8>
 struct TtCfg {
   static constexpr int TILE = kTtCH * D * 2;                   // one 16-bit K or V tile
   static constexpr int RAW = kTtCH * D;                        // one e4m3 tile
-  static constexpr int NSK = Q8 ? (NT == 2 ? 1 : 2) : (D == 64 ? 4 : (NT == 2 ? 2 : 3));
+  // (NT = 1: even, so that a slot always serves the same stream and its
+  // issuer sees every phase of the slot's barriers)
+  static constexpr int NSK = Q8 ? (NT == 2 ? 1 : 2) : (D == 64 ? 4 : 2);
   static constexpr int NSV = Q8 ? 2 : (D == 64 ? 4 : 2);
   static constexpr int NRK = Q8 ? 2 : 0;                       // raw K / V slots
   static constexpr int NRV = Q8 ? 1 : 0;
-  static constexpr int WARPS = Q8 ? 16 : 12;
+  static constexpr int WARPS = Q8 ? 16 : 12;                   // copies, 2 issuers, queries and clearing, 2 x 4 softmax (, 4 converters)
   static constexpr int THREADS = WARPS * 32;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = NT * TILE;
   static constexpr int V_OFF = K_OFF + NSK * TILE;
   static constexpr int R_OFF = V_OFF + NSV * TILE;             // raw K slots, raw V slots
   static constexpr int X_OFF = R_OFF + (NRK + NRV) * RAW;      // exchange, masks, barriers
-  static constexpr int X_BYTES = 6144;
+  static constexpr int X_BYTES = 16384;
   static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
@@ -84,17 +104,39 @@ struct TtCfg {
 struct TtShared {  // after the tiles
   float xm[2][128], xl[2][128], xu[2][128];  // a segment's stream statistics (NT = 1): maximum, sum, unit of O
   int par[DFLASH_MAX_TREE];
+  uint32_t mask[4][DFLASH_MAX_TREE][4];      // the tree rows' ancestors and themselves (none: padding)
   int ek[kTtRing], ev[kTtRing];   // chunk scale exponents (8-bit cache), by chunk counter
   uint32_t badv[kTtRing][4];      // tree rows whose V holds a NaN or infinity, by chunk counter
-  float cmax[2][2][4];            // converters: the warps' maxima of the tree rows (K, V)
-  int s0, it0, c0, len;           // the CTA's run: first item and chunk, number of chunks
+  float cmax[2][2][4];            // converters: the warps' maxima, by chunk & 1 (K, V)
+  __half2 fac[2][128];            // converters: the rows' factors
+  int s0, it0, c0, len, n0;       // the CTA's run: first item, position in it, number of positions; context of s0
+  int setup;
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t rkfull[2], rkempty[2], rvfull[2], rvempty[2];
-  uint64_t sfull[2], pdone[2], ofull[2], qfull, qempty;
+  uint64_t sfull[2], pdone[2], ofull[2], qraw[2], qfull[2], qfree[2];
+  uint64_t mready[4];             // ancestor masks written, by buffer
+  uint64_t vraw[4];               // V tiles with rows to clear, copied (at most NSV <= 4 are ahead of their P V)
   uint32_t tslot;
   int abort;
   int8_t qe[4][2][128];           // query vectors' scale exponents (8-bit cache), by segment
 };
+
+__device__ __forceinline__ void named_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// One lane of the warp (the same one each time).
+__device__ __forceinline__ bool tt_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]: A packed 16-bit, two per column, K along columns.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -113,19 +155,60 @@ __host__ __device__ constexpr uint32_t tt_idesc(int M, int N, bool b_mn) {
   return F16 ? base & ~((7u << 7) | (7u << 10)) : base;
 }
 
-// 32 packed columns of this thread's lane; returns once stored (one statement:
-// the source registers are read until the wait).
-__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
+// 32 columns of this thread's lane, not waited for: the registers hold them
+// after tmem_wait on the same array (which makes the compiler keep the order).
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-      "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+      "}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+
+// 16 packed columns of this thread's lane; returns once stored (one statement:
+// the source registers are read until the wait).
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
       "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// Packed fp32 pairs (two fused multiply-adds / additions per instruction).
+__device__ __forceinline__ unsigned long long tt_pair(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void tt_unpair(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long tt_fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long tt_add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ float tt_ex2(float x) {
@@ -154,85 +237,135 @@ __device__ __forceinline__ uint32_t tt_off(int row, int ch) {
 // A CTA's run walked segment by segment; every role keeps its own copy.
 struct Seg {
   const TreeAttnDesc* a;
-  int ips, left;       // items per sequence; chunks of the run not yet walked
+  bool uniform;        // a whole warp walks: loaded values through a reduction, which the compiler
+                       // knows to be the same in every lane
+  int ips, left;       // items per sequence; positions of the run not yet walked
+  int setup;           // positions an item has before its chunks
   int s, it;           // sequence, item of the sequence
   int n_ctx, nch;      // context slots, chunks of the item (the last one the tree)
+  int n_next;          // the next sequence's length, loaded ahead
   int c0, c1;          // the segment's chunks
+  __device__ __forceinline__ void ahead() { n_next = s + 1 < a->n_seqs ? __ldg(a->base_pos + s + 1) : 0; }
   __device__ __forceinline__ void load() {
-    n_ctx = min(max(__ldg(a->base_pos + s), 0), a->max_pos);
+    n_ctx = min(max(n_next, 0), a->max_pos);
+    if (uniform) n_ctx = __reduce_max_sync(0xffffffffu, n_ctx);
     nch = (n_ctx + kTtCH - 1) / kTtCH + 1;
+    ahead();
   }
-  __device__ __forceinline__ bool begin(const TreeAttnDesc* d, int ips_, const TtShared* sh) {
+  // The part of the current item from position v on, at most `left` positions.
+  __device__ __forceinline__ void take(int v) {
+    const int n = min(nch + setup - v, left);
+    c0 = max(0, v - setup);
+    c1 = max(0, v + n - setup);
+    left -= n;
+  }
+  __device__ __forceinline__ bool begin(const TreeAttnDesc* d, int ips_, const TtShared* sh, bool uni = false) {
     a = d;
     ips = ips_;
-    left = sh->len;
+    uniform = uni;
+    auto same = [&](int x) { return uniform ? __reduce_max_sync(0xffffffffu, x) : x; };
+    left = same(sh->len);
     if (left <= 0) return false;
-    s = sh->s0;
-    it = sh->it0;
-    load();
-    c0 = sh->c0;
-    c1 = min(nch, c0 + left);
-    return true;
+    s = same(sh->s0);
+    it = same(sh->it0);
+    setup = same(sh->setup);
+    n_ctx = same(sh->n0);
+    nch = (n_ctx + kTtCH - 1) / kTtCH + 1;
+    ahead();
+    take(same(sh->c0));
+    return c1 > c0 || next();
   }
   __device__ __forceinline__ bool next() {
-    left -= c1 - c0;
-    if (left <= 0) return false;
-    if (++it == ips) {
-      it = 0;
-      ++s;
-      load();
-    }
-    c0 = 0;
-    c1 = min(nch, left);
+    do {
+      if (left <= 0) return false;
+      if (++it == ips) {
+        it = 0;
+        ++s;
+        load();
+      }
+      take(0);
+    } while (c1 <= c0);
     return true;
   }
   __device__ __forceinline__ bool is_tree(int c) const { return c == nch - 1; }
   __device__ __forceinline__ int keys(int c) const { return is_tree(c) ? a->rows : min(kTtCH, n_ctx - c * kTtCH); }
 };
 
-// The run of CTA b among nb: chunks [b * per, (b + 1) * per) of all items'
-// chunks, per = ceil(total / nb).  One warp; sequences are scanned 32 at a time.
-__device__ __forceinline__ long long tt_total(const TreeAttnDesc& a, int ips) {
-  const int lane = threadIdx.x & 31;
-  long long t = 0;
-  for (int s = lane; s < a.n_seqs; s += 32) {
-    const int n = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
-    t += (long long)((n + kTtCH - 1) / kTtCH + 1) * ips;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
+// How the chunks of all items are cut into runs, one per CTA (the host checks
+// that their number fits 31 bits):
+//   flat     CTA b takes positions [b per, (b + 1) per) of all items in a row,
+//            per = ceil(total / nb): every CTA the same number.  An item has
+//            kTtSetup positions before its chunks', for what it costs besides
+//            them (queries, masks, first chunk, output: about 8k cycles);
+//   aligned  every item gets sp = nb / items CTAs of its own, each
+//            ceil(chunks / sp) chunks: no CTA has parts of two items, which
+//            costs a second query load, prologue and partial (about 6 us).
+// Aligned where its longest run is at most one chunk longer than the flat
+// one, i.e. for few sequences of similar lengths: 8 items of 33 chunks take
+// 2 chunks on 136 CTAs, flat 2 on 132 of which 7 straddle two items (batch 1,
+// 4k context: 12 us against 18).
+constexpr int kTtSetup = 2;
+struct Part {
+  int aligned, per, sp;  // flat: positions per CTA; aligned: CTAs per item
+  int total;             // positions
+};
+
+__device__ __forceinline__ int tt_chunks(const TreeAttnDesc& a, int s, int* n) {
+  *n = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
+  return (*n + kTtCH - 1) / kTtCH + 1;
 }
 
-// First chunk of sequence s in that order.
-__device__ __forceinline__ void tt_locate(const TreeAttnDesc& a, int ips, long long x, int* s_out, int* it_out,
-                                          int* c_out) {
+// One warp.
+__device__ __forceinline__ Part tt_part(const TreeAttnDesc& a, int ips, int nb) {
+  int t = 0, mx = 0, n;
+  for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
+    const int k = tt_chunks(a, s, &n);
+    t += k + kTtSetup;
+    mx = max(mx, k);
+  }
+  Part p;
+  p.total = __reduce_add_sync(0xffffffffu, t) * ips;
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  p.per = (p.total + nb - 1) / nb;
+  p.sp = nb / (a.n_seqs * ips);
+  p.aligned = p.sp > 0 && (mx + p.sp - 1) / p.sp <= p.per + 1;
+  return p;
+}
+
+// The sequence, item, position in the item, context length and number of
+// chunks at position x of the flat order.
+struct Spot {
+  int s, it, c, n, nch;
+};
+__device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
+  int before = 0;
+  Spot p = {a.n_seqs, 0, 0, 0, 1};
   for (int b = 0; b < a.n_seqs; b += 32) {
     const int s = b + lane;
-    const int n = s < a.n_seqs ? min(max(__ldg(a.base_pos + s), 0), a.max_pos) : 0;
-    const int nch = s < a.n_seqs ? (n + kTtCH - 1) / kTtCH + 1 : 0;
-    long long inc = (long long)nch * ips;
+    int n = 0;
+    const int nch = s < a.n_seqs ? tt_chunks(a, s, &n) : 0;
+    const int len = s < a.n_seqs ? nch + kTtSetup : 0;
+    int inc = len * ips;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, before + inc > x);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const long long start = before + __shfl_sync(0xffffffffu, inc, w) - (long long)__shfl_sync(0xffffffffu, nch, w) * ips;
-      const int k = __shfl_sync(0xffffffffu, nch, w);
-      *s_out = b + w;
-      *it_out = (int)((x - start) / k);
-      *c_out = (int)((x - start) % k);
-      return;
+      p.nch = __shfl_sync(0xffffffffu, nch, w);
+      const int k = p.nch + kTtSetup, at = x - (before + __shfl_sync(0xffffffffu, inc, w) - k * ips);
+      p.s = b + w;
+      p.it = at / k;
+      p.c = at % k;
+      p.n = __shfl_sync(0xffffffffu, n, w);
+      return p;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  *s_out = a.n_seqs;
-  *it_out = *c_out = 0;
+  return p;
 }
 
 // Scale 2^d as fp16 (d <= 0; 0 below the subnormals).
@@ -319,9 +452,9 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sh->kfull[i], Q8 ? 128 : 1);
-      tc::mbar_init(&sh->kempty[i], 1);
+      tc::mbar_init(&sh->kempty[i], NT);  // the issuers that read the slot
       tc::mbar_init(&sh->vfull[i], Q8 ? 128 : 1);
-      tc::mbar_init(&sh->vempty[i], 1);
+      tc::mbar_init(&sh->vempty[i], NT);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh->rkfull[i], 1);
@@ -334,9 +467,15 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       tc::mbar_init(&sh->pdone[i], 128);
       tc::mbar_init(&sh->ofull[i], 2);
     }
-    tc::mbar_init(&sh->qfull, 64);
-    tc::mbar_init(&sh->qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh->qraw[i], 1);
+      tc::mbar_init(&sh->qfull[i], Q8 || !p.q_tma ? 128 : 1);  // the rows' threads, or the copy
+      tc::mbar_init(&sh->qfree[i], NT == 1 ? 2 : 1);           // the issuers that read the tile
+    }
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh->vraw[i], 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh->mready[i], 32);
     sh->abort = 0;
+    for (int i = 0; i < kTtRing * 4; ++i) sh->badv[i >> 2][i & 3] = 0u;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&p.kc);
     tc::tma_prefetch_desc(&p.vc);
@@ -345,16 +484,31 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
-    const long long total = tt_total(a, ips);
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
-    const long long x0 = (long long)blockIdx.x * per;
-    int s0 = 0, it0 = 0, c0 = 0;
-    if (x0 < total) tt_locate(a, ips, x0, &s0, &it0, &c0);
+    const Part pt = tt_part(a, ips, gridDim.x);
+    Spot sp = {0, 0, 0, 0, 1};
+    int len = 0;
+    if (pt.aligned) {
+      const int item = (int)blockIdx.x / pt.sp;
+      if (item < a.n_seqs * ips) {
+        sp.s = item / ips;
+        sp.it = item % ips;
+        sp.nch = tt_chunks(a, sp.s, &sp.n);
+        const int per = (sp.nch + pt.sp - 1) / pt.sp;
+        sp.c = (int)blockIdx.x % pt.sp * per;
+        len = min(per, sp.nch - sp.c);
+      }
+    } else {
+      const int x0 = min((int)blockIdx.x * pt.per, pt.total);  // (nb * per < total + nb: no overflow)
+      len = min(pt.per, pt.total - x0);
+      if (len > 0) sp = tt_locate(a, ips, x0);
+    }
     if (lane == 0) {
-      sh->s0 = s0;
-      sh->it0 = it0;
-      sh->c0 = c0;
-      sh->len = x0 < total ? (int)min(per, total - x0) : 0;
+      sh->s0 = sp.s;
+      sh->it0 = sp.it;
+      sh->c0 = sp.c;
+      sh->n0 = sp.n;
+      sh->len = len;
+      sh->setup = pt.aligned ? 0 : kTtSetup;
     }
   }
   tc::tc_fence_before();
@@ -384,7 +538,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   if (warp == 0) {
     // ---------------------------------------------------- K/V copies
     if (lane == 0 && !stall) {
-      int nk = 0, nv = 0;  // copies issued
+      int nk = 0, nv = 0, nraw = 0;  // copies issued; V tiles with rows to clear
+      uint32_t parts = 0u;           // which of the last V tiles those were
       constexpr int SK = Q8 ? Cfg::NRK : NSK, SV = Q8 ? Cfg::NRV : NSV;
       uint64_t* kf = Q8 ? sh->rkfull : sh->kfull;
       uint64_t* ke = Q8 ? sh->rkempty : sh->kempty;
@@ -421,12 +576,15 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             tc::mbar_arrive_expect_tx(&vf[nv % SV], RAW);
             tc::tma_load_2d(Rv + (nv % SV) * RAW, &p.vc, 0, row, &vf[nv % SV], pol);
           } else {
-            tc::mbar_arrive_expect_tx(&vf[nv % SV], TILE);
+            const bool part = tree || sg.keys(c) < kTtCH;  // warp 3 clears rows and passes the tile on
+            uint64_t* bar = part ? &sh->vraw[nraw++ & 3] : &vf[nv % SV];
+            parts = parts << 1 | (part ? 1u : 0u);
+            tc::mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               uint8_t* dst = Vs + (nv % SV) * TILE + h * (kTtCH * 128);
-              if (tree) tc::tma_load_3d(dst, &p.vb, 64 * h, g, sg.s * a.rows, &vf[nv % SV]);
-              else tc::tma_load_2d(dst, &p.vc, 64 * h, row, &vf[nv % SV], pol);
+              if (tree) tc::tma_load_3d(dst, &p.vb, 64 * h, g, sg.s * a.rows, bar);
+              else tc::tma_load_2d(dst, &p.vc, 64 * h, row, bar, pol);
             }
           }
           ++nv;
@@ -434,111 +592,210 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       }
       // every copy has landed before the CTA's shared memory goes away
       for (int i = max(0, nk - SK); i < nk; ++i) tc::mbar_wait(&kf[i % SK], (uint32_t)(i / SK) & 1u, nullptr, lim_ns);
-      for (int i = max(0, nv - SV); i < nv; ++i) tc::mbar_wait(&vf[i % SV], (uint32_t)(i / SV) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nv - SV); i < nv; ++i)
+        if (!(parts >> (nv - 1 - i) & 1u)) tc::mbar_wait(&vf[i % SV], (uint32_t)(i / SV) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nraw - SV); i < nraw; ++i) tc::mbar_wait(&sh->vraw[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, lim_ns);
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idS = tt_idesc<Q8>(kTtRows, kTtCH, false);
-      constexpr uint32_t idV = tt_idesc<Q8>(kTtRows, D, true);
-      const uint32_t qb = tc::smem_u32(Qs), kb = tc::smem_u32(Ks), vb = tc::smem_u32(Vs);
-      // Jobs in order: (chunk, stream); stream = job & 1.  S of job j + 2 is
-      // issued after P V of job j, whose P lies in the same columns.
-      Seg ss;               // the S side's segment
-      int sj = 0, sc = 0;   // next S job, its chunk counter
-      int c = 0, seg_no = 0;
-      bool s_on = ss.begin(&a, ips, sh);
-      if (s_on) c = ss.c0;
-      auto issue_s = [&]() {  // S of job sj
-        const int t = sj & 1, slot = sc % NSK;
-        if (c == ss.c0 && (NT == 1 || t == 0) && !wait(&sh->qfull, (uint32_t)seg_no)) return;
-        if ((NT == 1 || t == 0) && !wait(&sh->kfull[slot], (uint32_t)(sc / NSK))) return;
-        tc::tc_fence_after();
-        const uint32_t q = qb + (NT == 2 ? t * TILE : 0), k = kb + slot * TILE;
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------------------- MMA issue, stream t
+    // The whole warp walks the stream's jobs, so that descriptors and
+    // addresses stay in uniform registers; one lane issues.  A warp per
+    // stream: a job's waits and commits (about 700 cycles in one thread) then
+    // run beside the other stream's.
+    const int t = warp - 1;
+    constexpr uint32_t idS = tt_idesc<Q8>(kTtRows, kTtCH, false);
+    constexpr uint32_t idV = tt_idesc<Q8>(kTtRows, D, true);
+    const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
+    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + (NT == 2 ? ut * TILE : 0u)),
+                   dk = tc::sdesc_sw128(tc::smem_u32(Ks)),
+                   dv = tc::sdesc_sw128_mn(tc::smem_u32(Vs), kTtCH * 128, 1024);
+    const uint32_t tm_s = __reduce_max_sync(0xffffffffu, tmem) + ut * 128u, tm_o = tm_s + 256u;
+    // S of the stream's next job is issued right behind P V of the job
+    // before, whose P lies in the same columns.
+    Seg ss;                      // the S side's segment
+    int sc = 0, c = 0;           // its chunk counter and chunk
+    int s_seg = 0, q_seen = 0;   // segments walked; query loads waited for (all, in order)
+    bool s_on = ss.begin(&a, ips, sh, true);
+    if (s_on) c = ss.c0;
+    auto s_next = [&]() {
+      ++sc;
+      if (++c == ss.c1) {
+        if (tt_elect()) tc::mma_commit(&sh->qfree[NT == 2 ? t : 0]);  // the segment's query tile has been read
+        __syncwarp();
+        ++s_seg;
+        s_on = ss.next();
+        c = ss.c0;
+      }
+    };
+    if (NT == 1 && s_on && ut == 1u) s_next();  // (stream 1 takes the odd chunks)
+    auto wait_s = [&]() {  // the operands of the next S
+      for (; q_seen <= s_seg; ++q_seen)
+        if (!wait_warp(&sh->qfull[NT == 2 ? t : 0], (uint32_t)q_seen)) return;
+      wait_warp(&sh->kfull[sc % NSK], (uint32_t)(sc / NSK));
+    };
+    auto issue_s = [&]() {
+      if (!ok) return;
+      const int slot = sc % NSK;
+      tc::tc_fence_after();
+      const uint64_t k = dk + (uint64_t)(slot * TILE / 16);
+      if (tt_elect()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = (uint32_t)((j >> 2) * (kTtCH * 128) + (j & 3) * 32);
-          tc::mma_bf16(tmem + t * 128, tc::sdesc_sw128(q + off), tc::sdesc_sw128(k + off), idS, j > 0 ? 1u : 0u);
+          constexpr int kBox = kTtCH * 128 / 16;  // descriptor addresses count 16 bytes
+          const uint64_t off = (uint64_t)((j >> 2) * kBox + (j & 3) * 2);
+          tc::mma_bf16(tm_s, dq + off, k + off, idS, j > 0 ? 1u : 0u);
         }
         tc::mma_commit(&sh->sfull[t]);
         tc::mbar_arrive(&sh->sfull[t]);
-        ++sj;
-        if (NT == 2 && t == 0) return;
         tc::mma_commit(&sh->kempty[slot]);
-        ++sc;
-        if (++c == ss.c1) {
-          tc::mma_commit(&sh->qempty);
-          ++seg_no;
-          s_on = ss.next();
-          c = ss.c0;
-        }
-      };
-      for (int i = 0; i < 2 && s_on && ok; ++i) issue_s();
-      int vc = 0, vj = 0;
-      for (bool on = sg.begin(&a, ips, sh); on && ok; on = sg.next()) {
-        bool fresh[2] = {true, true};  // the stream's next P V starts its accumulator
-        for (int x = sg.c0; x < sg.c1 && ok; ++x, ++vc) {
-          const int slot = vc % NSV;
+      }
+      __syncwarp();
+      s_next();
+      if (NT == 1 && s_on) s_next();
+    };
+    if (s_on) {
+      wait_s();
+      issue_s();
+    }
+    int vc = 0, vj = 0;
+    for (bool on = sg.begin(&a, ips, sh, true); on && ok; on = sg.next()) {
+      uint32_t acc0 = 0u;  // the stream's first P V of the segment starts its accumulator
+      for (int x = sg.c0; x < sg.c1 && ok; ++x, ++vc) {
+        if (NT == 1 && (uint32_t)(vc & 1) != ut) continue;
+        const int slot = vc % NSV;
+        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vc / NSV))) break;
+        // waited for early, so that S follows P V in the tensor pipe without a
+        // gap; not across segments, whose query load may still take a while
+        const bool last = x + NT >= sg.c1 + (NT == 2 ? 1 : -1);
+        if (!last && s_on) wait_s();
+        if (!wait_warp(&sh->pdone[t], (uint32_t)vj)) break;
+        ++vj;
+        tc::tc_fence_after();
+        const uint64_t v = dv + (uint64_t)(slot * TILE / 16);
+        if (tt_elect()) {
 #pragma unroll
-          for (int u = 0; u < NT; ++u, ++vj) {
-            const int t = vj & 1;
-            if (!wait(&sh->pdone[t], (uint32_t)(vj >> 1))) break;
-            if (u == 0 && !wait(&sh->vfull[slot], (uint32_t)(vc / NSV))) break;
-            tc::tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < kTtCH / 16; ++j)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * j,
-                     tc::sdesc_sw128_mn(vb + slot * TILE + (uint32_t)j * 2048u, kTtCH * 128, 1024), idV,
-                     (!fresh[t] || j > 0) ? 1u : 0u);
-            fresh[t] = false;
-            if (u == NT - 1) tc::mma_commit(&sh->vempty[slot]);
-            // the stream's last job of the segment: its output is complete
-            if (NT == 2 ? x == sg.c1 - 1 : x >= sg.c1 - 2) {
-              tc::mma_commit(&sh->ofull[t]);
-              tc::mbar_arrive(&sh->ofull[t]);
-            }
-            if (s_on) issue_s();
+          for (int j = 0; j < kTtCH / 16; ++j)
+            mma_ts(tm_o, tm_s + 8 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+          // the stream's last job of the segment: its output is complete
+          if (last) {
+            tc::mma_commit(&sh->ofull[t]);
+            tc::mbar_arrive(&sh->ofull[t]);
           }
         }
+        __syncwarp();
+        acc0 = 1u;
+        if (s_on) {
+          if (last) wait_s();
+          issue_s();
+        }
+        if (tt_elect()) tc::mma_commit(&sh->vempty[slot]);  // (behind S: the softmax waits for S, nobody yet for V)
+        __syncwarp();
       }
     }
-  } else if (warp < 4) {
-    // ---------------------------------------------------- queries
-    const int qt = tid - 64;
-    int seg_no = 0;
-    for (bool on = sg.begin(&a, ips, sh); on && ok; on = sg.next(), ++seg_no) {
+  } else if (warp == 3) {
+    // ---------------------------------------------------- ahead of the softmax: queries, masks, V rows to clear
+    // Values of slots past the last key may be anything (unwritten cache
+    // rows); a hidden tree row's may too.  0 * NaN is NaN, so such rows are
+    // cleared before the product: of the tree's rows only NaN and infinite
+    // elements, which the segment's end adds to the rows that see them.
+    // (8-bit: the converters do it.)
+    uint64_t* bar = Q8 ? sh->qraw : sh->qfull;
+    int n = 0, vc = 0, nraw = 0, nmask = 0, last_s = -1;
+    for (bool on = sg.begin(&a, ips, sh); on && ok; ++n) {
       const int g = sg.it / p.n_pt, qv0 = (sg.it % p.n_pt) * (NT * kTtRows);
-      if (seg_no > 0 && !wait_warp(&sh->qempty, (uint32_t)(seg_no - 1))) break;
-      constexpr int CPR = D / 8;
-      for (int i = qt; i < NT * kTtRows * CPR; i += 64) {
-        const int r = i / CPR, ch = i % CPR, qv = qv0 + r;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (qv < nqv) {
-          const int row = qv / grp, head = g * grp + qv % grp;
-          w = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                   ((size_t)sg.s * a.rows + row) * QD + (size_t)head * D) + ch);
-        }
-        if constexpr (Q8) {
-          float v[8];
-          const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll 1
+      for (int t = 0; t < NT; ++t) {
+        if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
+        // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
+        if (p.q_tma && lane == 0) {
+          tc::mbar_arrive_expect_tx(&bar[t], TILE);
+          const int tok = sg.s * a.rows + tt_div_grp(p, qv0 + t * kTtRows, grp);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(b2[e]);
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-          }
-          float mx = tt_finite_max(v);
-#pragma unroll
-          for (int o = CPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = tt_exp_of(mx);
-          w = tt_to_half(v, e);
-          if (ch == 0) sh->qe[seg_no & 3][r >> 7][r & 127] = (int8_t)e;
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(Qs + t * TILE + h * (kTtRows * 128), &p.q3, 64 * h, g * grp, tok, &bar[t]);
         }
-        *reinterpret_cast<uint4*>(Qs + (r >> 7) * TILE + tt_off(r & 127, ch)) = w;
       }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(&sh->qfull);
+      Seg nx = sg;
+      const bool more = nx.next();
+      if (more && p.q_tma && lane < NT * (D / 64)) {  // the next segment's queries into L2
+        const int t = lane / (D / 64), h = lane % (D / 64);
+        tma_prefetch_3d(&p.q3, 64 * h, nx.it / p.n_pt * grp,
+                        nx.s * a.rows + tt_div_grp(p, (nx.it % p.n_pt) * (NT * kTtRows) + t * kTtRows, grp));
+      }
+      // the tree's ancestor masks, once per sequence, in turn into four buffers
+      // (the queries of the segment before have been scored, so each stream's
+      // softmax is done with every chunk of the fourth segment back)
+      if (sg.c1 == sg.nch && sg.s != last_s) {
+        last_s = sg.s;
+        uint32_t(*mb)[4] = sh->mask[nmask & 3];
+        if (a.parent)
+          for (int i = lane; i < a.rows; i += 32) sh->par[i] = __ldg(a.parent + (size_t)sg.s * a.rows + i);
+        __syncwarp();
+        for (int i = lane; i < a.rows; i += 32) {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          bool bad = false;
+          if (!tree_row_mask(a.parent ? sh->par : nullptr, i, w, &bad)) w[0] = w[1] = w[2] = w[3] = 0u;  // padding: sees nothing
+          if (bad) raise_status(status, ST_RANGE);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mb[i][k] = w[k];
+        }
+        ++nmask;
+        __syncwarp();
+        tc::mbar_arrive(&sh->mready[(nmask - 1) & 3]);
+      }
+      if constexpr (!Q8) {
+        for (int c = sg.c0; c < sg.c1 && ok; ++c, ++vc) {
+          const int nk = sg.keys(c), slot = vc % NSV;
+          const bool tree = sg.is_tree(c);
+          if (!tree && nk == kTtCH) continue;
+          if (!wait_warp(&sh->vraw[nraw & 3], (uint32_t)(nraw >> 2))) break;
+          ++nraw;
+          constexpr int CPR = D / 8;
+          uint8_t* vt = Vs + slot * TILE;
+          auto at = [&](int i) { return reinterpret_cast<uint4*>(vt + tt_off(i / CPR, i % CPR)); };
+          if (tree) {
+            auto odd_of = [](const uint4& x) {  // bits 15, 31: an exponent of all ones
+              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+              uint32_t odd = 0u;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              return odd;
+            };
+            uint32_t any = 0u;
+#pragma unroll 8
+            for (int i = lane; i < nk * CPR; i += 32) any |= odd_of(*at(i));
+            if (lane < 4) sh->badv[vc % kTtRing][lane] = 0u;
+            __syncwarp();
+            if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll 1
+              for (int i = lane; i < nk * CPR; i += 32) {
+                const uint4 x = *at(i);
+                if (odd_of(x)) {
+                  uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+                    if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
+                  }
+                  *at(i) = make_uint4(e[0], e[1], e[2], e[3]);
+                  atomicOr(&sh->badv[vc % kTtRing][i / CPR >> 5], 1u << (i / CPR & 31));
+                }
+              }
+            }
+          }
+#pragma unroll 4
+          for (int i = nk * CPR + lane; i < kTtCH * CPR; i += 32) *at(i) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh->vfull[slot]);
+        }
+      }
+      on = more;
+      sg = nx;
     }
+    // (a copy that was issued lands before the CTA's shared memory goes away)
+    if (lane == 0 && p.q_tma && n > 0)
+      for (int t = 0; t < NT; ++t) tc::mbar_wait(&bar[t], (uint32_t)(n - 1) & 1u, nullptr, lim_ns);
   } else if (warp < 12) {
     // ---------------------------------------------------- softmax: stream t, one query vector per thread
     const int t = (warp - 4) >> 2;
@@ -548,155 +805,201 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     int nj = 0;         // jobs this stream has done
     int cc = 0;         // chunk counter
     int no[2] = {0, 0}; // segments in which each stream had a job
+    int nmask = 0, last_s = -1;  // ancestor masks waited for, and their sequence
     int seg_no = 0;
     for (bool on = sg.begin(&a, ips, sh); on; on = sg.next(), ++seg_no) {
       const int g = sg.it / p.n_pt, qv0 = (sg.it % p.n_pt) * (NT * kTtRows);
       const int qv = qv0 + (NT == 2 ? t * kTtRows : 0) + r;
       const bool has_row = qv < nqv;
       const bool warp_on = __any_sync(0xffffffffu, has_row);
-      const int node = has_row ? qv / grp : 0;
+      const int node = has_row ? tt_div_grp(p, qv, grp) : 0;
+      const int head = g * grp + (has_row ? qv - node * grp : 0);
+      if ((Q8 || !p.q_tma) && (NT == 2 || t == 0)) {
+        // ---- the thread's row of the query tile: loaded where it is no TMA
+        // box, scaled to fp16 in place with an 8-bit cache
+        uint8_t* qd = Qs + (NT == 2 ? t * TILE : 0);
+        if (p.q_tma) {
+          wait(&sh->qraw[NT == 2 ? t : 0], (uint32_t)seg_no);
+        } else {
+          if (seg_no > 0) wait(&sh->qfree[NT == 2 ? t : 0], (uint32_t)(seg_no - 1));
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                            ((size_t)sg.s * a.rows + node) * QD + (size_t)head * D);
+#pragma unroll 8
+          for (int ch = 0; ch < D / 8; ++ch)
+            *reinterpret_cast<uint4*>(qd + tt_off(r, ch)) = has_row ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+        }
+        if constexpr (Q8) {
+          float mx = 0.f;
+#pragma unroll 4
+          for (int ch = 0; ch < D / 8; ++ch) {
+            float v[8];
+            load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(r, ch)), v);
+            mx = fmaxf(mx, tt_finite_max(v));
+          }
+          const int e = tt_exp_of(mx);
+          sh->qe[seg_no & 3][NT == 2 ? t : 0][r] = (int8_t)e;
+#pragma unroll 4
+          for (int ch = 0; ch < D / 8; ++ch) {
+            uint8_t* q = qd + tt_off(r, ch);
+            float v[8];
+            load8(reinterpret_cast<const __nv_bfloat16*>(q), v);
+            *reinterpret_cast<uint4*>(q) = tt_to_half(v, e);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&sh->qfull[NT == 2 ? t : 0]);
+      }
       const bool has_tree = sg.c1 == sg.nch;  // the segment ends with the tree's rows
       const int tree_ring = (cc + sg.c1 - 1 - sg.c0) % kTtRing;
       float m_run = -INFINITY, l_run = 0.f;
       int e_run = 0;      // O is kept in units of 2^e_run (8-bit cache)
       const int nj0 = nj;
-      bool row_ok = true;
-      uint32_t tm[4] = {0u, 0u, 0u, 0u};
-      if (has_tree) {
-        tc::named_bar(4, 256);  // the parents of the item before have been read
-        if (t == 0 && a.parent && r < a.rows) sh->par[r] = __ldg(a.parent + (size_t)sg.s * a.rows + r);
-        if (!Q8 && t == 0 && r < 4) sh->badv[tree_ring][r] = 0u;
-        tc::named_bar(4, 256);
-        bool bad = false;
-        row_ok = has_row && tree_row_mask(a.parent ? sh->par : nullptr, node, tm, &bad);
-        if (bad) raise_status(status, ST_RANGE);
-      }
+      uint32_t tm[4] = {0u, 0u, 0u, 0u};  // the row's own ancestors, once the tree's chunk comes
+      auto load_mask = [&]() {
+        if (last_s != sg.s) {
+          last_s = sg.s;
+          wait(&sh->mready[nmask & 3], (uint32_t)(nmask >> 2));
+          ++nmask;
+        }
+        if (has_row) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tm[k] = sh->mask[(nmask - 1) & 3][node][k];
+        }
+      };
       for (int c = sg.c0; c < sg.c1; ++c, ++cc) {
         if (NT == 1 && (cc & 1) != t) continue;
         const bool tree = sg.is_tree(c);
         const int nk = sg.keys(c);
         const bool masked = tree || nk < kTtCH;
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = nk - 32 * i;
-          w[i] = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
-          if (tree) w[i] &= row_ok ? tm[i] : 0u;
-        }
-        if constexpr (!Q8) {
-          // Values of slots past the last key may be anything (unwritten
-          // cache rows); a hidden tree row's may too.  0 * NaN is NaN, so
-          // such rows are cleared before the product (NT = 2: by stream 0,
-          // whose product comes first); of the tree's rows only NaN and
-          // infinite elements, which the segment's end adds to who sees them.
-          if (masked && (NT == 1 || t == 0)) {
-            const int slot = cc % NSV;
-            uint8_t* vt = Vs + slot * TILE;
-            if (wait(&sh->vfull[slot], (uint32_t)(cc / NSV))) {
-              for (int i = r; i < kTtCH * (D / 8); i += 128) {
-                const int j = i / (D / 8), ch = i % (D / 8);
-                uint4* q = reinterpret_cast<uint4*>(vt + tt_off(j, ch));
-                if (j >= nk) {
-                  *q = make_uint4(0, 0, 0, 0);
-                } else if (tree) {
-                  uint4 v = *q;
-                  uint32_t e[4] = {v.x, v.y, v.z, v.w};
-                  bool odd = false;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if ((e[k] & 0x7F80u) == 0x7F80u) { e[k] &= 0xFFFF0000u; odd = true; }
-                    if ((e[k] & 0x7F800000u) == 0x7F800000u) { e[k] &= 0xFFFFu; odd = true; }
-                  }
-                  if (odd) {
-                    *q = make_uint4(e[0], e[1], e[2], e[3]);
-                    atomicOr(&sh->badv[tree_ring][j >> 5], 1u << (j & 31));
-                  }
-                }
-              }
-            }
-          }
-        }
+        if (tree) load_mask();
         wait(&sh->sfull[t], (uint32_t)nj);
+        if constexpr (NT == 2) {  // the streams' softmaxes take turns
+          if (t == 1) tc::named_bar(7, 256);
+          else if (nj > 0) tc::named_bar(6, 256);
+        }
         __syncwarp();
         tc::tc_fence_after();
-        if (warp_on) {
-          float cs = a.scale;  // score scale (log2 units)
-          int dv = 0;          // exponent of the chunk's V against O's unit
-          int up = 0;          // how far O's unit moves first
-          if constexpr (Q8) {
-            cs = tt_scale(a.scale, sh->ek[cc % kTtRing] + sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
-            const int ev = sh->ev[cc % kTtRing];
-            if (nj == nj0) e_run = ev;
-            dv = ev - e_run;
-            if (dv > 6) {  // P reaches 2^(8 + dv): fp16 holds 2^15
-              up = dv;
-              e_run = ev;
-              dv = 0;
-            }
+        float cs = a.scale;  // score scale (log2 units)
+        int dv = 0;          // exponent of the chunk's V against O's unit
+        int up = 0;          // how far O's unit moves first
+        if constexpr (Q8) {
+          cs = tt_scale(a.scale, sh->ek[cc % kTtRing] + sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
+          const int ev = sh->ev[cc % kTtRing];
+          if (nj == nj0) e_run = ev;
+          dv = ev - e_run;
+          if (dv > 6) {  // P reaches 2^(8 + dv): fp16 holds 2^15
+            up = dv;
+            e_run = ev;
+            dv = 0;
           }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x[32];
-            tc::tmem_ld32(ts + 32 * i, x);
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = (w[i] >> k) & 1u ? x[k] : -INFINITY;
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
-          }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cs;
-          const float m_new = (m_run == -INFINITY || mx > m_run + 8.f) ? fmaxf(mx, m_run) : m_run;
-          const float alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
-          // O holds the stream's chunks before this one: their products
-          // precede this chunk's S in the tensor pipe, so they are complete.
-          const float beta = up ? tt_scale(alpha, -up) : alpha;
-          if (nj > nj0 && __any_sync(0xffffffffu, beta != 1.f)) {
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              float o[16];
-              tc::tmem_ld16(to + 16 * q, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= beta;
-              tc::tmem_st16(to + 16 * q, o);
-            }
-          }
-          const float sub = m_new == -INFINITY ? 0.f : (float)dv - m_new;
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x[32];
-              tc::tmem_ld32(ts + 64 * h + 32 * i, x);
-              if (masked) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = (w[2 * h + i] >> k) & 1u ? x[k] : -INFINITY;
-              }
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                x[k] = tt_ex2(fmaf(x[k], cs, sub));
-                s4[k & 3] += x[k];
-              }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) pk[16 * i + k] = tt_pack<Q8>(x[2 * k], x[2 * k + 1]);
-            }
-            tmem_st32u(ts + 32 * h, pk);  // over the scores just read
-          }
-          float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          if constexpr (Q8) sum = tt_scale(sum, -dv);
-          l_run = fmaf(l_run, alpha, sum);
-          m_run = m_new;
         }
-        tc::fence_proxy_async_smem();
+        if (warp_on) {
+          // keys 32 i .. of the chunk that the row sees, as bits
+          auto seen = [&](int i) {
+            const int n = nk - 32 * i;
+            uint32_t w = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+            if (tree) w &= i == 0 ? tm[0] : i == 1 ? tm[1] : i == 2 ? tm[2] : tm[3];
+            return w;
+          };
+          auto hide = [&](float (&x)[32], int i) {
+            if (masked) {
+              const uint32_t w = seen(i);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
+            }
+          };
+          auto chunk_max = [&]() {
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float x[32];
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              tc::tmem_ld32(ts + 32 * i, x);
+              hide(x, i);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
+            }
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cs;
+          };
+          unsigned long long sa, sb;
+          auto piece = [&](float (&x)[32], uint32_t (&pk)[16], float m0) {  // weights 2^(cs x + m0), packed; their sums
+            const unsigned long long cs2 = tt_pair(cs, cs), m2 = tt_pair(m0, m0);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float lo, hi;
+              tt_unpair(tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), cs2, m2), lo, hi);
+              lo = tt_ex2(lo);
+              hi = tt_ex2(hi);
+              if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
+              else sa = tt_add2(sa, tt_pair(lo, hi));
+              pk[k] = tt_pack<Q8>(lo, hi);
+            }
+          };
+          auto rescale = [&](float f) {
+            // O holds the stream's chunks before this one: their products
+            // precede this chunk's S in the tensor pipe, so they are complete.
+            if (nj > nj0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                float o[16];
+                tc::tmem_ld16(to + 16 * q, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= f;
+                tc::tmem_st16(to + 16 * q, o);
+              }
+            }
+          };
+          float s0, s1;
+          uint32_t pk[4][16];
+          // bf16: the first chunk is tried against reference 0.  fp16 needs a
+          // reference near its maximum.
+          bool again = Q8 && (nj == nj0 || up);
+#pragma unroll 1
+          for (;;) {
+            float alpha = 1.f;
+            if (again) {
+              const float mx = chunk_max();
+              const float m_new = fmaxf(mx, m_run);
+              alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
+              rescale(up ? tt_scale(alpha, -up) : alpha);
+              m_run = m_new;
+            }
+            const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
+            sa = sb = tt_pair(0.f, 0.f);
+            float x[2][32];
+            tmem_ld32_async(ts, x[0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // the next scores arrive while these are exponentiated
+              tmem_wait(x[i & 1]);
+              if (i < 3) tmem_ld32_async(ts + 32 * (i + 1), x[(i + 1) & 1]);
+              hide(x[i & 1], i);
+              piece(x[i & 1], pk[i], m0);
+            }
+            tt_unpair(tt_add2(sa, sb), s0, s1);
+            const float sum = s0 + s1;
+            // too large for the reference; or a row's first keys, which reference 0 does not suit
+            const bool over = Q8 ? sum > 0x1p15f || (m_run == -INFINITY && sum > 0.f)
+                                 : sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
+            if (again || !__any_sync(0xffffffffu, over)) {
+              if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
+              l_run = fmaf(l_run, alpha, Q8 ? tt_scale(sum, -dv) : sum);
+              break;
+            }
+            again = true;
+          }
+          if constexpr (NT == 2) named_arrive(t == 0 ? 7 : 6, 256);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_st16u(ts + 16 * i, pk[i]);
+        } else if constexpr (NT == 2) {
+          named_arrive(t == 0 ? 7 : 6, 256);
+        }
         tc::tc_fence_before();
         tc::mbar_arrive(&sh->pdone[t]);
         ++nj;
       }
 
       // ---- the segment's end: normalise and write, or leave a partial
+      if (NT == 1 && has_tree && (nj == nj0 || ((cc - 1) & 1) != t)) load_mask();  // (the other stream had the tree)
+      const bool row_ok = !has_tree || (tm[0] | tm[1] | tm[2] | tm[3]) != 0u;
       bool had[2];  // streams with a job in this segment
       had[t] = nj > nj0;
       had[t ^ 1] = NT == 2 ? false : (sg.c1 - sg.c0) > (nj - nj0);
@@ -711,12 +1014,11 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         sh->xl[t][r] = l_run;
         sh->xu[t][r] = f_own;
         tc::named_bar(4, 256);
-        const float mo = sh->xm[t ^ 1][r];
+        const float mo = sh->xm[t ^ 1][r], lo = sh->xl[t ^ 1][r];
         M = fmaxf(m_run, mo);
         const float ao = mo == -INFINITY ? 0.f : tt_ex2(mo - M), as = m_run == -INFINITY ? 0.f : tt_ex2(m_run - M);
         // (both streams' threads form the same sum: stream 0's term first)
-        const float t0 = t == 0 ? l_run * as : sh->xl[0][r] * ao, t1 = t == 0 ? sh->xl[1][r] * ao : l_run * as;
-        L = t0 + t1;
+        L = t == 0 ? l_run * as + lo * ao : lo * ao + l_run * as;
         f_own *= as;
         f_oth = ao * sh->xu[t ^ 1][r];
       }
@@ -731,32 +1033,37 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;
         constexpr int NCOL = NT == 1 ? D / 2 : D;       // columns this thread writes
         const int col0 = NT == 1 ? t * NCOL : 0;
-        const uint32_t o_own = to, o_oth = lane_base + 256 + (t ^ 1) * 128;
         float* part = static_cast<float*>(a.work) +
                       ((size_t)2 * blockIdx.x + (sg.c0 > 0 ? 0 : 1)) * tt_slot_floats<D, NT>();
         const int prow = (NT == 2 ? t * kTtRows : 0) + r;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + ((size_t)sg.s * a.rows + node) * QD +
-                             (size_t)(g * grp + (has_row ? qv % grp : 0)) * D;
+        // (16 bytes per lane and store, to 32 rows: more cache-line accesses than
+        // rows turned among lanes first, but a quarter of the instructions, and
+        // nothing else here uses the load/store unit)
+        const bool write = row_ok && has_row && DFL_CHECK(node < a.rows, status);
+        uint4* out4 = reinterpret_cast<uint4*>(a.out) + ((size_t)(sg.s * a.rows + node) * a.nq + head) * (D / 8);
+        constexpr int W = NCOL < 32 ? NCOL : 32;  // columns per step
+#pragma unroll 1
+        for (int q = 0; q < NCOL / W; ++q) {
+          const int col = col0 + W * q;
+          float o[W];
 #pragma unroll
-        for (int q = 0; q < NCOL / 16; ++q) {
-          const int col = col0 + 16 * q;
-          float o[16], x[16];
+          for (int k = 0; k < W; ++k) o[k] = 0.f;
           __syncwarp();  // the loads below are warp-collective
-          if (had[t]) {
-            tc::tmem_ld16(o_own + col, o);
-          } else {
+          // stream 0's term first whichever thread adds them (NT = 1)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+          for (int u = 0; u < 2; ++u) {
+            const bool own = u == t;
+            if (NT == 2 && !own) continue;
+            if (!had[u]) continue;
+            const float f = own ? f_own : f_oth;
+#pragma unroll
+            for (int e = 0; e < W / 16; ++e) {
+              float x[16];
+              tc::tmem_ld16(lane_base + 256 + u * 128 + col + 16 * e, x);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[16 * e + k] = fmaf(x[k], f, o[16 * e + k]);
+            }
           }
-          if (NT == 1 && had[t ^ 1]) {
-            tc::tmem_ld16(o_oth + col, x);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
-          }
-          // (stream 0's term first whichever thread adds them)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = t == 0 ? fmaf(o[k], f_own, x[k] * f_oth) : fmaf(x[k], f_oth, o[k] * f_own);
           if (any_bad) {  // visible NaN or infinite values: added as they are
             for (int i = 0; i < 4; ++i)
               for (uint32_t b = bad[i]; b; b &= b - 1) {
@@ -764,24 +1071,25 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.vb) +
                                          (((size_t)sg.s * a.rows + j) * a.nkv + g) * D + col;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < W; ++k) {
                   const float f = __bfloat162float(v[k]);
                   if (!(fabsf(f) < INFINITY)) o[k] += f;
                 }
               }
           }
+          __syncwarp();
           if (whole) {
-            if (row_ok && has_row && DFL_CHECK(node < a.rows, status)) {
-              uint4* d4 = reinterpret_cast<uint4*>(dst + col);
-              d4[0] = make_uint4(tt_pack<false>(o[0], o[1]), tt_pack<false>(o[2], o[3]), tt_pack<false>(o[4], o[5]),
-                                 tt_pack<false>(o[6], o[7]));
-              d4[1] = make_uint4(tt_pack<false>(o[8], o[9]), tt_pack<false>(o[10], o[11]),
-                                 tt_pack<false>(o[12], o[13]), tt_pack<false>(o[14], o[15]));
+            if (write) {
+#pragma unroll
+              for (int k = 0; k < W / 8; ++k)
+                out4[col / 8 + k] = make_uint4(tt_pack<false>(o[8 * k], o[8 * k + 1]), tt_pack<false>(o[8 * k + 2], o[8 * k + 3]),
+                                               tt_pack<false>(o[8 * k + 4], o[8 * k + 5]),
+                                               tt_pack<false>(o[8 * k + 6], o[8 * k + 7]));
             }
           } else if (has_row) {
             float4* p4 = reinterpret_cast<float4*>(part) + (size_t)(prow >> 7) * (kTtRows * D / 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < W / 4; ++k)
               p4[(size_t)(col / 4 + k) * kTtRows + (prow & 127)] =
                   make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
@@ -792,131 +1100,167 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           ml[NT * kTtRows + prow] = row_ok ? L : -1.f;
         }
       }
-      if constexpr (NT == 1) tc::named_bar(4, 256);  // both outputs read before either stream goes on
+      // both outputs have been read before either stream goes on
+      if constexpr (NT == 1) tc::named_bar(4, 256);
     }
+    if (NT == 2 && t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
   } else {
     // ---------------------------------------------------- 8-bit cache: tiles to fp16 operands
+    // (after a wait gave up the loops run on without work, to meet the barriers)
     if constexpr (Q8) {
       const int ct = tid - 384, cw = warp - 12;
-      constexpr int LPR = D / 16;       // lanes per code row (16 codes each)
-      constexpr int RPP = 128 / LPR;    // rows per pass
-      constexpr int NP = 128 / RPP;     // passes
-      int i = 0, nr = 0;                // chunks, raw chunks
-      // (after a wait gave up the loops run on without work, to meet the barrier)
+      constexpr int LPR = D / 16;                     // lanes per code row (16 codes each)
+      constexpr int RPP = 128 / LPR, NP = 128 / RPP;  // rows per pass, passes
+      const int cr = ct / LPR, pc = ct % LPR;
+      int i = 0, nr = 0;                      // chunks, raw chunks
+      int ekn = 0, evn = 0;                   // the next chunk's exponents of row ct
+      auto load_exp = [&](int c, int g) {
+        bool badp = false;
+        const size_t row = (size_t)km.row0(sg.s, c * kTtCH, &badp) + (size_t)g * km.head_rows() + ct;
+        const bool in = ct < sg.keys(c);
+        ekn = in ? (int)__ldg(a.k_exp + row) - 127 : -1000;
+        evn = in ? (int)__ldg(a.v_exp + row) - 127 : -1000;
+      };
+      // The largest x and y of the 128 threads, through shared memory.
+      auto group_max = [&](int& x, int& y) {
+        int(*em)[4] = reinterpret_cast<int(*)[4]>(sh->cmax[i & 1]);
+        const int wx = __reduce_max_sync(0xffffffffu, x), wy = __reduce_max_sync(0xffffffffu, y);
+        if (lane == 0) {
+          em[0][cw] = wx;
+          em[1][cw] = wy;
+        }
+        tc::named_bar(5, 128);
+        x = max(max(em[0][0], em[0][1]), max(em[0][2], em[0][3]));
+        y = max(max(em[1][0], em[1][1]), max(em[1][2], em[1][3]));
+      };
       for (bool on = sg.begin(&a, ips, sh); on; on = sg.next()) {
         const int g = sg.it / p.n_pt;
-        int e_top = -1000;              // largest V exponent of the segment so far
+        int e_top = -1000;                    // the largest V exponent of the segment so far
         for (int c = sg.c0; c < sg.c1; ++c, ++i) {
-          const bool tree = sg.is_tree(c);
           const int nk = sg.keys(c);
-          const int ks = i % NSK, vs = i % NSV;
-          uint8_t *kt = Ks + ks * TILE, *vt = Vs + vs * TILE;
-          if (!tree) {
-            bool badp = false;
-            const size_t row0 = (size_t)km.row0(sg.s, c * kTtCH, &badp) + (size_t)g * km.head_rows();
-            int ek4[4], ev4[4];  // rows lane + 32 j
-            int ekm = -1000, evm = -1000;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = lane + 32 * j;
-              ek4[j] = r < nk ? (int)__ldg(a.k_exp + row0 + r) - 127 : -1000;
-              ev4[j] = r < nk ? (int)__ldg(a.v_exp + row0 + r) - 127 : -1000;
-              ekm = max(ekm, ek4[j]);
-              evm = max(evm, ev4[j]);
-            }
-            ekm = __reduce_max_sync(0xffffffffu, ekm);
-            evm = max(__reduce_max_sync(0xffffffffu, evm), e_top - 30);
-            e_top = max(e_top, evm);
+          if (!sg.is_tree(c)) {
+            if (c == sg.c0) load_exp(c, g);
+            const int ek = ekn, ev = evn;
+            if (c + 1 < sg.c1 && !sg.is_tree(c + 1)) load_exp(c + 1, g);
+            int rk = ek, rv = ev;
+            group_max(rk, rv);
+            rv = max(rv, e_top - 30);         // (O's unit never lies 2^30 above a chunk's: see the sums)
+            e_top = max(e_top, rv);
+            sh->fac[0][ct] = tt_half_pow2(max(ek - rk, -1000));
+            sh->fac[1][ct] = tt_half_pow2(max(ev - rv, -1000));
             if (ct == 0) {
-              sh->ek[i % kTtRing] = ekm;
-              sh->ev[i % kTtRing] = evm;
+              sh->ek[i % kTtRing] = rk;
+              sh->ev[i % kTtRing] = rv;
             }
+            tc::named_bar(5, 128);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {     // K, then V
+              const int NR = v ? Cfg::NRV : Cfg::NRK, NS = v ? NSV : NSK, slot = i % NS, rs = nr % NR;
+              const uint8_t* raw = (v ? Rv : Rk) + rs * RAW + cr * D + pc * 16;
+              uint8_t* dst = (v ? Vs : Ks) + slot * TILE;
+              const __half2* fac = sh->fac[v] + cr;
+              if (i >= NS && !wait_warp(v ? &sh->vempty[slot] : &sh->kempty[slot], (uint32_t)(i / NS - 1))) continue;
+              if (!wait_warp(v ? &sh->rvfull[rs] : &sh->rkfull[rs], (uint32_t)(nr / NR))) continue;
+              // all reads of the tile before the first write (one warp per
+              // scheduler: nothing else hides their latency); rows past the
+              // last key zero, their codes may be the NaN code
+              uint4 code[NP];
+              __half2 f[NP];
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {  // K, then V
-              constexpr int NRK = Cfg::NRK, NRV = Cfg::NRV;
-              const int rs = v ? nr % NRV : nr % NRK, rn = v ? nr / NRV : nr / NRK;
-              const uint8_t* raw = (v ? Rv : Rk) + rs * RAW;
-              uint8_t* dstt = v ? vt : kt;
-              if (v ? i >= NSV && !wait_warp(&sh->vempty[vs], (uint32_t)(i / NSV - 1))
-                    : i >= NSK && !wait_warp(&sh->kempty[ks], (uint32_t)(i / NSK - 1)))
-                continue;
-              if (!wait_warp(v ? &sh->rvfull[rs] : &sh->rkfull[rs], (uint32_t)rn)) continue;
+              for (int b = 0; b < NP; ++b) {
+                code[b] = *reinterpret_cast<const uint4*>(raw + b * RPP * D);
+                f[b] = fac[b * RPP];
+              }
 #pragma unroll
-              for (int ps = 0; ps < NP; ++ps) {
-                const int r = ps * RPP + ct / LPR, pc = ct % LPR;
-                const int e = __shfl_sync(0xffffffffu, v ? ev4[ps * RPP / 32] : ek4[ps * RPP / 32], r & 31);
-                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                if (r < nk) {
-                  const uint4 code = *reinterpret_cast<const uint4*>(raw + r * D + pc * 16);
-                  tt_codes_to_half(code, tt_half_pow2(e - (v ? evm : ekm)), lo, hi);
-                }
-                *reinterpret_cast<uint4*>(dstt + tt_off(r, 2 * pc)) = lo;
-                *reinterpret_cast<uint4*>(dstt + tt_off(r, 2 * pc + 1)) = hi;
+              for (int b = 0; b < NP; ++b) {
+                const int row = b * RPP + cr;
+                uint4 lo, hi;
+                if (row >= nk) code[b] = make_uint4(0, 0, 0, 0);
+                tt_codes_to_half(code[b], f[b], lo, hi);
+                *reinterpret_cast<uint4*>(dst + tt_off(row, 2 * pc)) = lo;
+                *reinterpret_cast<uint4*>(dst + tt_off(row, 2 * pc + 1)) = hi;
               }
               tc::fence_proxy_async_smem();
-              tc::mbar_arrive(v ? &sh->vfull[vs] : &sh->kfull[ks]);
+              tc::mbar_arrive(v ? &sh->vfull[slot] : &sh->kfull[slot]);
               tc::mbar_arrive(v ? &sh->rvempty[rs] : &sh->rkempty[rs]);
             }
             ++nr;
           } else {
-            // the tree's bf16 rows: one scale per chunk from their largest finite element
-            constexpr int CPR = D / 8;
-            const size_t base = ((size_t)sg.s * a.rows * a.nkv + g) * D;
+            // the tree's bf16 rows: one scale per chunk from their largest finite
+            // element.  Eight 16-byte pieces per thread and round, in flight at once.
+            constexpr int CPR = D / 8, RS = 128 / CPR, U = 8, RN = RS * U;  // rows per step, per round
             const size_t rstr = (size_t)a.nkv * D;
-            const __nv_bfloat16* kb = reinterpret_cast<const __nv_bfloat16*>(a.kb) + base;
-            const __nv_bfloat16* vb = reinterpret_cast<const __nv_bfloat16*>(a.vb) + base;
+            const size_t off = ((size_t)sg.s * a.rows * a.nkv + g) * D + (size_t)(ct / CPR) * rstr + (ct % CPR) * 8;
+            uint4 x[U];
+            auto load_rows = [&](int v, int r0) {
+              const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(v ? a.vb : a.kb) + off;
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                x[u] = r0 + u * RS + ct / CPR < nk ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(r0 + u * RS) * rstr))
+                                                   : make_uint4(0, 0, 0, 0);
+            };
+            auto unpack = [](const uint4& w, float (&y)[8]) {
+              const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = __bfloat1622float2(b2[k]);
+                y[2 * k] = f.x;
+                y[2 * k + 1] = f.y;
+              }
+            };
             float mk = 0.f, mv = 0.f;
-            for (int q = ct; q < nk * CPR; q += 128) {
-              float x[8];
-              load8(kb + (q / CPR) * rstr + (q % CPR) * 8, x);
-              mk = fmaxf(mk, tt_finite_max(x));
-              load8(vb + (q / CPR) * rstr + (q % CPR) * 8, x);
-              mv = fmaxf(mv, tt_finite_max(x));
-            }
-            mk = warp_max(mk);
-            mv = warp_max(mv);
-            float(*cm)[4] = sh->cmax[i & 1];
-            if (lane == 0) {
-              cm[0][cw] = mk;
-              cm[1][cw] = mv;
+#pragma unroll 1
+            for (int v = 1; v >= 0; --v)      // (K's first round stays in registers)
+#pragma unroll 1
+              for (int r0 = (nk - 1) / RN * RN; r0 >= 0; r0 -= RN) {
+                load_rows(v, r0);
+                float m = v ? mv : mk;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  float y[8];
+                  unpack(x[u], y);
+                  m = fmaxf(m, tt_finite_max(y));
+                }
+                if (v) mv = m;
+                else mk = m;
+              }
+            int rk = tt_exp_of(mk), rv = tt_exp_of(mv);
+            group_max(rk, rv);
+            rv = max(rv, e_top - 30);
+            if (ct == 0) {
+              sh->ek[i % kTtRing] = rk;
+              sh->ev[i % kTtRing] = rv;
             }
             if (ct < 4) sh->badv[i % kTtRing][ct] = 0u;
             tc::named_bar(5, 128);
-            mk = fmaxf(fmaxf(cm[0][0], cm[0][1]), fmaxf(cm[0][2], cm[0][3]));
-            mv = fmaxf(fmaxf(cm[1][0], cm[1][1]), fmaxf(cm[1][2], cm[1][3]));
-            const int ekm = tt_exp_of(mk);
-            const int evm = max(tt_exp_of(mv), e_top - 30);
-            if (ct == 0) {
-              sh->ek[i % kTtRing] = ekm;
-              sh->ev[i % kTtRing] = evm;
-            }
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < 2; ++v) {
-              if (v ? i >= NSV && !wait_warp(&sh->vempty[vs], (uint32_t)(i / NSV - 1))
-                    : i >= NSK && !wait_warp(&sh->kempty[ks], (uint32_t)(i / NSK - 1)))
-                continue;
-              for (int q = ct; q < kTtCH * CPR; q += 128) {
-                const int r = q / CPR, ch = q % CPR;
-                uint4 o = make_uint4(0, 0, 0, 0);
-                if (r < nk) {
-                  float x[8];
-                  load8((v ? vb : kb) + r * rstr + ch * 8, x);
+              const int NS = v ? NSV : NSK, slot = i % NS;
+              uint8_t* dst = (v ? Vs : Ks) + slot * TILE;
+              if (i >= NS && !wait_warp(v ? &sh->vempty[slot] : &sh->kempty[slot], (uint32_t)(i / NS - 1))) continue;
+#pragma unroll 1
+              for (int r0 = 0; r0 < kTtCH; r0 += RN) {
+                if (v || r0 > 0) load_rows(v, r0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  const int row = r0 + u * RS + ct / CPR;
+                  float y[8];
+                  unpack(x[u], y);
                   if (v) {  // a NaN or infinity must not meet a hidden row's weight 0
                     bool odd = false;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                      if (!(fabsf(x[e]) < INFINITY)) {
-                        x[e] = 0.f;
+                    for (int k = 0; k < 8; ++k)
+                      if (!(fabsf(y[k]) < INFINITY)) {
+                        y[k] = 0.f;
                         odd = true;
                       }
-                    if (odd) atomicOr(&sh->badv[i % kTtRing][r >> 5], 1u << (r & 31));
+                    if (odd) atomicOr(&sh->badv[i % kTtRing][row >> 5], 1u << (row & 31));
                   }
-                  o = tt_to_half(x, v ? evm : ekm);
+                  *reinterpret_cast<uint4*>(dst + tt_off(row, ct % CPR)) = tt_to_half(y, v ? rv : rk);
                 }
-                *reinterpret_cast<uint4*>((v ? vt : kt) + tt_off(r, ch)) = o;
               }
               tc::fence_proxy_async_smem();
-              tc::mbar_arrive(v ? &sh->vfull[vs] : &sh->kfull[ks]);
+              tc::mbar_arrive(v ? &sh->vfull[slot] : &sh->kfull[slot]);
             }
           }
         }
@@ -931,81 +1275,105 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   }
 }
 
-// Joins the partials of the items that several CTAs shared.  One warp per
-// (item, tile, 32 rows, 16 columns): lanes are rows, so the partials' reads are
-// 512 contiguous bytes; items of one CTA return at once.
-template <int D, int NT>
+// Joins the partials of the items that several CTAs shared.  Grid: y = the
+// item's first boundary between runs (flat) or the item (aligned), so that
+// only shared items' warps do anything; x = (32 rows, CW columns) of the
+// item, one warp each: lanes are rows, so the partials' reads are 512
+// contiguous bytes; the loads of U partials are in flight at once.
+template <int D, int NT, int CW, int U>
 __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constant__ TreeAttnDesc a, int n_pt, int nb) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int ips = a.nkv * n_pt, grp = a.nq / a.nkv, nqv = a.rows * grp;
-  constexpr int RG = NT * 4, CG = D / 16;  // row groups, column groups of an item
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (long long)a.n_seqs * ips * RG * CG) return;
-  const int cg = (int)(w % CG), rg = (int)(w / CG % RG);
-  const int it = (int)(w / CG / RG % ips), s = (int)(w / CG / RG / ips);
+  constexpr int CG = D / CW;
+  const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int cg = w % CG, rg = w / CG;
+  if (rg >= min(NT * 4, (nqv + 31) / 32)) return;
+  const Part pt = tt_part(a, ips, nb);
+  int s, it, b0, b1, X = 0, per;
+  if (pt.aligned) {
+    const int item = blockIdx.y;
+    if (item >= a.n_seqs * ips) return;
+    s = item / ips;
+    it = item % ips;
+    int n;
+    const int nch = tt_chunks(a, s, &n);
+    per = (nch + pt.sp - 1) / pt.sp;
+    b0 = item * pt.sp;
+    b1 = b0 + (nch - 1) / per;
+  } else {
+    per = pt.per;
+    const int x = (int)(blockIdx.y + 1) * per;
+    if (x >= pt.total) return;
+    const Spot sp = tt_locate(a, ips, x);
+    s = sp.s;
+    it = sp.it;
+    X = x - sp.c + kTtSetup;  // the item's chunks are [X, X + nch)
+    b0 = X / per;
+    b1 = (X + sp.nch - 1) / per;
+    if (x <= X || b0 != (int)blockIdx.y) return;  // no item cut here, or not its first cut
+  }
+  if (b0 == b1) return;  // written by its CTA
   const int g = it / n_pt, qv = (it % n_pt) * (NT * kTtRows) + rg * 32 + lane;
   if (qv - lane >= nqv) return;
-  // the item's chunks [X, X + nch) among all chunks, and the runs that hold them
-  const int n = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
-  const int nch = (n + kTtCH - 1) / kTtCH + 1;
-  long long X = 0, total = 0;
-  for (int q = lane; q < a.n_seqs; q += 32) {
-    const int m = min(max(__ldg(a.base_pos + q), 0), a.max_pos);
-    const long long k = (long long)((m + kTtCH - 1) / kTtCH + 1) * ips;
-    total += k;
-    if (q < s) X += k;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    X += __shfl_xor_sync(0xffffffffu, X, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  X += (long long)it * nch;
-  const long long per = (total + nb - 1) / nb;
-  const int b0 = (int)(X / per), b1 = (int)((X + nch - 1) / per);
-  if (b0 == b1) return;  // written by its CTA
   const int tile = rg >> 2, prow = (rg & 3) * 32 + lane;
-  const float* base = static_cast<const float*>(a.work);
-  auto slot = [&](int b) {
-    return base + ((size_t)2 * b + ((long long)b * per > X ? 0 : 1)) * tt_slot_floats<D, NT>();
-  };
   constexpr int ML = NT * kTtRows * D;
-  const int mrow = tile * kTtRows + prow;
-  const float lb1 = qv < nqv ? slot(b1)[ML + NT * kTtRows + mrow] : -1.f;
-  float M = -INFINITY, L = 0.f, o[16];
+  const int mrow = ML + tile * kTtRows + prow;
+  const size_t orow = (size_t)tile * (kTtRows * D) + ((size_t)(cg * (CW / 4)) * kTtRows + prow) * 4;
+  float M = -INFINITY, L = 0.f, o[CW], last = 0.f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  for (int b = b0; b <= b1; ++b) {
-    const float* sl = slot(b);
-    float4 v[4];
-    const float4* p4 = reinterpret_cast<const float4*>(sl) + (size_t)tile * (kTtRows * D / 4) + (size_t)(cg * 4) * kTtRows + prow;
+  for (int k = 0; k < CW; ++k) o[k] = 0.f;
+#pragma unroll 1
+  for (int b = b0; b <= b1; b += U) {
+    float4 v[U][CW / 4];
+    float mb[U], lb[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = p4[(size_t)k * kTtRows];
-    const float mb = sl[ML + mrow], lb = sl[ML + NT * kTtRows + mrow];
-    const float Mn = fmaxf(M, mb);
-    const float x = M == -INFINITY ? 0.f : tt_ex2(M - Mn), y = mb == -INFINITY ? 0.f : tt_ex2(mb - Mn);
+    for (int u = 0; u < U; ++u) {
+      const int bb = b + u;
+      mb[u] = -INFINITY;
+      lb[u] = 0.f;
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (bb > b1) continue;
+      // slot 0: the item began in an earlier CTA
+      const float* sl = static_cast<const float*>(a.work) + ((size_t)2 * bb + (bb > b0 ? 0 : 1)) * tt_slot_floats<D, NT>();
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) v[u][k] = *reinterpret_cast<const float4*>(sl + orow + (size_t)4 * k * kTtRows);
+      mb[u] = sl[mrow];
+      lb[u] = sl[mrow + NT * kTtRows];
+    }
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, mb[u]);
+    const float x = M == -INFINITY ? 0.f : tt_ex2(M - Mn);
     M = Mn;
-    L = L * x + lb * y;
+    L *= x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[4 * k] = fmaf(v[k].x, y, o[4 * k] * x);
-      o[4 * k + 1] = fmaf(v[k].y, y, o[4 * k + 1] * x);
-      o[4 * k + 2] = fmaf(v[k].z, y, o[4 * k + 2] * x);
-      o[4 * k + 3] = fmaf(v[k].w, y, o[4 * k + 3] * x);
+    for (int k = 0; k < CW; ++k) o[k] *= x;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float y = mb[u] == -INFINITY ? 0.f : tt_ex2(mb[u] - M);
+      L = fmaf(lb[u], y, L);
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) {
+        o[4 * k] = fmaf(v[u][k].x, y, o[4 * k]);
+        o[4 * k + 1] = fmaf(v[u][k].y, y, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(v[u][k].z, y, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(v[u][k].w, y, o[4 * k + 3]);
+      }
+      if (b + u == b1) last = lb[u];  // the tree's partial: negative in a padding row
     }
   }
-  if (qv >= nqv || lb1 < 0.f) return;
+  if (qv >= nqv || last < 0.f) return;
   const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
   const int node = qv / grp, head = g * grp + qv % grp;
-  uint4* d4 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                       ((size_t)s * a.rows + node) * a.nq * D + (size_t)head * D + cg * 16);
-  uint32_t u[8];
+  uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((size_t)s * a.rows + node) * a.nq * D +
+                                        (size_t)head * D + cg * CW);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) u[k] = tt_pack<false>(o[2 * k] * inv, o[2 * k + 1] * inv);
-  d4[0] = make_uint4(u[0], u[1], u[2], u[3]);
-  d4[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  for (int k = 0; k < CW / 8; ++k)
+    out[k] = make_uint4(tt_pack<false>(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack<false>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                        tt_pack<false>(o[8 * k + 4] * inv, o[8 * k + 5] * inv), tt_pack<false>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
 }
 
 template <int D, int NT, bool Q8>
@@ -1015,6 +1383,8 @@ cudaError_t tt_launch(const TreeAttnDesc& a, int num_sms, cudaStream_t st) {
   p.a = a;
   const int nqv = a.rows * (a.nq / a.nkv);
   p.n_pt = (nqv + NT * kTtRows - 1) / (NT * kTtRows);
+  const uint32_t grp = a.nq / a.nkv;
+  p.grp_mul = grp >= 2 && grp <= 256 ? (uint32_t)((0x100000000ull + grp - 1) / grp) : 0u;
   const uint64_t rows = a.pages ? (uint64_t)a.pool * a.nkv * a.ps : (uint64_t)a.n_seqs * a.nkv * a.cap;
   bool okm;
   if (Q8) {
@@ -1026,14 +1396,21 @@ cudaError_t tt_launch(const TreeAttnDesc& a, int num_sms, cudaStream_t st) {
     okm = make_tmap_bf16(&p.kc, a.kc, D, rows, kTtCH) && make_tmap_bf16(&p.vc, a.vc, D, rows, kTtCH) &&
           make_tmap3_bf16(&p.kb, a.kb, D, a.nkv, M, 1, kTtCH) && make_tmap3_bf16(&p.vb, a.vb, D, a.nkv, M, 1, kTtCH);
   }
+  p.q_tma = kTtRows % grp == 0;
+  if (p.q_tma)
+    okm = okm && make_tmap3_bf16(&p.q3, a.q, D, a.nq, (uint64_t)a.n_seqs * a.rows, grp, kTtRows / grp);
+  else
+    p.q3 = p.kc;
   if (!okm) return cudaErrorInvalidValue;
   cudaError_t e =
       cudaFuncSetAttribute(tree_tc_kernel<D, NT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_tc_kernel<D, NT, Q8>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)a.n_seqs * a.nkv * p.n_pt * (NT * 4) * (D / 16);
-  return launch_pdl(tree_tc_merge_kernel<D, NT>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a, p.n_pt,
+  // NT = 1: narrow columns (many warps, few rows a call); NT = 2: wide ones.
+  constexpr int CW = NT == 1 ? 8 : 32, U = NT == 1 ? 8 : 2;
+  const int warps = (nqv < NT * kTtRows ? (nqv + 31) / 32 : NT * 4) * (D / CW);
+  return launch_pdl(tree_tc_merge_kernel<D, NT, CW, U>, dim3((warps + 3) / 4, num_sms), dim3(128), 0, st, a, p.n_pt,
                     num_sms);
 }
 
