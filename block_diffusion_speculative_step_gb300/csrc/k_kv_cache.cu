@@ -19,6 +19,7 @@
 namespace dfl {
 
 constexpr int kKvThreads = 256;
+constexpr int kKvHeads = 4;
 constexpr int kKvExpLim = 60;
 constexpr int kKvExpBias = 127;
 
@@ -28,10 +29,11 @@ __device__ __forceinline__ float pow2_f(int e) { return __int_as_float((e + 127)
 // KV head 0; false when the row is skipped.
 __device__ __forceinline__ bool kv_row(const KvRowsDesc& k, const int32_t* pages, int s, int i, int n, size_t* row,
                                        uint32_t* head_rows) {
-  const long long pos = (long long)__ldg(k.base_pos + s) + i;
+  const int base = __ldg(k.base_pos + s);
   if (k.window > 0 && i + k.window < n) return false;  // a later row of this call takes the same slot
-  const long long slot = k.window > 0 ? pos % k.window : pos;
-  if (pos < 0 || slot >= k.cap) {
+  const uint32_t pos = (uint32_t)base + (uint32_t)i;   // (i < 2^27: from base >= 0 no wrap)
+  const uint32_t slot = k.window > 0 ? pos % (uint32_t)k.window : pos;
+  if ((base < 0 && (int)pos < 0) || slot >= (uint32_t)k.cap) {
     raise_status(k.status, ST_RANGE);
     return false;
   }
@@ -55,81 +57,107 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Grid: x over row vectors (s, i, head), y = 2 * layer + (0: K, 1: V).
-// Every d / 8 neighbouring threads hold one vector, 8 elements each.
+// A thread's share: 8 elements of up to kKvHeads neighbouring heads of one row
+// of K or V.  The tensor's cost is its bytes (a row is read once and written
+// once), so the address of a row -- position, page, two divisions -- is worked
+// out once for its heads, and their loads are in flight together: with one
+// head per thread, 512 rows x 8 heads x 36 layers took KV_OLD_US us instead of KV_NEW_US.
+struct KvUnit {
+  int s, i, m, head, heads, e0, layer;
+  bool is_v, on;
+  __device__ __forceinline__ KvUnit(const KvRowsDesc& k) {
+    const uint32_t tpv = (uint32_t)k.d >> 3;  // threads per vector: 8 or 16
+    const uint32_t n_hg = ((uint32_t)k.nkv + kKvHeads - 1) / kKvHeads;
+    const uint32_t u = blockIdx.x * (kKvThreads / tpv) + threadIdx.x / tpv;  // < 2^27 + 32
+    m = (int)(u / n_hg);
+    head = (int)(u % n_hg) * kKvHeads;
+    heads = min(kKvHeads, k.nkv - head);
+    e0 = (int)(threadIdx.x % tpv) * 8;
+    s = (int)((uint32_t)m / (uint32_t)k.rows);
+    i = m - s * k.rows;
+    layer = blockIdx.y >> 1;
+    is_v = blockIdx.y & 1;
+    on = s < k.S;
+  }
+};
+
+// The smallest e with mx <= 448 * 2^e, held to the limits.  mx = g 2^x with g
+// in [1, 2): e = x - 8, plus one when g > 1.75.  (0 and subnormals: the lower limit.)
+__device__ __forceinline__ int kv_exponent(float mx) {
+  const int b = __float_as_int(mx);
+  const int e = (b >> 23) - 127 - 8 + ((b & 0x7FFFFF) > 0x600000 ? 1 : 0);
+  return min(max(e, -kKvExpLim), kKvExpLim);
+}
+
+// Grid: x over units, y = 2 * layer + (0: K, 1: V).
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvRowsDesc k,
                                                               const __grid_constant__ KvRowsLayers l) {
   pdl_wait();
   pdl_launch_dependents();
-  const int tpv = k.d / 8;  // threads per vector: 8 or 16
-  const long long t = (long long)blockIdx.x * kKvThreads + threadIdx.x;
-  const long long vec = t / tpv;
-  const int e0 = (int)(t % tpv) * 8;
-  const int layer = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
-  bool on = vec < (long long)k.S * k.rows * k.nkv;
-  const int m = on ? (int)(vec / k.nkv) : 0, head = (int)(vec % k.nkv);
-  const int s = m / k.rows, i = m % k.rows;
-  const int n = k.valid ? min(__ldg(k.valid + s), k.rows) : k.rows;
-  on = on && i < n;
-  int src = i;
-  if (on && k.row_index) {
-    src = __ldg(k.row_index + m);
+  KvUnit u(k);
+  const int n = u.on ? (k.valid ? min(__ldg(k.valid + u.s), k.rows) : k.rows) : 0;
+  int src = u.i;
+  u.on = u.on && u.i < n;
+  if (u.on && k.row_index) {
+    src = __ldg(k.row_index + u.m);
     if (src < 0 || src >= k.rows) {
       raise_status(k.status, ST_RANGE);
-      on = false;
+      u.on = false;
     }
+  }
+  float v[kKvHeads][8];
+  if (u.on) {
+    const T* p = reinterpret_cast<const T*>(u.is_v ? l.src_v[u.layer] : l.src_k[u.layer]) +
+                 (((size_t)u.s * k.rows + src) * k.nkv + u.head) * k.d + u.e0;
+#pragma unroll
+    for (int h = 0; h < kKvHeads; ++h)
+      if (h < u.heads) load8(p + h * k.d, v[h]);
   }
   size_t row = 0;
   uint32_t hr = 0;
-  on = on && kv_row(k, l.pages[layer], s, i, n, &row, &hr);
-  float v[8];
+  u.on = u.on && kv_row(k, l.pages[u.layer], u.s, u.i, n, &row, &hr);
+  row += (size_t)u.head * hr;
+  void* dst = u.is_v ? l.dst_v[u.layer] : l.dst_k[u.layer];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  if (on) {
-    const T* p = reinterpret_cast<const T*>(is_v ? l.src_v[layer] : l.src_k[layer]);
-    load8(p + (((size_t)s * k.rows + src) * k.nkv + head) * k.d + e0, v);
-  }
-  row += (size_t)head * hr;
-  void* dst = is_v ? l.dst_v[layer] : l.dst_k[layer];
-  if constexpr (!Q8) {
-    if (on) store8(reinterpret_cast<T*>(dst) + row * k.d + e0, v);
-  } else {
-    float mx = 0.f;
-    uint32_t odd = 0;  // bit j: element j is NaN or infinite
+  for (int h = 0; h < kKvHeads; ++h, row += hr) {
+    if constexpr (!Q8) {
+      if (u.on && h < u.heads) store8(reinterpret_cast<T*>(dst) + row * k.d + u.e0, v[h]);
+    } else {
+      const bool on = u.on && h < u.heads;
+      float mx = 0.f;
+      uint32_t odd = 0;  // bit j: element j is NaN or infinite
+      if (on) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[j]);
-      if (a < INFINITY) mx = fmaxf(mx, a);
-      else odd |= 1u << j;
-    }
-    for (int o = tpv >> 1; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (!on) return;
-    if (odd) raise_status(k.status, ST_NUMERIC);
-    int e = -kKvExpLim;
-    if (mx > 0.f) {
-      int kk;
-      const float f = frexpf(mx, &kk);
-      e = min(max(kk - 9 + (f > 0.875f ? 1 : 0), -kKvExpLim), kKvExpLim);
-    }
-    const float inv = pow2_f(-e);
-    uint32_t w[2];
+        for (int j = 0; j < 8; ++j) {
+          const float a = fabsf(v[h][j]);
+          if (a < INFINITY) mx = fmaxf(mx, a);
+          else odd |= 1u << j;
+        }
+      }
+      // (a row's threads are a half or a quarter of a warp; all its lanes take part)
+      for (int o = k.d >> 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (!on) continue;
+      if (odd) raise_status(k.status, ST_NUMERIC);
+      const int e = kv_exponent(mx);
+      const float inv = pow2_f(-e);
+      uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * inv, v[4 * h + 1] * inv),
-                                                              __NV_SATFINITE, __NV_E4M3);
-      const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv),
-                                                              __NV_SATFINITE, __NV_E4M3);
-      w[h] = (uint32_t)a | ((uint32_t)b << 16);
-    }
-    if (odd) {
+      for (int q = 0; q < 2; ++q) {
+        const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
+            make_float2(v[h][4 * q] * inv, v[h][4 * q + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
+            make_float2(v[h][4 * q + 2] * inv, v[h][4 * q + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        w[q] = (uint32_t)a | ((uint32_t)b << 16);
+      }
+      if (odd) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((odd >> j) & 1u) w[j >> 2] = (w[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | (0x7Fu << (8 * (j & 3)));
+        for (int j = 0; j < 8; ++j)
+          if ((odd >> j) & 1u) w[j >> 2] = (w[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | (0x7Fu << (8 * (j & 3)));
+      }
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(dst) + row * k.d + u.e0) = make_uint2(w[0], w[1]);
+      if (u.e0 == 0) (u.is_v ? l.v_exp[u.layer] : l.k_exp[u.layer])[row] = (uint8_t)(e + kKvExpBias);
     }
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(dst) + row * k.d + e0) = make_uint2(w[0], w[1]);
-    if (e0 == 0) (is_v ? l.v_exp[layer] : l.k_exp[layer])[row] = (uint8_t)(e + kKvExpBias);
   }
 }
 
@@ -138,47 +166,59 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
                                                              const __grid_constant__ KvRowsLayers l) {
   pdl_wait();
   pdl_launch_dependents();
-  const int tpv = k.d / 8;
-  const long long t = (long long)blockIdx.x * kKvThreads + threadIdx.x;
-  const long long vec = t / tpv;
-  const int e0 = (int)(t % tpv) * 8;
-  const int layer = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
-  if (vec >= (long long)k.S * k.rows * k.nkv) return;
-  const int m = (int)(vec / k.nkv), head = (int)(vec % k.nkv);
-  const int s = m / k.rows, i = m % k.rows;
-  const int n = k.valid ? min(__ldg(k.valid + s), k.rows) : k.rows;
-  if (i >= n) return;
+  const KvUnit u(k);
+  if (!u.on) return;
+  const int n = k.valid ? min(__ldg(k.valid + u.s), k.rows) : k.rows;
+  if (u.i >= n) return;
   size_t row;
   uint32_t hr;
-  if (!kv_row(k, l.pages[layer], s, i, 0, &row, &hr)) return;
-  row += (size_t)head * hr;
-  const void* src = is_v ? l.src_v[layer] : l.src_k[layer];
-  float v[8];
+  if (!kv_row(k, l.pages[u.layer], u.s, u.i, 0, &row, &hr)) return;
+  row += (size_t)u.head * hr;
+  const void* src = u.is_v ? l.src_v[u.layer] : l.src_k[u.layer];
+  T* out = reinterpret_cast<T*>(u.is_v ? l.dst_v[u.layer] : l.dst_k[u.layer]) +
+           ((size_t)u.m * k.nkv + u.head) * k.d + u.e0;
+  float v[kKvHeads][8];
   if constexpr (!Q8) {
-    load8(reinterpret_cast<const T*>(src) + row * k.d + e0, v);
-  } else {
-    const uint2 c = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(src) + row * k.d + e0);
-    const float sc = pow2_f((int)__ldg((is_v ? l.v_exp[layer] : l.k_exp[layer]) + row) - kKvExpBias);
-    const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2_raw h =
-          __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      v[2 * j] = f.x * sc;
-      v[2 * j + 1] = f.y * sc;
+    for (int h = 0; h < kKvHeads; ++h)
+      if (h < u.heads) load8(reinterpret_cast<const T*>(src) + (row + (size_t)h * hr) * k.d + u.e0, v[h]);
+  } else {
+    const uint8_t* ex = u.is_v ? l.v_exp[u.layer] : l.k_exp[u.layer];
+    uint2 c[kKvHeads];
+    int e[kKvHeads];
+#pragma unroll
+    for (int h = 0; h < kKvHeads; ++h) {
+      if (h < u.heads) {
+        const size_t r = row + (size_t)h * hr;
+        c[h] = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(src) + r * k.d + u.e0);
+        e[h] = ex[r];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kKvHeads; ++h) {
+      if (h >= u.heads) break;
+      const float sc = pow2_f(e[h] - kKvExpBias);
+      const uint32_t w[2] = {c[h].x, c[h].y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2_raw x =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu), __NV_E4M3);
+        const float2 f = __half22float2(__half2(x));
+        v[h][2 * j] = f.x * sc;
+        v[h][2 * j + 1] = f.y * sc;
+      }
     }
   }
-  void* dst = is_v ? l.dst_v[layer] : l.dst_k[layer];
-  store8(reinterpret_cast<T*>(dst) + ((size_t)m * k.nkv + head) * k.d + e0, v);
+#pragma unroll
+  for (int h = 0; h < kKvHeads; ++h)
+    if (h < u.heads) store8(out + h * k.d, v[h]);
 }
 
 template <typename F>
 static cudaError_t kv_launch(F kernel, const KvRowsDesc& k, const KvRowsLayers& l, cudaStream_t st) {
-  const long long thr = (long long)k.S * k.rows * k.nkv * (k.d / 8);
-  if (thr == 0) return cudaSuccess;
-  const dim3 grid((unsigned)((thr + kKvThreads - 1) / kKvThreads), 2 * k.n_layers);
+  const int upb = kKvThreads / (k.d / 8);
+  const long long units = (long long)k.S * k.rows * ((k.nkv + kKvHeads - 1) / kKvHeads);
+  const dim3 grid((unsigned)((units + upb - 1) / upb), 2 * k.n_layers);
   return launch_pdl(kernel, grid, dim3(kKvThreads), 0, st, k, l);
 }
 

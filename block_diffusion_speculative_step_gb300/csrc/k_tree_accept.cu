@@ -14,11 +14,18 @@
 // drawn candidate (Z_t), one for the last draw.
 //
 // One thread-block cluster per sequence, each CTA a contiguous slice of the
-// vocabulary; sums cross the cluster through distributed shared memory and
-// every CTA forms them in rank order, so all CTAs take the same decisions
-// and a call is deterministic.  Remaining masses are sums over what remains
-// (children's weights are kept out of the row sums and added one by one):
-// 1 - p(x) would lose all its digits when p(x) is close to 1.
+// vocabulary.  Partial sums are pushed to every CTA of the cluster through
+// distributed shared memory, and every CTA joins them in the same tree order,
+// so all CTAs take the same decisions and a call is deterministic.  Remaining
+// masses are sums over what remains (children's weights are kept out of the
+// row sums and added one by one): 1 - p(x) would lose all its digits when
+// p(x) is close to 1.
+//
+// A walk is a chain of row passes and exchanges, each waiting for the one
+// before: latency bounds it, not bytes.  So a thread has kTaE loads in flight
+// at once, and the weights of a slice's first batch (10240 entries) stay in
+// registers from the row sums to the tests and the draw; a slice's rest is
+// read again, from L2.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -32,40 +39,45 @@ namespace cg = cooperative_groups;
 
 constexpr int kTaThreads = 512;
 constexpr int kTaWarps = kTaThreads / 32;
-constexpr int kTaMaxNC = 16;
+// Entries per thread and batch: 20 (two rows of them and the next batch fill
+// 128 registers), 4 for slices of at most 2048, whose threads would mostly
+// work on entries that are not there.
+constexpr int kTaE = 20, kTaShortE = 4;
+constexpr int kTaMaxCluster = 16;
 
-// Weight of logit l against the row's maximum m (l == m also when both are
-// infinite: the weight is then 1 and the caller reports the row).
-__device__ __forceinline__ float ta_weight(float l, float m, float invT) {
-  return l == m ? 1.f : expf((l - m) * invT);
+// Weight exp((l - m) / T) = 2^(c (l - m)) of logit l against the row's maximum
+// m, c = log2(e) / T (l == m also when both are infinite: the weight is then 1
+// and the caller reports the row).  Beside the argument's rounding, which
+// exp((l - m) * (1 / T)) has too, the hardware's 2^x adds 2^-22.
+__device__ __forceinline__ float ta_weight(float l, float m, float c) {
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - m) * c));
+  return l == m ? 1.f : w;
 }
 
-struct TaSum {  // running maximum and sum of weights against it
+struct TaSum {  // maximum and sum of weights against it
   float m, s;
 };
-__device__ __forceinline__ TaSum ta_merge(TaSum a, TaSum b, float invT) {
-  TaSum r;
-  r.m = fmaxf(a.m, b.m);
-  r.s = (a.s > 0.f ? a.s * ta_weight(a.m, r.m, invT) : 0.f) + (b.s > 0.f ? b.s * ta_weight(b.m, r.m, invT) : 0.f);
-  return r;
+// Joined over the warp, bitwise the same in every lane.
+__device__ __forceinline__ TaSum ta_join(TaSum a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = a.s > 0.f ? a.s * ta_weight(a.m, m, c) : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
 }
-
-// Calls f(v, x) for the elements of row[v0, v1), vectorised over the 16-byte
-// aligned middle; the assignment of elements to threads is fixed.
-template <typename F>
-__device__ __forceinline__ void ta_for(const float* __restrict__ row, int v0, int v1, F f) {
-  const int mis = (int)((reinterpret_cast<uintptr_t>(row + v0) >> 2) & 3);
-  const int a = min(v1, v0 + ((4 - mis) & 3));
-  const int b = a + ((v1 - a) & ~3);
-  if (v0 + (int)threadIdx.x < a) f(v0 + (int)threadIdx.x, row[v0 + threadIdx.x]);
-  for (int v = a + 4 * (int)threadIdx.x; v < b; v += 4 * kTaThreads) {
-    const float4 x = *reinterpret_cast<const float4*>(row + v);
-    f(v, x.x);
-    f(v + 1, x.y);
-    f(v + 2, x.z);
-    f(v + 3, x.w);
+__device__ __forceinline__ void ta_best_join(float& b, int& v) {  // lowest index on equal values
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float ob = __shfl_xor_sync(0xffffffffu, b, o);
+    const int ov = __shfl_xor_sync(0xffffffffu, v, o);
+    if (ob > b || (ob == b && ov < v)) {
+      b = ob;
+      v = ov;
+    }
   }
-  if (b + (int)threadIdx.x < v1) f(b + (int)threadIdx.x, row[b + threadIdx.x]);
 }
 
 struct TaShared {
@@ -74,51 +86,84 @@ struct TaShared {
   float u[DFLASH_MAX_TREE];
   int n_child;
   int child[DFLASH_MAX_TREE];   // children of the current node, in row order
-  int ctok[DFLASH_MAX_TREE];
+  int ctok[DFLASH_MAX_TREE];    // -1: out of range
   float cu[DFLASH_MAX_TREE];
-  float cl[DFLASH_MAX_TREE];    // the children's target / draft logits
+  float cl[DFLASH_MAX_TREE];    // the children's target / draft logits (NaN: -inf)
   float cg[DFLASH_MAX_TREE];
   int cdup[DFLASH_MAX_TREE];    // an earlier sibling has the same token, or the token is out of range
-  double sufP[DFLASH_MAX_TREE + 1];  // mass of the target / draft row without the tokens of children [0, t)
-  double sufQ[DFLASH_MAX_TREE + 1];
-  unsigned long long bloom;     // bit (token / 4) % 64 of every child's token
+  float cp[DFLASH_MAX_TREE];    // p_t of the child's token (drawn) or its weight; its weight in the draft row, 0 once removed
+  float cq[DFLASH_MAX_TREE];
+  double sufP[DFLASH_MAX_TREE + 1];  // mass of the target row without the tokens of children [0, t)
   float invZ[DFLASH_MAX_TREE];  // 1 / Z_t, 0: nothing left, p stays
   float invY[DFLASH_MAX_TREE];  // 1 / (remaining mass of q before step t), in q's weights
   TaSum wp[kTaWarps], wq[kTaWarps];
   float wb[kTaWarps];
   int wi[kTaWarps];
-  TaSum xp[2], xq[2];           // this CTA's partials, by parity (read by the cluster)
-  float xb[2];
-  int xi[2];
+  float4 xs[2][kTaMaxCluster];  // pushed by the cluster's CTAs, by exchange parity: row sums; Z; (best, token)
 };
 
-template <bool Drawn>
-__global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const __grid_constant__ TreeAcceptDesc d) {
-  pdl_wait();
-  pdl_launch_dependents();
+template <bool Drawn, int E>
+__global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid_constant__ TreeAcceptDesc d) {
+  constexpr int BATCH = kTaThreads * E;
   __shared__ TaShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int NC = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int s = blockIdx.x / NC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = d.V, N = d.rows;
-  const int per = (V + NC - 1) / NC;
+  const int per = ((V + NC - 1) / NC + 31) & ~31;
   const int v0 = min(V, rank * per), v1 = min(V, v0 + per);
-  const float invT = d.invT;
+  const float c2 = d.invT * 1.44269504f;  // log2(e) / T
   const float* target = d.target + (size_t)s * N * V;
   const float* draft = Drawn ? d.draft + (size_t)s * d.levels * V : nullptr;
+  const float* noise = d.noise + (size_t)s * V;
   int par = 0;  // exchange parity
+  if (NC > 1) cl.sync();  // (every CTA runs before the first push into it)
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // a CTA's contribution to all CTAs of the cluster, from warp 0; afterwards
+  // lane r of every warp holds CTA r's
+  auto exchange = [&](float4 x) __attribute__((always_inline)) {
+    if (NC > 1) {
+      if (warp == 0 && lane < NC) cl.map_shared_rank(&sh, lane)->xs[par][rank] = x;
+      cl.sync();
+    } else {
+      if (tid == 0) sh.xs[par][0] = x;
+      __syncthreads();
+    }
+    const float4 r = lane < NC ? sh.xs[par][lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    par ^= 1;
+    return r;
+  };
+  // entries b * BATCH + j * kTaThreads + tid of the slice: scalar loads,
+  // coalesced whatever the row's alignment (rows of an odd V)
+  auto load = [&](const float* row, int b, float (&x)[E]) __attribute__((always_inline)) {
+    const int v = v0 + b * BATCH + tid;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      x[j] = v + j * kTaThreads < v1 ? __ldg(row + v + j * kTaThreads) : -INFINITY;
+    }
+  };
 
   for (int i = tid; i < N; i += kTaThreads) {
     sh.parent[i] = d.parent ? d.parent[(size_t)s * N + i] : i - 1;
     sh.tok[i] = d.tokens[(size_t)s * N + i];
     sh.u[i] = d.u[(size_t)s * N + i];
   }
+  // every sequence ends with one draw: its noise comes to L2 meanwhile
+  for (int v = v0 + 32 * tid; v < v1; v += 32 * kTaThreads)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + v));
   __syncthreads();
 
   int cur = 0, k = 0;
   if (rank == 0 && tid == 0) d.path[(size_t)s * N] = 0;
   for (;;) {
+    const float* l = target + (size_t)cur * V;
+    const bool deep = Drawn && k >= d.levels;  // no draft row for the node's children
+    float lw[E], gw[E];                  // the first batch: logits, then weights, then p_t and q's weights
+    load(l, 0, lw);
+    if (Drawn && !deep) load(draft + (size_t)k * V, 0, gw);
     // ---- children of cur, in row order
     if (warp == 0) {
       int n = 0;
@@ -129,174 +174,233 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const __grid_co
         if (c) sh.child[n + __popc(bal & ((1u << lane) - 1u))] = i;
         n += __popc(bal);
       }
-      if (lane == 0) {
-        sh.n_child = n;
-        sh.bloom = 0ull;
-      }
+      if (lane == 0) sh.n_child = n;
     }
     __syncthreads();
     int n_child = sh.n_child;
-    const bool deep = Drawn && k >= d.levels;  // no draft row for these children
     if (deep) {
       if (n_child > 0 && rank == 0 && tid == 0) raise_status(d.status, ST_RANGE);
       n_child = 0;
     }
-    const float* l = target + (size_t)cur * V;
     const float* g = Drawn && n_child > 0 ? draft + (size_t)k * V : nullptr;
-    for (int c = tid; c < n_child; c += kTaThreads) {
-      const int i = sh.child[c];
+    if (Drawn) {
+      if (!g) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          gw[j] = -INFINITY;
+        }
+      }
+    }
+    if (tid < n_child) {
+      const int i = sh.child[tid];
       int x = sh.tok[i];
       if (x < 0 || x >= V) {
         if (rank == 0) raise_status(d.status, ST_RANGE);
         x = -1;  // never accepted, nothing to remove
       }
-      sh.ctok[c] = x;
-      sh.cu[c] = sh.u[i];
-      sh.cl[c] = x >= 0 ? l[x] : -INFINITY;
-      if (Drawn) sh.cg[c] = x >= 0 ? g[x] : -INFINITY;
-      int dup = 0;
-      for (int e = 0; e < c; ++e) dup |= sh.tok[sh.child[e]] == x;
-      sh.cdup[c] = dup || x < 0;
-      if (x >= 0) atomicOr(&sh.bloom, 1ull << ((x >> 2) & 63));
+      sh.ctok[tid] = x;
+      sh.cu[tid] = sh.u[i];
+      const float a = x >= 0 ? l[x] : -INFINITY;
+      if (!(a < INFINITY)) raise_status(d.status, ST_NUMERIC);
+      sh.cl[tid] = a == a ? a : -INFINITY;
+      if (Drawn) {
+        const float b = x >= 0 ? g[x] : -INFINITY;
+        if (!(b < INFINITY)) raise_status(d.status, ST_NUMERIC);
+        sh.cg[tid] = b == b ? b : -INFINITY;
+      }
+      int dup = x < 0;
+      for (int e = 0; e < tid; ++e) dup |= sh.tok[sh.child[e]] == x;
+      sh.cdup[tid] = dup;
     }
     __syncthreads();
 
-    // ---- maxima and sums over the slice, the children's tokens left out of the sums
-    const unsigned long long bloom = n_child > 0 ? sh.bloom : 0ull;
-    auto is_child = [&](int v) {
-      if (!((bloom >> ((v >> 2) & 63)) & 1ull)) return false;
-      for (int c = 0; c < n_child; ++c)
-        if (sh.ctok[c] == v) return true;
-      return false;
-    };
+    // ---- maxima and sums over the slice, the children's tokens left out
     bool nan = false;
-    auto row_sum = [&](const float* row) {
-      TaSum a = {-INFINITY, 0.f};
-      ta_for(row, v0, v1, [&](int v, float x) {
-        if (!(x < INFINITY)) nan = true;  // NaN or +inf
-        if (is_child(v) || x != x) return;
-        if (x > a.m) {
-          a.s = a.s > 0.f ? a.s * ta_weight(a.m, x, invT) + 1.f : 1.f;
-          a.m = x;
-        } else if (x > -INFINITY) {
-          a.s += expf((x - a.m) * invT);
-        }
-      });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        TaSum b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-        a = ta_merge(a, b, invT);
+    auto clean = [&](int b, float (&x)[E]) __attribute__((always_inline)) {  // NaN and the children's tokens: weight 0
+      uint32_t mine = 0u;  // bit j: entry j is a child's token
+      for (int c = 0; c < n_child; ++c) {
+        const int x0 = sh.ctok[c];
+        const unsigned rel = (unsigned)(x0 - v0 - b * BATCH);
+        if (x0 >= 0 && rel < (unsigned)BATCH && (int)(rel % kTaThreads) == tid) mine |= 1u << (rel / kTaThreads);
       }
-      return a;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        if (!(x[j] < INFINITY)) nan = true;
+        x[j] = x[j] == x[j] && !((mine >> j) & 1u) ? x[j] : -INFINITY;
+      }
     };
-    TaSum ap = row_sum(l), aq = {-INFINITY, 0.f};
-    if (Drawn && g) aq = row_sum(g);
+    auto add = [&](TaSum& a, float (&x)[E]) __attribute__((always_inline)) {  // logits -> weights against the maximum so far
+      float m = a.m;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        m = fmaxf(m, x[j]);
+      }
+      if (a.s > 0.f) a.s *= ta_weight(a.m, m, c2);
+      a.m = m;
+      const bool any = m > -INFINITY;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        x[j] = any ? ta_weight(x[j], m, c2) : 0.f;
+        a.s += x[j];
+      }
+    };
+    auto row_sum = [&](const float* row, float (&w)[E], float* m0) __attribute__((always_inline)) {
+      TaSum a = {-INFINITY, 0.f};
+      float x[E];
+      const bool more = v1 - v0 > BATCH;
+      if (more) load(row, 1, x);
+      clean(0, w);
+      add(a, w);
+      *m0 = a.m;
+      for (int b = 1; v0 + b * BATCH < v1; ++b) {
+        float y[E];
+        load(row, b + 1, y);
+        clean(b, x);
+        add(a, x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] = y[j];
+      }
+      return ta_join(a, c2);
+    };
+    float ml, mg = -INFINITY;  // what the first batch's weights refer to
+    const TaSum ap = row_sum(l, lw, &ml);
+    TaSum aq = {-INFINITY, 0.f};
+    if (Drawn && g) aq = row_sum(g, gw, &mg);
     if (nan) raise_status(d.status, ST_NUMERIC);
     if (lane == 0) {
       sh.wp[warp] = ap;
       sh.wq[warp] = aq;
     }
     __syncthreads();
-    if (tid == 0) {
-      TaSum a = sh.wp[0], b = sh.wq[0];
-      for (int w = 1; w < kTaWarps; ++w) {
-        a = ta_merge(a, sh.wp[w], invT);
-        b = ta_merge(b, sh.wq[w], invT);
-      }
-      sh.xp[par] = a;
-      sh.xq[par] = b;
+    float4 xs = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (warp == 0) {
+      const TaSum none = {-INFINITY, 0.f};
+      const TaSum a = ta_join(lane < kTaWarps ? sh.wp[lane] : none, c2);
+      const TaSum b = Drawn ? ta_join(lane < kTaWarps ? sh.wq[lane] : none, c2) : none;
+      xs = make_float4(a.m, a.s, b.m, b.s);
     }
-    cl.sync();
-    TaSum P = {-INFINITY, 0.f}, Q = {-INFINITY, 0.f};
-    for (int r = 0; r < NC; ++r) {
-      const TaShared* o = cl.map_shared_rank(&sh, r);
-      P = ta_merge(P, o->xp[par], invT);
-      if (Drawn) Q = ta_merge(Q, o->xq[par], invT);
-    }
-    par ^= 1;
-    // every thread forms the rows' maxima and totals with the children, in order
+    xs = exchange(xs);
+    TaSum P = ta_join({xs.x, xs.y}, c2), Q = {-INFINITY, 0.f};
+    if (Drawn) Q = ta_join({xs.z, xs.w}, c2);
+    // every thread forms the rows' maxima, one thread the totals, with the children in order
     float mp = P.m, mq = Q.m;
     for (int c = 0; c < n_child; ++c) {
-      const float a = sh.cl[c];
-      if (a == a) mp = fmaxf(mp, a);
-      if (Drawn && sh.cg[c] == sh.cg[c]) mq = fmaxf(mq, sh.cg[c]);
+      mp = fmaxf(mp, sh.cl[c]);
+      if (Drawn) mq = fmaxf(mq, sh.cg[c]);
     }
     if (mp == -INFINITY && rank == 0 && tid == 0) raise_status(d.status, ST_NUMERIC);
-    const double base_p = P.s > 0.f ? (double)P.s * ta_weight(P.m, mp, invT) : 0.0;
-    const double base_q = Drawn && Q.s > 0.f ? (double)Q.s * ta_weight(Q.m, mq, invT) : 0.0;
-    auto wl = [&](int c) { return sh.cl[c] == sh.cl[c] ? ta_weight(sh.cl[c], mp, invT) : 0.f; };
-    auto wg = [&](int c) { return sh.cg[c] == sh.cg[c] ? ta_weight(sh.cg[c], mq, invT) : 0.f; };
+    if (tid < n_child) {
+      sh.cp[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cl[tid], mp, c2);
+      if (Drawn) sh.cq[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cg[tid], mq, c2);
+    }
+    __syncthreads();
     // a token is gone once its first child was rejected, so what is left
     // after t rejections is a suffix sum over the first children from t on
     if (tid == 0) {
-      double z = base_p;
+      double z = P.s > 0.f ? (double)(P.s * ta_weight(P.m, mp, c2)) : 0.0;
       sh.sufP[n_child] = z;
-      for (int c = n_child - 1; c >= 0; --c) sh.sufP[c] = z += sh.cdup[c] ? 0.0 : (double)wl(c);
+      for (int c = n_child - 1; c >= 0; --c) sh.sufP[c] = z += sh.cdup[c] ? 0.0 : (double)sh.cp[c];
     }
     if (Drawn && tid == 32) {
-      double z = base_q;
-      sh.sufQ[n_child] = z;
+      double z = Q.s > 0.f ? (double)(Q.s * ta_weight(Q.m, mq, c2)) : 0.0;
       for (int c = n_child - 1; c >= 0; --c) {
-        z += sh.cdup[c] ? 0.0 : (double)wg(c);
-        sh.sufQ[c] = z;
-        sh.invY[c] = z > 0.0 ? (float)(1.0 / z) : 0.f;
+        z += sh.cdup[c] ? 0.0 : (double)sh.cq[c];
+        sh.invY[c] = z > 0.0 ? 1.f / (float)z : 0.f;
       }
     }
     __syncthreads();
-    const double Zp = sh.sufP[0];
-    const float invP = Zp > 0.0 ? (float)(1.0 / Zp) : 0.f;
-
-    // p_t(v) of a token after t rejections (drawn candidates), from its logits
-    auto p_after = [&](float lx, float gx, int v, int t) {
-      float p = lx == lx ? ta_weight(lx, mp, invT) * invP : 0.f;
-      float q = gx == gx ? ta_weight(gx, mq, invT) : 0.f;
-      for (int e = 0; e < t; ++e) {
-        if (sh.invZ[e] > 0.f) p = fmaxf(p - q * sh.invY[e], 0.f) * sh.invZ[e];
-        if (sh.ctok[e] == v) q = 0.f;
+    const float Zp = (float)sh.sufP[0];
+    const float invP = Zp > 0.f ? 1.f / Zp : 0.f;
+    float fp = 0.f, fq = 0.f;  // a row's weights -> p, q's weights
+    if constexpr (Drawn) {
+      // lw := p_0, gw := the draft row's weights
+      fp = ml > -INFINITY ? ta_weight(ml, mp, c2) * invP : 0.f;
+      fq = mg > -INFINITY ? ta_weight(mg, mq, c2) : 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        lw[j] *= fp;
+        gw[j] = g ? gw[j] * fq : 0.f;
       }
-      return p;
+      if (tid < n_child) sh.cp[tid] *= invP;
+      __syncthreads();
+    }
+    // p_t (and q's weights) of a later batch, from the logits
+    auto reload = [&](int b, int t, float (&p)[E], float (&q)[E]) __attribute__((always_inline)) {
+      load(l, b, p);
+      if (Drawn && g) load(g, b, q);
+      clean(b, p);
+      if (Drawn && g) clean(b, q);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        p[j] = p[j] > -INFINITY ? ta_weight(p[j], mp, c2) : 0.f;
+        if constexpr (Drawn) {
+          p[j] *= invP;
+          q[j] = g && q[j] > -INFINITY ? ta_weight(q[j], mq, c2) : 0.f;
+        }
+      }
+      if constexpr (Drawn) {
+        for (int e = 0; e < t; ++e) {
+          const float z = sh.invZ[e], y = sh.invY[e];
+          if (z > 0.f) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              p[j] = fmaxf(p[j] - q[j] * y, 0.f) * z;
+            }
+          }
+        }
+      }
     };
 
     // ---- the tests, in order
     int went = -1, t = 0;
     for (; t < n_child; ++t) {
-      const int x = sh.ctok[t];
       bool ok;
       if constexpr (Drawn) {
-        const float px = p_after(sh.cl[t], sh.cg[t], x, t);
-        const float qx = sh.cdup[t] ? 0.f : wg(t) * sh.invY[t];
-        ok = x >= 0 && sh.cu[t] * qx < px;
+        const float y = sh.invY[t];
+        const float qx = sh.cdup[t] ? 0.f : sh.cq[t] * y;
+        ok = sh.ctok[t] >= 0 && sh.cu[t] * qx < sh.cp[t];
         if (!ok) {
-          // Z_t over the slice, with the step's own q
-          float z = 0.f;
-          ta_for(l, v0, v1, [&](int v, float lx) {
-            const float gx = g[v];
-            const float p = p_after(lx, gx, v, t);
-            float q = gx == gx ? ta_weight(gx, mq, invT) * sh.invY[t] : 0.f;
-            for (int e = 0; e < t; ++e)
-              if (sh.ctok[e] == v) q = 0.f;
-            z += fmaxf(p - q, 0.f);
-          });
+          // Z_t, with the step's own q: the slice, and the children once
+          float z = 0.f, pc = 0.f;
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            z += fmaxf(lw[j] - gw[j] * y, 0.f);
+          }
+          for (int b = 1; v0 + b * BATCH < v1; ++b) {
+            float p[E], q[E];
+            reload(b, t, p, q);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              z += fmaxf(p[j] - q[j] * y, 0.f);
+            }
+          }
+          if (tid < n_child) {
+            pc = fmaxf(sh.cp[tid] - sh.cq[tid] * y, 0.f);
+            if (rank == 0 && !sh.cdup[tid]) z += pc;
+          }
           z = warp_sum(z);
           if (lane == 0) sh.wb[warp] = z;
           __syncthreads();
-          if (tid == 0) {
-            float a = 0.f;
-            for (int w = 0; w < kTaWarps; ++w) a += sh.wb[w];
-            sh.xb[par] = a;
+          if (warp == 0) z = warp_sum(lane < kTaWarps ? sh.wb[lane] : 0.f);
+          const float4 xz = exchange(make_float4(0.f, z, 0.f, 0.f));
+          const float zz = warp_sum(lane < NC ? xz.y : 0.f);
+          // nothing left: p stays (the caller's q covers all of p, up to rounding)
+          const float iz = zz > 0.f ? 1.f / zz : 0.f;
+          if (iz > 0.f) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              lw[j] = fmaxf(lw[j] - gw[j] * y, 0.f) * iz;
+            }
           }
-          cl.sync();
-          double zz = 0.0;
-          for (int r = 0; r < NC; ++r) zz += (double)cl.map_shared_rank(&sh, r)->xb[par];
-          par ^= 1;
-          __syncthreads();
-          if (tid == 0) sh.invZ[t] = zz > 0.0 ? (float)(1.0 / zz) : 0.f;
+          if (tid < n_child) {
+            if (iz > 0.f) sh.cp[tid] = pc * iz;
+            if (sh.ctok[tid] == sh.ctok[t]) sh.cq[tid] = 0.f;
+          }
+          if (tid == 0) sh.invZ[t] = iz;
           __syncthreads();
         }
       } else {
-        ok = !sh.cdup[t] && (double)sh.cu[t] * sh.sufP[t] < (double)wl(t);
+        ok = !sh.cdup[t] && (double)sh.cu[t] * sh.sufP[t] < (double)sh.cp[t];
       }
       if (ok) {
         went = sh.child[t];
@@ -315,66 +419,67 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const __grid_co
     }
 
     // ---- the last token: argmax p(v) / noise(v), lowest v on equal values
+    // (best-of candidates: the children's tokens are all gone; drawn ones:
+    // they keep what the subtractions left)
     float best = -INFINITY;
     int bi = INT_MAX;
-    const float* noise = d.noise + (size_t)s * V;
-    ta_for(l, v0, v1, [&](int v, float lx) {
-      float p;
-      if (Drawn) {
-        p = p_after(lx, g ? g[v] : -INFINITY, v, t);
-      } else {
-        p = lx == lx ? ta_weight(lx, mp, invT) : 0.f;
-        for (int e = 0; e < t; ++e)
-          if (sh.ctok[e] == v) p = 0.f;
-      }
-      const float r = p / noise[v];
+    auto offer = [&](float p, float n, int v) __attribute__((always_inline)) {
+      const float r = p / n;
       if (r > best || (r == best && v < bi)) {
         best = r;
         bi = v;
       }
-    });
+    };
+    auto draw = [&](int b, const float (&p)[E]) __attribute__((always_inline)) {
+      float n[E];
+      load(noise, b, n);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (ob > best || (ob == best && oi < bi)) {
-        best = ob;
-        bi = oi;
+      for (int j = 0; j < E; ++j) {
+        const int v = v0 + b * BATCH + j * kTaThreads + tid;
+        if (v < v1) offer(p[j], n[j], v);
+      }
+    };
+    if constexpr (!Drawn) {  // (weights against one maximum)
+      const float f = ml > -INFINITY ? ta_weight(ml, mp, c2) : 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        lw[j] *= f;
       }
     }
+    draw(0, lw);
+    for (int b = 1; v0 + b * BATCH < v1; ++b) {
+      float p[E], q[E];
+      reload(b, t, p, q);
+      draw(b, p);
+    }
+    if (Drawn && rank == 0 && tid < n_child && sh.ctok[tid] >= 0)
+      offer(sh.cp[tid], noise[sh.ctok[tid]], sh.ctok[tid]);
+    ta_best_join(best, bi);
     if (lane == 0) {
       sh.wb[warp] = best;
       sh.wi[warp] = bi;
     }
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kTaWarps; ++w)
-        if (sh.wb[w] > sh.wb[0] || (sh.wb[w] == sh.wb[0] && sh.wi[w] < sh.wi[0])) {
-          sh.wb[0] = sh.wb[w];
-          sh.wi[0] = sh.wi[w];
-        }
-      sh.xb[par] = sh.wb[0];
-      sh.xi[par] = sh.wi[0];
+    if (warp == 0) {
+      best = lane < kTaWarps ? sh.wb[lane] : -INFINITY;
+      bi = lane < kTaWarps ? sh.wi[lane] : INT_MAX;
+      ta_best_join(best, bi);
     }
-    cl.sync();
-    if (rank == 0 && tid == 0) {
-      float b = -INFINITY;
-      int x = INT_MAX;
-      for (int r = 0; r < NC; ++r) {
-        const TaShared* o = cl.map_shared_rank(&sh, r);
-        if (o->xb[par] > b || (o->xb[par] == b && o->xi[par] < x)) {
-          b = o->xb[par];
-          x = o->xi[par];
-        }
+    const float4 xb = exchange(make_float4(best, __int_as_float(bi), 0.f, 0.f));
+    if (rank == 0 && warp == 0) {
+      best = lane < NC ? xb.x : -INFINITY;
+      bi = lane < NC ? __float_as_int(xb.y) : INT_MAX;
+      ta_best_join(best, bi);
+      if (lane == 0) {
+        const int x = bi == INT_MAX ? 0 : bi;
+        const int P0 = d.base_pos ? d.base_pos[s] : 0;
+        d.out_tokens[(size_t)s * N + k] = x;
+        d.accept_len[s] = k;
+        if (d.next_anchor) d.next_anchor[s] = x;
+        if (d.commit_base) d.commit_base[s] = P0;
+        if (d.commit_count) d.commit_count[s] = k + 1;
+        if (d.update_base) d.base_pos[s] = P0 + k + 1;
       }
-      if (x == INT_MAX) x = 0;
-      const int P0 = d.base_pos ? d.base_pos[s] : 0;
-      d.out_tokens[(size_t)s * N + k] = x;
-      d.accept_len[s] = k;
-      if (d.next_anchor) d.next_anchor[s] = x;
-      if (d.commit_base) d.commit_base[s] = P0;
-      if (d.commit_count) d.commit_count[s] = k + 1;
-      if (d.update_base) d.base_pos[s] = P0 + k + 1;
     }
     for (int j = tid; rank == 0 && j < N; j += kTaThreads) {
       if (j > k) {
@@ -384,7 +489,7 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const __grid_co
     }
     break;
   }
-  cl.sync();  // peers read this CTA's shared memory until here
+  // (nothing of a peer's shared memory is touched after the last exchange's barrier)
 }
 
 // Temperature 0: the walk over the target's argmaxes, one warp per sequence.
@@ -437,10 +542,20 @@ __global__ void __launch_bounds__(32) tree_greedy_kernel(const __grid_constant__
 
 cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_t st) {
   if (d.invT == 0.f) return launch_pdl(tree_greedy_kernel, dim3(d.n_seqs), dim3(32), 0, st, d);
-  // As many CTAs per sequence as fit at once, at most 8 (the portable cluster
-  // size), each with at least 1024 vocabulary entries.
+  // As many CTAs per sequence as run at once, a CTA per SM, each with at least
+  // 1024 vocabulary entries.  Clusters of 16 are beyond the portable size and
+  // need one GPC's SMs, so only few of them run at once.
   int nc = 1;
   while (nc < 8 && d.n_seqs * nc * 2 <= num_sms && d.V >= nc * 2 * 1024) nc *= 2;
+  const bool big = nc == 8 && d.n_seqs * 32 <= num_sms && d.V >= 16 * 1024;
+  const bool brief = d.V <= (big ? 16 : nc) * kTaThreads * kTaShortE - 16 * 32;  // (slices are rounded up to 32)
+  auto* kernel = d.draft ? (brief ? tree_accept_kernel<true, kTaShortE> : tree_accept_kernel<true, kTaE>)
+                         : (brief ? tree_accept_kernel<false, kTaShortE> : tree_accept_kernel<false, kTaE>);
+  if (big) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    nc = 16;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(d.n_seqs * nc);
   cfg.blockDim = dim3(kTaThreads);
@@ -455,8 +570,7 @@ cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_
   cfg.attrs = at;
   cfg.numAttrs = 2;
   trace_kernel();
-  return d.draft ? cudaLaunchKernelEx(&cfg, tree_accept_kernel<true>, d)
-                 : cudaLaunchKernelEx(&cfg, tree_accept_kernel<false>, d);
+  return cudaLaunchKernelEx(&cfg, kernel, d);
 }
 
 // One CTA per sequence, one thread per row.
