@@ -81,6 +81,52 @@ struct KvUnit {
   }
 };
 
+// Eight elements as loaded, their magnitudes' largest bit pattern (patterns of
+// non-negative floats order as integers), and their codes.
+template <typename T>
+struct KvRow8;
+template <>
+struct KvRow8<__nv_bfloat16> {
+  uint32_t w[4];
+  static constexpr uint32_t kInf = 0x7F80u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    constexpr uint32_t M = 0x7FFF7FFFu;
+    const uint32_t m = __vimax3_u16x2(w[0] & M, w[1] & M, __vmaxu2(w[2] & M, w[3] & M));
+    return max(m >> 16, m & 0xFFFFu);
+  }
+  static __device__ __forceinline__ float value(uint32_t top) { return __uint_as_float(top << 16); }
+};
+template <>
+struct KvRow8<float> {
+  float v[8];
+  static constexpr uint32_t kInf = 0x7F800000u;
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void store(float* p) const { store8(p, v); }
+  __device__ __forceinline__ float at(int j) const { return v[j]; }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ __forceinline__ float value(uint32_t top) { return __uint_as_float(top); }
+};
+
 // The smallest e with mx <= 448 * 2^e, held to the limits.  mx = g 2^x with g
 // in [1, 2): e = x - 8, plus one when g > 1.75.  (0 and subnormals: the lower limit.)
 __device__ __forceinline__ int kv_exponent(float mx) {
@@ -106,54 +152,77 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
       u.on = false;
     }
   }
-  float v[kKvHeads][8];
+  KvRow8<T> v[kKvHeads];
+#pragma unroll
+  for (int h = 0; h < kKvHeads; ++h) v[h].zero();
   if (u.on) {
     const T* p = reinterpret_cast<const T*>(u.is_v ? l.src_v[u.layer] : l.src_k[u.layer]) +
                  (((size_t)u.s * k.rows + src) * k.nkv + u.head) * k.d + u.e0;
 #pragma unroll
     for (int h = 0; h < kKvHeads; ++h)
-      if (h < u.heads) load8(p + h * k.d, v[h]);
+      if (h < u.heads) v[h].load(p + h * k.d);
   }
   size_t row = 0;
   uint32_t hr = 0;
   u.on = u.on && kv_row(k, l.pages[u.layer], u.s, u.i, n, &row, &hr);
   row += (size_t)u.head * hr;
   void* dst = u.is_v ? l.dst_v[u.layer] : l.dst_k[u.layer];
+  if constexpr (!Q8) {
 #pragma unroll
-  for (int h = 0; h < kKvHeads; ++h, row += hr) {
-    if constexpr (!Q8) {
-      if (u.on && h < u.heads) store8(reinterpret_cast<T*>(dst) + row * k.d + u.e0, v[h]);
-    } else {
-      const bool on = u.on && h < u.heads;
-      float mx = 0.f;
-      uint32_t odd = 0;  // bit j: element j is NaN or infinite
-      if (on) {
+    for (int h = 0; h < kKvHeads; ++h, row += hr)
+      if (u.on && h < u.heads) v[h].store(reinterpret_cast<T*>(dst) + row * k.d + u.e0);
+  } else {
+    uint32_t top[kKvHeads];
+    uint32_t odd[kKvHeads];  // bit j: element j is NaN or infinite
+#pragma unroll
+    for (int h = 0; h < kKvHeads; ++h) {
+      top[h] = v[h].top();
+      odd[h] = 0u;
+      if (top[h] >= KvRow8<T>::kInf) {
+        top[h] = 0u;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float a = fabsf(v[h][j]);
-          if (a < INFINITY) mx = fmaxf(mx, a);
-          else odd |= 1u << j;
+          const float a = fabsf(v[h].at(j));
+          if (a < INFINITY) top[h] = max(top[h], __float_as_uint(a) >> (sizeof(T) == 2 ? 16 : 0));
+          else odd[h] |= 1u << j;
         }
       }
-      // (a row's threads are a half or a quarter of a warp; all its lanes take part)
-      for (int o = k.d >> 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (!on) continue;
-      if (odd) raise_status(k.status, ST_NUMERIC);
-      const int e = kv_exponent(mx);
+    }
+    // the maximum over a row's threads, a half or a quarter of a warp (two bf16 heads per shuffle)
+    if constexpr (sizeof(T) == 2) {
+      static_assert(kKvHeads % 2 == 0, "");
+#pragma unroll
+      for (int h = 0; h < kKvHeads; h += 2) {
+        uint32_t m = top[h] | top[h + 1] << 16;
+        for (int o = k.d >> 4; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        top[h] = m & 0xFFFFu;
+        top[h + 1] = m >> 16;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < kKvHeads; ++h)
+        for (int o = k.d >> 4; o > 0; o >>= 1) top[h] = max(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+    }
+    if (!u.on) return;
+#pragma unroll
+    for (int h = 0; h < kKvHeads; ++h, row += hr) {
+      if (h >= u.heads) break;
+      const int e = kv_exponent(KvRow8<T>::value(top[h]));
       const float inv = pow2_f(-e);
       uint32_t w[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[h][4 * q] * inv, v[h][4 * q + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            make_float2(v[h].at(4 * q) * inv, v[h].at(4 * q + 1) * inv), __NV_SATFINITE, __NV_E4M3);
         const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[h][4 * q + 2] * inv, v[h][4 * q + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            make_float2(v[h].at(4 * q + 2) * inv, v[h].at(4 * q + 3) * inv), __NV_SATFINITE, __NV_E4M3);
         w[q] = (uint32_t)a | ((uint32_t)b << 16);
       }
-      if (odd) {
+      if (odd[h]) {
+        raise_status(k.status, ST_NUMERIC);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if ((odd >> j) & 1u) w[j >> 2] = (w[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | (0x7Fu << (8 * (j & 3)));
+          if ((odd[h] >> j) & 1u) w[j >> 2] = (w[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | (0x7Fu << (8 * (j & 3)));
       }
       *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(dst) + row * k.d + u.e0) = make_uint2(w[0], w[1]);
       if (u.e0 == 0) (u.is_v ? l.v_exp[u.layer] : l.k_exp[u.layer])[row] = (uint8_t)(e + kKvExpBias);
