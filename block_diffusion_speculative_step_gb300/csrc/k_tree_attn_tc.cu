@@ -155,27 +155,20 @@ __host__ __device__ constexpr uint32_t tt_idesc(int M, int N, bool b_mn) {
   return F16 ? base & ~((7u << 7) | (7u << 10)) : base;
 }
 
-// 32 columns of this thread's lane, not waited for: the registers hold them
+// 16 columns of this thread's lane, not waited for: the registers hold them
 // after tmem_wait on the same array (which makes the compiler keep the order).
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
-      "}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
-                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
 }
@@ -901,30 +894,30 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (tree) w &= i == 0 ? tm[0] : i == 1 ? tm[1] : i == 2 ? tm[2] : tm[3];
             return w;
           };
-          auto hide = [&](float (&x)[32], int i) {
+          auto hide = [&](float (&x)[16], int i) {  // columns 16 i ..
             if (masked) {
-              const uint32_t w = seen(i);
+              const uint32_t w = seen(i >> 1) >> (16 * (i & 1));
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
+              for (int k = 0; k < 16; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
             }
           };
           auto chunk_max = [&]() {
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            float x[32];
+            float x[16];
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              tc::tmem_ld32(ts + 32 * i, x);
+            for (int i = 0; i < 8; ++i) {
+              tc::tmem_ld16(ts + 16 * i, x);
               hide(x, i);
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
+              for (int k = 0; k < 16; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
             }
             return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cs;
           };
           unsigned long long sa, sb;
-          auto piece = [&](float (&x)[32], uint32_t (&pk)[16], float m0) {  // weights 2^(cs x + m0), packed; their sums
+          auto piece = [&](float (&x)[16], uint32_t* pk, float m0) {  // weights 2^(cs x + m0), packed; their sums
             const unsigned long long cs2 = tt_pair(cs, cs), m2 = tt_pair(m0, m0);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
               float lo, hi;
               tt_unpair(tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), cs2, m2), lo, hi);
               lo = tt_ex2(lo);
@@ -965,14 +958,14 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
             const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
             sa = sb = tt_pair(0.f, 0.f);
-            float x[2][32];
-            tmem_ld32_async(ts, x[0]);
+            float x[2][16];
+            tmem_ld16_async(ts, x[0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // the next scores arrive while these are exponentiated
+            for (int i = 0; i < 8; ++i) {  // the next scores arrive while these are exponentiated
               tmem_wait(x[i & 1]);
-              if (i < 3) tmem_ld32_async(ts + 32 * (i + 1), x[(i + 1) & 1]);
+              if (i < 7) tmem_ld16_async(ts + 16 * (i + 1), x[(i + 1) & 1]);
               hide(x[i & 1], i);
-              piece(x[i & 1], pk[i], m0);
+              piece(x[i & 1], pk[i >> 1] + 8 * (i & 1), m0);
             }
             tt_unpair(tt_add2(sa, sb), s0, s1);
             const float sum = s0 + s1;
