@@ -85,17 +85,18 @@ struct TtCfg {
   static constexpr int RAW = kTtCH * D;                        // one e4m3 tile
   // (NT = 1: even, so that a slot always serves the same stream and its
   // issuer sees every phase of the slot's barriers)
-  static constexpr int NSK = Q8 ? (NT == 2 ? 1 : 2) : (D == 64 ? 4 : 2);
-  static constexpr int NSV = Q8 ? 2 : (D == 64 ? 4 : 2);
-  static constexpr int NRK = Q8 ? 2 : 0;                       // raw K / V slots
-  static constexpr int NRV = Q8 ? 1 : 0;
+  static constexpr int NSK = D == 64 ? 4 : 2;                  // K slots
+  static constexpr int NSV = !Q8 && D == 64 ? 4 : 2;           // V slots (16 bit)
+  static constexpr int NRV = !Q8 ? 0 : NT == 2 && D == 128 ? 1 : 2;  // raw V slots
+  static constexpr int KT = Q8 ? RAW : TILE;                   // K slot
   static constexpr int WARPS = Q8 ? 16 : 12;                   // copies, 2 issuers, queries and clearing, 2 x 4 softmax (, 4 converters)
   static constexpr int THREADS = WARPS * 32;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = NT * TILE;
-  static constexpr int V_OFF = K_OFF + NSK * TILE;
-  static constexpr int R_OFF = V_OFF + NSV * TILE;             // raw K slots, raw V slots
-  static constexpr int X_OFF = R_OFF + (NRK + NRV) * RAW;      // exchange, masks, barriers
+  static constexpr int T_OFF = K_OFF + NSK * KT;               // 8-bit: the tree's K in two e4m3 tiles
+  static constexpr int V_OFF = T_OFF + (Q8 ? 2 * RAW : 0);
+  static constexpr int R_OFF = V_OFF + NSV * TILE;             // raw V slots
+  static constexpr int X_OFF = R_OFF + NRV * RAW;              // exchange, masks, barriers
   static constexpr int X_BYTES = 16384;
   static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -105,14 +106,17 @@ struct TtShared {  // after the tiles
   float xm[2][128], xl[2][128], xu[2][128];  // a segment's stream statistics (NT = 1): maximum, sum, unit of O
   int par[DFLASH_MAX_TREE];
   uint32_t mask[4][DFLASH_MAX_TREE][4];      // the tree rows' ancestors and themselves (none: padding)
-  int ek[kTtRing], ev[kTtRing];   // chunk scale exponents (8-bit cache), by chunk counter
+  uint16_t kf[4][kTtCH];          // 8-bit: the keys' scales 2^e as bf16, by chunk counter (two V slots keep the converters at most 3 ahead)
+  int ev[kTtRing];                // 8-bit: the chunk's V exponent
   uint32_t badv[kTtRing][4];      // tree rows whose V holds a NaN or infinity, by chunk counter
-  float cmax[2][2][4];            // converters: the warps' maxima, by chunk & 1 (K, V)
-  __half2 fac[2][128];            // converters: the rows' factors
+  int cmax[2][4];                 // converters: the warps' maxima, by chunk & 1
+  __half2 fac[128];               // converters: the V rows' factors
   int s0, it0, c0, len, n0;       // the CTA's run: first item, position in it, number of positions; context of s0
   int setup;
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t rkfull[2], rkempty[2], rvfull[2], rvempty[2];
+  uint64_t rvfull[2], rvempty[2];
+  uint64_t kfr[kTtRing];          // kf and ev written
+  uint64_t tkfull[2], tkempty;    // the tree's K tiles (NT = 1: by the stream that takes them)
   uint64_t sfull[2], pdone[2], ofull[2], qraw[2], qfull[2], qfree[2];
   uint64_t mready[4];             // ancestor masks written, by buffer
   uint64_t vraw[4];               // V tiles with rows to clear, copied (at most NSV <= 4 are ahead of their P V)
@@ -148,6 +152,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, u
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, 32 of K.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Descriptor of a K-major tile with rows of 128 bytes, or of 64 with their swizzle.
+template <int ROW>
+__device__ __forceinline__ uint64_t tt_sdesc(uint32_t saddr) {
+  const uint64_t d = tc::sdesc_sw128(saddr);
+  if (ROW == 128) return d;
+  // 64-byte swizzle (type 4 in bits 61..63), groups of 8 rows 512 bytes apart
+  return (d & ~((7ull << 61) | (0x3FFFull << 32))) | (4ull << 61) | ((uint64_t)(512 >> 4) << 32);
+}
+// Byte offset of (row, 16-byte piece) in such a tile of codes.
+template <int ROW>
+__device__ __forceinline__ uint32_t tt_off8(int row, int ch) {
+  return ROW == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+}
+
 // kind::f16 with both operands fp16 (type code 0) instead of bf16 (1).
 template <bool F16>
 __host__ __device__ constexpr uint32_t tt_idesc(int M, int N, bool b_mn) {
@@ -157,7 +185,7 @@ __host__ __device__ constexpr uint32_t tt_idesc(int M, int N, bool b_mn) {
 
 // 16 columns of this thread's lane, not waited for: the registers hold them
 // after tmem_wait on the same array (which makes the compiler keep the order).
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ld_async(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
@@ -201,6 +229,12 @@ __device__ __forceinline__ unsigned long long tt_fma2(unsigned long long a, unsi
 __device__ __forceinline__ unsigned long long tt_add2(unsigned long long a, unsigned long long b) {
   unsigned long long r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ unsigned long long tt_mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -389,6 +423,32 @@ __device__ __forceinline__ float tt_finite_max(const float (&v)[8]) {
   return mx;
 }
 
+// The smallest e in [-118, 120] with mx <= 448 * 2^e (e4m3's largest value).
+__device__ __forceinline__ int tt_exp8_of(float mx) {
+  const int b = __float_as_int(mx);
+  return min(max((b >> 23) - 135 + ((b & 0x7FFFFF) > 0x600000 ? 1 : 0), -118), 120);
+}
+
+// Eight elements over 2^e as the sum of two e4m3 codes each: 4 significant
+// bits, then 4 of what is left.  A bf16's 8 are kept down to 2^-10 of the
+// largest element's power of two; below, the second code's smallest step bounds
+// the error by 2^-18 of the largest.  NaN and infinite elements give NaN.
+__device__ __forceinline__ void tt_split8(const float (&v)[8], int e, uint2& hi, uint2& lo) {
+  const float s = __int_as_float((127 - e) << 23);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 y = make_float2(v[2 * i] * s, v[2 * i + 1] * s);
+    y.x = fabsf(y.x) < INFINITY ? y.x : NAN;
+    y.y = fabsf(y.y) < INFINITY ? y.y : NAN;
+    h[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[i], __NV_E4M3)));
+    l[i] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - f.x, y.y - f.y), __NV_SATFINITE, __NV_E4M3);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
 // Eight elements scaled by 2^-e to fp16.
 __device__ __forceinline__ uint4 tt_to_half(const float (&v)[8], int e) {
   uint32_t w[4];
@@ -430,8 +490,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   uint8_t* Qs = sm + Cfg::Q_OFF;
   uint8_t* Ks = sm + Cfg::K_OFF;
   uint8_t* Vs = sm + Cfg::V_OFF;
-  uint8_t* Rk = sm + Cfg::R_OFF;
-  uint8_t* Rv = Rk + Cfg::NRK * RAW;
+  uint8_t* Ts = sm + Cfg::T_OFF;
+  uint8_t* Rv = sm + Cfg::R_OFF;
   TtShared* sh = reinterpret_cast<TtShared*>(sm + Cfg::X_OFF);
   static_assert(sizeof(TtShared) <= Cfg::X_BYTES, "exchange area");
   volatile int* abort = &sh->abort;
@@ -444,14 +504,13 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(&sh->kfull[i], Q8 ? 128 : 1);
+      tc::mbar_init(&sh->kfull[i], 1);
       tc::mbar_init(&sh->kempty[i], NT);  // the issuers that read the slot
       tc::mbar_init(&sh->vfull[i], Q8 ? 128 : 1);
       tc::mbar_init(&sh->vempty[i], NT);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sh->rkfull[i], 1);
-      tc::mbar_init(&sh->rkempty[i], 128);
+      tc::mbar_init(&sh->tkfull[i], 128);
       tc::mbar_init(&sh->rvfull[i], 1);
       tc::mbar_init(&sh->rvempty[i], 128);
       // the product's commit, and the issuer's own arrival: what the issuer has
@@ -465,6 +524,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       tc::mbar_init(&sh->qfull[i], Q8 || !p.q_tma ? 128 : 1);  // the rows' threads, or the copy
       tc::mbar_init(&sh->qfree[i], NT == 1 ? 2 : 1);           // the issuers that read the tile
     }
+    for (int i = 0; i < kTtRing; ++i) tc::mbar_init(&sh->kfr[i], 128);
+    tc::mbar_init(&sh->tkempty, NT);
     for (int i = 0; i < 4; ++i) tc::mbar_init(&sh->vraw[i], 1);
     for (int i = 0; i < 4; ++i) tc::mbar_init(&sh->mready[i], 32);
     sh->abort = 0;
@@ -533,9 +594,9 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     if (lane == 0 && !stall) {
       int nk = 0, nv = 0, nraw = 0;  // copies issued; V tiles with rows to clear
       uint32_t parts = 0u;           // which of the last V tiles those were
-      constexpr int SK = Q8 ? Cfg::NRK : NSK, SV = Q8 ? Cfg::NRV : NSV;
-      uint64_t* kf = Q8 ? sh->rkfull : sh->kfull;
-      uint64_t* ke = Q8 ? sh->rkempty : sh->kempty;
+      constexpr int SK = NSK, SV = Q8 ? Cfg::NRV : NSV;
+      uint64_t* kf = sh->kfull;
+      uint64_t* ke = sh->kempty;
       uint64_t* vf = Q8 ? sh->rvfull : sh->vfull;
       uint64_t* ve = Q8 ? sh->rvempty : sh->vempty;
       const uint64_t pol = tc::policy_evict_first();
@@ -543,7 +604,6 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         const int g = sg.it / p.n_pt;
         for (int c = sg.c0; c < sg.c1 && ok; ++c) {
           const bool tree = sg.is_tree(c);
-          if (Q8 && tree) continue;  // the converters read the tree's rows themselves
           int row = 0;
           if (!tree) {
             bool bad = false;
@@ -552,8 +612,12 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           }
           if (nk >= SK && !wait(&ke[nk % SK], (uint32_t)(nk / SK - 1))) break;
           if constexpr (Q8) {
+            if (tree) {  // the converters read the tree's rows themselves; its slot stays unused
+              tc::mbar_arrive(&kf[nk++ % SK]);
+              continue;
+            }
             tc::mbar_arrive_expect_tx(&kf[nk % SK], RAW);
-            tc::tma_load_2d(Rk + (nk % SK) * RAW, &p.kc, 0, row, &kf[nk % SK], pol);
+            tc::tma_load_2d(Ks + (nk % SK) * RAW, &p.kc, 0, row, &kf[nk % SK], pol);
           } else {
             tc::mbar_arrive_expect_tx(&kf[nk % SK], TILE);
 #pragma unroll
@@ -596,11 +660,11 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     // stream: a job's waits and commits (about 700 cycles in one thread) then
     // run beside the other stream's.
     const int t = warp - 1;
-    constexpr uint32_t idS = tt_idesc<Q8>(kTtRows, kTtCH, false);
+    constexpr uint32_t idS = tt_idesc<Q8>(kTtRows, kTtCH, false);  // (8-bit: e4m3 has fp16's type code)
     constexpr uint32_t idV = tt_idesc<Q8>(kTtRows, D, true);
     const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
     const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + (NT == 2 ? ut * TILE : 0u)),
-                   dk = tc::sdesc_sw128(tc::smem_u32(Ks)),
+                   dk = tt_sdesc<Q8 ? D : 128>(tc::smem_u32(Ks)), dt = tt_sdesc<Q8 ? D : 128>(tc::smem_u32(Ts)),
                    dv = tc::sdesc_sw128_mn(tc::smem_u32(Vs), kTtCH * 128, 1024);
     const uint32_t tm_s = __reduce_max_sync(0xffffffffu, tmem) + ut * 128u, tm_o = tm_s + 256u;
     // S of the stream's next job is issued right behind P V of the job
@@ -608,6 +672,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     Seg ss;                      // the S side's segment
     int sc = 0, c = 0;           // its chunk counter and chunk
     int s_seg = 0, q_seen = 0;   // segments walked; query loads waited for (all, in order)
+    int t_seen = 0;              // the tree's K tiles waited for
     bool s_on = ss.begin(&a, ips, sh, true);
     if (s_on) c = ss.c0;
     auto s_next = [&]() {
@@ -624,23 +689,44 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     auto wait_s = [&]() {  // the operands of the next S
       for (; q_seen <= s_seg; ++q_seen)
         if (!wait_warp(&sh->qfull[NT == 2 ? t : 0], (uint32_t)q_seen)) return;
-      wait_warp(&sh->kfull[sc % NSK], (uint32_t)(sc / NSK));
+      if (!wait_warp(&sh->kfull[sc % NSK], (uint32_t)(sc / NSK))) return;
+      if (Q8 && ss.is_tree(c)) wait_warp(&sh->tkfull[NT == 1 ? t : 0], (uint32_t)t_seen++);
     };
     auto issue_s = [&]() {
       if (!ok) return;
       const int slot = sc % NSK;
       tc::tc_fence_after();
-      const uint64_t k = dk + (uint64_t)(slot * TILE / 16);
+      const uint64_t k = dk + (uint64_t)(slot * Cfg::KT / 16);
+      const bool tree = Q8 && ss.is_tree(c);
       if (tt_elect()) {
+        if constexpr (Q8) {
+          // 32 dims a step: the queries' high codes, then what those left
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          constexpr int kBox = kTtCH * 128 / 16;  // descriptor addresses count 16 bytes
-          const uint64_t off = (uint64_t)((j >> 2) * kBox + (j & 3) * 2);
-          tc::mma_bf16(tm_s, dq + off, k + off, idS, j > 0 ? 1u : 0u);
+          for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_e4m3(tm_s, dq + (uint64_t)((j >> 1) * (kTtRows * 128 / 16) + (j & 1) * 4 + h * 2),
+                       (tree ? dt : k) + (uint64_t)(2 * j), idS, j + h > 0 ? 1u : 0u);
+          if (tree) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_e4m3(tm_s, dq + (uint64_t)((j >> 1) * (kTtRows * 128 / 16) + (j & 1) * 4 + h * 2),
+                         dt + (uint64_t)(RAW / 16 + 2 * j), idS, 1u);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            constexpr int kBox = kTtCH * 128 / 16;  // descriptor addresses count 16 bytes
+            const uint64_t off = (uint64_t)((j >> 2) * kBox + (j & 3) * 2);
+            tc::mma_bf16(tm_s, dq + off, k + off, idS, j > 0 ? 1u : 0u);
+          }
         }
         tc::mma_commit(&sh->sfull[t]);
         tc::mbar_arrive(&sh->sfull[t]);
         tc::mma_commit(&sh->kempty[slot]);
+        if (tree) tc::mma_commit(&sh->tkempty);
       }
       __syncwarp();
       s_next();
@@ -829,14 +915,23 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(r, ch)), v);
             mx = fmaxf(mx, tt_finite_max(v));
           }
-          const int e = tt_exp_of(mx);
+          const int e = tt_exp8_of(mx);
           sh->qe[seg_no & 3][NT == 2 ? t : 0][r] = (int8_t)e;
-#pragma unroll 4
-          for (int ch = 0; ch < D / 8; ++ch) {
-            uint8_t* q = qd + tt_off(r, ch);
-            float v[8];
-            load8(reinterpret_cast<const __nv_bfloat16*>(q), v);
-            *reinterpret_cast<uint4*>(q) = tt_to_half(v, e);
+          // 32 dims (64 bytes) at a time, in place: 32 codes, then the codes of what those left
+#pragma unroll 1
+          for (int j = 0; j < D / 32; ++j) {
+            uint2 h[4], l[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[8];
+              load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(r, 4 * j + c)), v);
+              tt_split8(v, e, h[c], l[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              *reinterpret_cast<uint4*>(qd + tt_off(r, 4 * j + c)) = make_uint4(h[2 * c].x, h[2 * c].y, h[2 * c + 1].x, h[2 * c + 1].y);
+              *reinterpret_cast<uint4*>(qd + tt_off(r, 4 * j + 2 + c)) = make_uint4(l[2 * c].x, l[2 * c].y, l[2 * c + 1].x, l[2 * c + 1].y);
+            }
           }
         }
         tc::fence_proxy_async_smem();
@@ -865,6 +960,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         const int nk = sg.keys(c);
         const bool masked = tree || nk < kTtCH;
         if (tree) load_mask();
+        if (Q8) wait(&sh->kfr[cc % kTtRing], (uint32_t)(cc / kTtRing));
         wait(&sh->sfull[t], (uint32_t)nj);
         if constexpr (NT == 2) {  // the streams' softmaxes take turns
           if (t == 1) tc::named_bar(7, 256);
@@ -876,7 +972,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         int dv = 0;          // exponent of the chunk's V against O's unit
         int up = 0;          // how far O's unit moves first
         if constexpr (Q8) {
-          cs = tt_scale(a.scale, sh->ek[cc % kTtRing] + sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
+          cs = tt_scale(a.scale, sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
           const int ev = sh->ev[cc % kTtRing];
           if (nj == nj0) e_run = ev;
           dv = ev - e_run;
@@ -894,37 +990,88 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (tree) w &= i == 0 ? tm[0] : i == 1 ? tm[1] : i == 2 ? tm[2] : tm[3];
             return w;
           };
-          auto hide = [&](float (&x)[16], int i) {  // columns 16 i ..
+          constexpr int W = 16, HC = Q8 ? 32 : 64, NH = kTtCH / HC;  // columns per step, per part
+          auto hide = [&](float (&x)[W], int i) {  // columns W i ..
             if (masked) {
-              const uint32_t w = seen(i >> 1) >> (16 * (i & 1));
+              const uint32_t w = seen(i * W >> 5) >> (W * i & 31);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
+              for (int k = 0; k < W; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
             }
           };
-          auto chunk_max = [&]() {
+          const uint4* kf4 = reinterpret_cast<const uint4*>(sh->kf[cc & 3]);
+          // the keys' scales of step i; read a step ahead (shared memory is busy
+          // with the products' operands, and a wait for scores holds loads back)
+          struct Scales {
+            uint32_t w[Q8 ? W / 2 : 1];
+          };
+          auto load_kf = [&](int i, Scales& f) {
+            if constexpr (Q8) {
+#pragma unroll
+              for (int k = 0; k < W / 8; ++k) {
+                const uint4 y = kf4[i * (W / 8) + k];
+                f.w[4 * k] = y.x, f.w[4 * k + 1] = y.y, f.w[4 * k + 2] = y.z, f.w[4 * k + 3] = y.w;
+              }
+            }
+          };
+          auto scale2 = [&](const Scales& f, int k) {  // the score scales of columns 2 k, 2 k + 1
+            const unsigned long long cs2 = tt_pair(cs, cs);
+            if constexpr (Q8) return tt_mul2(tt_pair(__uint_as_float(f.w[k] << 16), __uint_as_float(f.w[k] & 0xFFFF0000u)), cs2);
+            else return cs2;
+          };
+          auto cols_max = [&](int i0, int n) {  // the largest score of n steps
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            float x[16];
+            float x[W];
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              tc::tmem_ld16(ts + 16 * i, x);
+            for (int i = i0; i < i0 + n; ++i) {
+              Scales f;
+              tmem_ld_async(ts + W * i, x);
+              load_kf(i, f);
+              tmem_wait(x);
+#pragma unroll
+              for (int k = 0; k < W; k += 2) tt_unpair(tt_mul2(tt_pair(x[k], x[k + 1]), scale2(f, k / 2)), x[k], x[k + 1]);
               hide(x, i);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
+              for (int k = 0; k < W; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
             }
-            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cs;
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           };
           unsigned long long sa, sb;
-          auto piece = [&](float (&x)[16], uint32_t* pk, float m0) {  // weights 2^(cs x + m0), packed; their sums
-            const unsigned long long cs2 = tt_pair(cs, cs), m2 = tt_pair(m0, m0);
+          auto piece = [&](float (&x)[W], const Scales& f, uint32_t* pk, float m0) {  // weights 2^(scale x + m0), packed; their sums
+            const unsigned long long m2 = tt_pair(m0, m0);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < W / 2; ++k) {
               float lo, hi;
-              tt_unpair(tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), cs2, m2), lo, hi);
+              tt_unpair(tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), scale2(f, k), m2), lo, hi);
               lo = tt_ex2(lo);
               hi = tt_ex2(hi);
               if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
               else sa = tt_add2(sa, tt_pair(lo, hi));
               pk[k] = tt_pack<Q8>(lo, hi);
+            }
+          };
+          // the weights of the chunk's first n columns, packed in n / 2
+          auto rescale_p = [&](float f, int n) {
+            if (!__any_sync(0xffffffffu, f != 1.f)) return;
+#pragma unroll 1
+            for (int q = 0; q < n / 32; ++q) {
+              float w[16];
+              uint32_t v[16];
+              tc::tmem_ld16(ts + 16 * q, w);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const uint32_t u = __float_as_uint(w[k]);
+                float lo, hi;
+                if constexpr (Q8) {
+                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u));
+                  lo = y.x;
+                  hi = y.y;
+                } else {
+                  lo = __uint_as_float(u << 16);
+                  hi = __uint_as_float(u & 0xFFFF0000u);
+                }
+                v[k] = tt_pack<Q8>(lo * f, hi * f);
+              }
+              tmem_st16u(ts + 16 * q, v);
             }
           };
           auto rescale = [&](float f) {
@@ -941,47 +1088,69 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               }
             }
           };
-          float s0, s1;
-          uint32_t pk[4][16];
-          // bf16: the first chunk is tried against reference 0.  fp16 needs a
-          // reference near its maximum.
-          bool again = Q8 && (nj == nj0 || up);
-#pragma unroll 1
-          for (;;) {
-            float alpha = 1.f;
-            if (again) {
-              const float mx = chunk_max();
-              const float m_new = fmaxf(mx, m_run);
-              alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
-              rescale(up ? tt_scale(alpha, -up) : alpha);
-              m_run = m_new;
-            }
-            const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
-            sa = sb = tt_pair(0.f, 0.f);
-            float x[2][16];
-            tmem_ld16_async(ts, x[0]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // the next scores arrive while these are exponentiated
-              tmem_wait(x[i & 1]);
-              if (i < 7) tmem_ld16_async(ts + 16 * (i + 1), x[(i + 1) & 1]);
-              hide(x[i & 1], i);
-              piece(x[i & 1], pk[i >> 1] + 8 * (i & 1), m0);
-            }
-            tt_unpair(tt_add2(sa, sb), s0, s1);
-            const float sum = s0 + s1;
-            // too large for the reference; or a row's first keys, which reference 0 does not suit
-            const bool over = Q8 ? sum > 0x1p15f || (m_run == -INFINITY && sum > 0.f)
-                                 : sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
-            if (again || !__any_sync(0xffffffffu, over)) {
-              if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
-              l_run = fmaf(l_run, alpha, Q8 ? tt_scale(sum, -dv) : sum);
-              break;
-            }
-            again = true;
+          // a new reference: the largest of what it has and of n steps' scores
+          auto refer = [&](int i0, int n) {
+            const float m_new = fmaxf(cols_max(i0, n), m_run);
+            const float alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
+            m_run = m_new;
+            return alpha;
+          };
+          if (Q8 && (nj == nj0 || up)) {  // (fp16 needs a reference near a row's maximum)
+            const float alpha = refer(0, kTtCH / W);
+            rescale(up ? tt_scale(alpha, -up) : alpha);
+            l_run *= alpha;
           }
-          if constexpr (NT == 2) named_arrive(t == 0 ? 7 : 6, 256);
+          // A part of a chunk at a time, whose weights stay in registers until
+          // their sum shows that the reference suits them.  (8-bit: 16 warps'
+          // 128 registers hold a quarter; what spills goes to L2, for shared
+          // memory takes the first-level cache, and doubles the chunk's time.)
+          float sum0 = 0.f;
+#pragma unroll 1
+          for (int h = 0; h < NH; ++h) {
+            uint32_t pk[HC / 32][16];
+            float sum;
+            bool again = false;
+#pragma unroll 1
+            for (;;) {
+              const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
+              sa = sb = tt_pair(0.f, 0.f);
+              float x[2][W];
+              Scales f[2];
+              tmem_ld_async(ts + HC * h, x[0]);
+              load_kf(h * (HC / W), f[0]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_st16u(ts + 16 * i, pk[i]);
+              for (int i = 0; i < HC / W; ++i) {  // the next scores arrive while these are exponentiated
+                tmem_wait(x[i & 1]);
+                if (i + 1 < HC / W) {
+                  tmem_ld_async(ts + HC * h + W * (i + 1), x[(i + 1) & 1]);
+                  load_kf(h * (HC / W) + i + 1, f[(i + 1) & 1]);
+                }
+                hide(x[i & 1], h * (HC / W) + i);
+                piece(x[i & 1], f[i & 1], pk[i * W >> 5] + (i * W / 2 & 15), m0);
+              }
+              float s0, s1;
+              tt_unpair(tt_add2(sa, sb), s0, s1);
+              sum = s0 + s1;
+              // too large for the reference; or a row's first keys, which reference 0 does not suit
+              const bool over = Q8 ? sum > 0x1p15f || (m_run == -INFINITY && sum > 0.f)
+                                   : sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
+              if (again || !__any_sync(0xffffffffu, over)) break;
+              again = true;
+              const float alpha = refer(h * (HC / W), HC / W);
+              rescale(alpha);
+              l_run *= alpha;
+              if (h) {  // the parts before, stored already
+                sum0 *= alpha;
+                rescale_p(alpha, HC * h);
+              }
+            }
+            if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
+            sum0 += sum;
+            if (NT == 2 && h + 1 == NH) named_arrive(t == 0 ? 7 : 6, 256);
+#pragma unroll
+            for (int i = 0; i < HC / 32; ++i) tmem_st16u(ts + HC / 2 * h + 16 * i, pk[i]);
+          }
+          l_run += Q8 ? tt_scale(sum0, -dv) : sum0;
         } else if constexpr (NT == 2) {
           named_arrive(t == 0 ? 7 : 6, 256);
         }
@@ -1105,55 +1274,45 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       constexpr int LPR = D / 16;                     // lanes per code row (16 codes each)
       constexpr int RPP = 128 / LPR, NP = 128 / RPP;  // rows per pass, passes
       const int cr = ct / LPR, pc = ct % LPR;
-      int i = 0, nr = 0;                      // chunks, raw chunks
+      int i = 0, nr = 0, nt = 0;              // chunks, raw chunks, trees
       int ekn = 0, evn = 0;                   // the next chunk's exponents of row ct
       auto load_exp = [&](int c, int g) {
         bool badp = false;
         const size_t row = (size_t)km.row0(sg.s, c * kTtCH, &badp) + (size_t)g * km.head_rows() + ct;
         const bool in = ct < sg.keys(c);
-        ekn = in ? (int)__ldg(a.k_exp + row) - 127 : -1000;
+        ekn = in ? (int)__ldg(a.k_exp + row) - 127 : 0;
         evn = in ? (int)__ldg(a.v_exp + row) - 127 : -1000;
       };
-      // The largest x and y of the 128 threads, through shared memory.
-      auto group_max = [&](int& x, int& y) {
-        int(*em)[4] = reinterpret_cast<int(*)[4]>(sh->cmax[i & 1]);
-        const int wx = __reduce_max_sync(0xffffffffu, x), wy = __reduce_max_sync(0xffffffffu, y);
-        if (lane == 0) {
-          em[0][cw] = wx;
-          em[1][cw] = wy;
-        }
+      // The largest x of the 128 threads, through shared memory.
+      auto group_max = [&](int x) {
+        const int wx = __reduce_max_sync(0xffffffffu, x);
+        if (lane == 0) sh->cmax[i & 1][cw] = wx;
         tc::named_bar(5, 128);
-        x = max(max(em[0][0], em[0][1]), max(em[0][2], em[0][3]));
-        y = max(max(em[1][0], em[1][1]), max(em[1][2], em[1][3]));
+        const int* em = sh->cmax[i & 1];
+        return max(max(em[0], em[1]), max(em[2], em[3]));
       };
       for (bool on = sg.begin(&a, ips, sh); on; on = sg.next()) {
         const int g = sg.it / p.n_pt;
         int e_top = -1000;                    // the largest V exponent of the segment so far
         for (int c = sg.c0; c < sg.c1; ++c, ++i) {
-          const int nk = sg.keys(c);
+          const int nk = sg.keys(c), slot = i % NSV;
+          uint8_t* dst = Vs + slot * TILE;
           if (!sg.is_tree(c)) {
             if (c == sg.c0) load_exp(c, g);
             const int ek = ekn, ev = evn;
             if (c + 1 < sg.c1 && !sg.is_tree(c + 1)) load_exp(c + 1, g);
-            int rk = ek, rv = ev;
-            group_max(rk, rv);
-            rv = max(rv, e_top - 30);         // (O's unit never lies 2^30 above a chunk's: see the sums)
+            const int rv = max(group_max(ev), e_top - 30);  // (O's unit never lies 2^30 above a chunk's: see the sums)
             e_top = max(e_top, rv);
-            sh->fac[0][ct] = tt_half_pow2(max(ek - rk, -1000));
-            sh->fac[1][ct] = tt_half_pow2(max(ev - rv, -1000));
-            if (ct == 0) {
-              sh->ek[i % kTtRing] = rk;
-              sh->ev[i % kTtRing] = rv;
-            }
+            sh->kf[i & 3][ct] = (uint16_t)((127 + ek) << 7);
+            if (ct == 0) sh->ev[i % kTtRing] = rv;
+            tc::mbar_arrive(&sh->kfr[i % kTtRing]);
+            sh->fac[ct] = tt_half_pow2(max(ev - rv, -1000));
             tc::named_bar(5, 128);
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {     // K, then V
-              const int NR = v ? Cfg::NRV : Cfg::NRK, NS = v ? NSV : NSK, slot = i % NS, rs = nr % NR;
-              const uint8_t* raw = (v ? Rv : Rk) + rs * RAW + cr * D + pc * 16;
-              uint8_t* dst = (v ? Vs : Ks) + slot * TILE;
-              const __half2* fac = sh->fac[v] + cr;
-              if (i >= NS && !wait_warp(v ? &sh->vempty[slot] : &sh->kempty[slot], (uint32_t)(i / NS - 1))) continue;
-              if (!wait_warp(v ? &sh->rvfull[rs] : &sh->rkfull[rs], (uint32_t)(nr / NR))) continue;
+            const int rs = nr % Cfg::NRV;
+            const uint8_t* raw = Rv + rs * RAW + cr * D + pc * 16;
+            const __half2* fac = sh->fac + cr;
+            if (i >= NSV) wait_warp(&sh->vempty[slot], (uint32_t)(i / NSV - 1));
+            if (wait_warp(&sh->rvfull[rs], (uint32_t)(nr / Cfg::NRV))) {
               // all reads of the tile before the first write (one warp per
               // scheduler: nothing else hides their latency); rows past the
               // last key zero, their codes may be the NaN code
@@ -1164,6 +1323,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 code[b] = *reinterpret_cast<const uint4*>(raw + b * RPP * D);
                 f[b] = fac[b * RPP];
               }
+              tc::mbar_arrive(&sh->rvempty[rs]);
 #pragma unroll
               for (int b = 0; b < NP; ++b) {
                 const int row = b * RPP + cr;
@@ -1174,13 +1334,13 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 *reinterpret_cast<uint4*>(dst + tt_off(row, 2 * pc + 1)) = hi;
               }
               tc::fence_proxy_async_smem();
-              tc::mbar_arrive(v ? &sh->vfull[slot] : &sh->kfull[slot]);
-              tc::mbar_arrive(v ? &sh->rvempty[rs] : &sh->rkempty[rs]);
+              tc::mbar_arrive(&sh->vfull[slot]);
             }
             ++nr;
           } else {
-            // the tree's bf16 rows: one scale per chunk from their largest finite
-            // element.  Eight 16-byte pieces per thread and round, in flight at once.
+            // the tree's bf16 rows: K as two e4m3 codes with a scale per row, V
+            // with one scale per chunk from its largest finite element.  Eight
+            // 16-byte pieces per thread and round, in flight at once.
             constexpr int CPR = D / 8, RS = 128 / CPR, U = 8, RN = RS * U;  // rows per step, per round
             const size_t rstr = (size_t)a.nkv * D;
             const size_t off = ((size_t)sg.s * a.rows * a.nkv + g) * D + (size_t)(ct / CPR) * rstr + (ct % CPR) * 8;
@@ -1201,59 +1361,73 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 y[2 * k + 1] = f.y;
               }
             };
-            float mk = 0.f, mv = 0.f;
+            if (nt > 0) wait_warp(&sh->tkempty, (uint32_t)(nt - 1));
 #pragma unroll 1
-            for (int v = 1; v >= 0; --v)      // (K's first round stays in registers)
-#pragma unroll 1
-              for (int r0 = (nk - 1) / RN * RN; r0 >= 0; r0 -= RN) {
-                load_rows(v, r0);
-                float m = v ? mv : mk;
+            for (int r0 = 0; r0 < kTtCH; r0 += RN) {
+              if (r0 < nk) load_rows(0, r0);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
+              for (int u = 0; u < U; ++u) {
+                const int row = r0 + u * RS + ct / CPR;
+                int e = 0;
+                if (r0 < nk) {
                   float y[8];
                   unpack(x[u], y);
-                  m = fmaxf(m, tt_finite_max(y));
+                  float m = tt_finite_max(y);
+#pragma unroll
+                  for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                  e = tt_exp8_of(m);
+                  uint2 hi, lo;
+                  tt_split8(y, e, hi, lo);
+                  uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;
+                  *reinterpret_cast<uint2*>(q) = hi;
+                  *reinterpret_cast<uint2*>(q + RAW) = lo;
                 }
-                if (v) mv = m;
-                else mk = m;
+                if (ct % CPR == 0) sh->kf[i & 3][row] = (uint16_t)((127 + e) << 7);
               }
-            int rk = tt_exp_of(mk), rv = tt_exp_of(mv);
-            group_max(rk, rv);
-            rv = max(rv, e_top - 30);
-            if (ct == 0) {
-              sh->ek[i % kTtRing] = rk;
-              sh->ev[i % kTtRing] = rv;
             }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&sh->tkfull[NT == 1 ? i & 1 : 0]);
+            ++nt;
+            float mv = 0.f;
+#pragma unroll 1
+            for (int r0 = (nk - 1) / RN * RN; r0 >= 0; r0 -= RN) {  // (the first round stays in registers)
+              load_rows(1, r0);
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                float y[8];
+                unpack(x[u], y);
+                mv = fmaxf(mv, tt_finite_max(y));
+              }
+            }
+            const int rv = max(group_max(tt_exp_of(mv)), e_top - 30);
+            if (ct == 0) sh->ev[i % kTtRing] = rv;
+            tc::mbar_arrive(&sh->kfr[i % kTtRing]);
             if (ct < 4) sh->badv[i % kTtRing][ct] = 0u;
             tc::named_bar(5, 128);
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {
-              const int NS = v ? NSV : NSK, slot = i % NS;
-              uint8_t* dst = (v ? Vs : Ks) + slot * TILE;
-              if (i >= NS && !wait_warp(v ? &sh->vempty[slot] : &sh->kempty[slot], (uint32_t)(i / NS - 1))) continue;
+            if (i >= NSV) wait_warp(&sh->vempty[slot], (uint32_t)(i / NSV - 1));
+            if (ok) {
 #pragma unroll 1
               for (int r0 = 0; r0 < kTtCH; r0 += RN) {
-                if (v || r0 > 0) load_rows(v, r0);
+                if (r0 > 0) load_rows(1, r0);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                   const int row = r0 + u * RS + ct / CPR;
                   float y[8];
                   unpack(x[u], y);
-                  if (v) {  // a NaN or infinity must not meet a hidden row's weight 0
-                    bool odd = false;
+                  // a NaN or infinity must not meet a hidden row's weight 0
+                  bool odd = false;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                      if (!(fabsf(y[k]) < INFINITY)) {
-                        y[k] = 0.f;
-                        odd = true;
-                      }
-                    if (odd) atomicOr(&sh->badv[i % kTtRing][row >> 5], 1u << (row & 31));
-                  }
-                  *reinterpret_cast<uint4*>(dst + tt_off(row, ct % CPR)) = tt_to_half(y, v ? rv : rk);
+                  for (int k = 0; k < 8; ++k)
+                    if (!(fabsf(y[k]) < INFINITY)) {
+                      y[k] = 0.f;
+                      odd = true;
+                    }
+                  if (odd) atomicOr(&sh->badv[i % kTtRing][row >> 5], 1u << (row & 31));
+                  *reinterpret_cast<uint4*>(dst + tt_off(row, ct % CPR)) = tt_to_half(y, rv);
                 }
               }
               tc::fence_proxy_async_smem();
-              tc::mbar_arrive(v ? &sh->vfull[slot] : &sh->kfull[slot]);
+              tc::mbar_arrive(&sh->vfull[slot]);
             }
           }
         }
@@ -1381,7 +1555,7 @@ cudaError_t tt_launch(const TreeAttnDesc& a, int num_sms, cudaStream_t st) {
   const uint64_t rows = a.pages ? (uint64_t)a.pool * a.nkv * a.ps : (uint64_t)a.n_seqs * a.nkv * a.cap;
   bool okm;
   if (Q8) {
-    okm = make_tmap_u8(&p.kc, a.kc, D, rows, kTtCH) && make_tmap_u8(&p.vc, a.vc, D, rows, kTtCH);
+    okm = make_tmap_u8(&p.kc, a.kc, D, rows, kTtCH, true) && make_tmap_u8(&p.vc, a.vc, D, rows, kTtCH);
     p.kb = p.kc;
     p.vb = p.vc;
   } else {

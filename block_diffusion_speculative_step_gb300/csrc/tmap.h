@@ -49,9 +49,11 @@ inline bool make_tmap3_bf16(CUtensorMap* m, const void* base, uint64_t inner, ui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Row-major byte [rows][inner] tensor, box = inner x box_rows, no swizzle (the
-// box lands as box_rows contiguous rows of inner bytes).
-inline bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+// Row-major byte [rows][inner] tensor, box = inner x box_rows: it lands as
+// box_rows contiguous rows of inner bytes, with the swizzle of that width
+// (inner = 64 or 128) when asked for.
+inline bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                         bool swizzle = false) {
   auto fn = tmap_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, rows};
@@ -59,7 +61,9 @@ inline bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint6
   cuuint32_t box[2] = {(cuuint32_t)inner, box_rows};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
