@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       uint32_t acc0 = 0u;  // the stream's first P V of the segment starts its accumulator
       for (int x = sg.c0; x < sg.c1 && ok; ++x, ++vc) {
         if (NT == 1 && (uint32_t)(vc & 1) != ut) continue;
-        const int slot = vc % NSV;
+        const int slot = vc % NSV, nk = sg.keys(x);
         if (!wait_warp(&sh->vfull[slot], (uint32_t)(vc / NSV))) break;
         // waited for early, so that S follows P V in the tensor pipe without a
         // gap; not across segments, whose query load may still take a while
@@ -753,8 +753,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         const uint64_t v = dv + (uint64_t)(slot * TILE / 16);
         if (tt_elect()) {
 #pragma unroll
-          for (int j = 0; j < kTtCH / 16; ++j)
-            mma_ts(tm_o, tm_s + 8 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+          for (int j = 0; j < kTtCH / 16; ++j)  // (16 keys a step; of a short chunk only those that hold some)
+            if (16 * j < nk) mma_ts(tm_o, tm_s + 8 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
           // the stream's last job of the segment: its output is complete
           if (last) {
             tc::mma_commit(&sh->ofull[t]);
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
           }
 #pragma unroll 4
-          for (int i = nk * CPR + lane; i < kTtCH * CPR; i += 32) *at(i) = make_uint4(0, 0, 0, 0);
+          for (int i = nk * CPR + lane; i < (nk + 15 & ~15) * CPR; i += 32) *at(i) = make_uint4(0, 0, 0, 0);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh->vfull[slot]);
@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (tree) w &= i == 0 ? tm[0] : i == 1 ? tm[1] : i == 2 ? tm[2] : tm[3];
             return w;
           };
-          constexpr int W = 16, HC = Q8 ? 32 : 64, NH = kTtCH / HC;  // columns per step, per part
+          constexpr int W = 16, HC = Q8 ? 32 : 64;  // columns per step, per part
           auto hide = [&](float (&x)[W], int i) {  // columns W i ..
             if (masked) {
               const uint32_t w = seen(i * W >> 5) >> (W * i & 31);
@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return alpha;
           };
           if (Q8 && (nj == nj0 || up)) {  // (fp16 needs a reference near a row's maximum)
-            const float alpha = refer(0, kTtCH / W);
+            const float alpha = refer(0, (nk + W - 1) / W);
             rescale(up ? tt_scale(alpha, -up) : alpha);
             l_run *= alpha;
           }
@@ -1104,9 +1104,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           // their sum shows that the reference suits them.  (8-bit: 16 warps'
           // 128 registers hold a quarter; what spills goes to L2, for shared
           // memory takes the first-level cache, and doubles the chunk's time.)
+          const int np = (nk + HC - 1) / HC;  // parts that hold keys
           float sum0 = 0.f;
 #pragma unroll 1
-          for (int h = 0; h < NH; ++h) {
+          for (int h = 0; h < np; ++h) {
             uint32_t pk[HC / 32][16];
             float sum;
             bool again = false;
@@ -1146,7 +1147,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
             if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
-            if (NT == 2 && h + 1 == NH) named_arrive(t == 0 ? 7 : 6, 256);
+            if (NT == 2 && h + 1 == (Q8 ? 1 : np)) named_arrive(t == 0 ? 7 : 6, 256);
 #pragma unroll
             for (int i = 0; i < HC / 32; ++i) tmem_st16u(ts + HC / 2 * h + 16 * i, pk[i]);
           }
@@ -1320,12 +1321,14 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               __half2 f[NP];
 #pragma unroll
               for (int b = 0; b < NP; ++b) {
+                if (b * RPP >= nk) break;  // (the product reads 16 keys at a time, a pass's rows or half of them)
                 code[b] = *reinterpret_cast<const uint4*>(raw + b * RPP * D);
                 f[b] = fac[b * RPP];
               }
               tc::mbar_arrive(&sh->rvempty[rs]);
 #pragma unroll
               for (int b = 0; b < NP; ++b) {
+                if (b * RPP >= nk) break;
                 const int row = b * RPP + cr;
                 uint4 lo, hi;
                 if (row >= nk) code[b] = make_uint4(0, 0, 0, 0);
@@ -1363,25 +1366,22 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             };
             if (nt > 0) wait_warp(&sh->tkempty, (uint32_t)(nt - 1));
 #pragma unroll 1
-            for (int r0 = 0; r0 < kTtCH; r0 += RN) {
-              if (r0 < nk) load_rows(0, r0);
+            for (int r0 = 0; r0 < nk; r0 += RN) {
+              load_rows(0, r0);
 #pragma unroll
               for (int u = 0; u < U; ++u) {
                 const int row = r0 + u * RS + ct / CPR;
-                int e = 0;
-                if (r0 < nk) {
-                  float y[8];
-                  unpack(x[u], y);
-                  float m = tt_finite_max(y);
+                float y[8];
+                unpack(x[u], y);
+                float m = tt_finite_max(y);
 #pragma unroll
-                  for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                  e = tt_exp8_of(m);
-                  uint2 hi, lo;
-                  tt_split8(y, e, hi, lo);
-                  uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;
-                  *reinterpret_cast<uint2*>(q) = hi;
-                  *reinterpret_cast<uint2*>(q + RAW) = lo;
-                }
+                for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int e = tt_exp8_of(m);
+                uint2 hi, lo;
+                tt_split8(y, e, hi, lo);
+                uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;
+                *reinterpret_cast<uint2*>(q) = hi;
+                *reinterpret_cast<uint2*>(q + RAW) = lo;
                 if (ct % CPR == 0) sh->kf[i & 3][row] = (uint16_t)((127 + e) << 7);
               }
             }
@@ -1407,7 +1407,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (i >= NSV) wait_warp(&sh->vempty[slot], (uint32_t)(i / NSV - 1));
             if (ok) {
 #pragma unroll 1
-              for (int r0 = 0; r0 < kTtCH; r0 += RN) {
+              for (int r0 = 0; r0 < nk; r0 += RN) {
                 if (r0 > 0) load_rows(1, r0);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {

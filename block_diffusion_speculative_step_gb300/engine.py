@@ -9,8 +9,14 @@ no host synchronisation:
                                               commit = (base_pos, k + 1), base_pos += k + 1
   fuse_context(feats, commit)              -> draft context K/V of the committed positions
 
-Torch here only allocates device memory and provides the stream; every step
-of the cycle runs in libdflash kernels.
+A tree cycle (tree_cycle) verifies several candidates a position instead of
+one: the draft's candidates become a tree of rows, the target runs over the
+tree, the walk down the tree accepts a path, and only that path's keys and
+values are committed to the target cache.
+
+Torch here only allocates device memory, provides the stream and puts rows in
+order (tokens of a tree forward, the accepted rows' tap features); every
+other step of a cycle runs in libdflash kernels.
 """
 from __future__ import annotations
 
@@ -43,13 +49,20 @@ class Caches:
     tv: list
     dk: list  # draft context K per layer [S][nkv][dcap][d]
     dv: list
+    tke: list  # 8-bit target caches: scale exponents [S][nkv][cap]
+    tve: list
 
 
 class Engine:
-    """One target + draft pair resident on the GPU, n_seqs sequences."""
+    """One target + draft pair resident on the GPU, n_seqs sequences.
+
+    kv8: the target's caches hold 8-bit e4m3 rows with a power-of-two scale
+    per (slot, KV head), half the bytes of bf16.  Target forwards then run as
+    tree forwards (a chain where no tree is given) whose keys and values are
+    committed by dflash_kv_write."""
 
     def __init__(self, w: synth.Workload, model: dict, n_seqs: int, cap: int, device="cuda",
-                 prefill_chunk: int = 256, fuse_rows: int = 0):
+                 prefill_chunk: int = 256, fuse_rows: int = 0, kv8: bool = False):
         self.w = w
         self.m = model
         self.S = n_seqs
@@ -57,7 +70,8 @@ class Engine:
         self.cap = cap
         self.dev = torch.device(device)
         self.dt = synth.torch_dtype(w)
-        self.chunk = prefill_chunk
+        self.chunk = min(prefill_chunk, D.DFLASH_MAX_TREE) if kv8 else prefill_chunk
+        self.kv8 = kv8
         self.F = len(w.taps)
         tdims = w.target
         self.ddims = dims_of(w, w.draft)
@@ -70,11 +84,15 @@ class Engine:
         # caches
         dcap = w.window if w.window > 0 else cap
         self.dcap = dcap
+        n_tl = tdims.layers if self.has_target else 0
+        tdt = torch.uint8 if kv8 else self.dt
         self.caches = Caches(
-            tk=[z(S, tdims.n_kv, cap, tdims.head_dim) for _ in range(tdims.layers)] if self.has_target else [],
-            tv=[z(S, tdims.n_kv, cap, tdims.head_dim) for _ in range(tdims.layers)] if self.has_target else [],
+            tk=[z(S, tdims.n_kv, cap, tdims.head_dim, dt=tdt) for _ in range(n_tl)],
+            tv=[z(S, tdims.n_kv, cap, tdims.head_dim, dt=tdt) for _ in range(n_tl)],
             dk=[z(S, w.draft.n_kv, dcap, w.draft.head_dim) for _ in range(w.draft.layers)],
-            dv=[z(S, w.draft.n_kv, dcap, w.draft.head_dim) for _ in range(w.draft.layers)])
+            dv=[z(S, w.draft.n_kv, dcap, w.draft.head_dim) for _ in range(w.draft.layers)],
+            tke=[z(S, tdims.n_kv, cap, dt=tdt) for _ in range(n_tl if kv8 else 0)],
+            tve=[z(S, tdims.n_kv, cap, dt=tdt) for _ in range(n_tl if kv8 else 0)])
         # RoPE tables (positions up to cap)
         self.rope_max = cap + B
         self.rope_t = z(self.rope_max, tdims.head_dim // 2, 2, dt=torch.float32) if self.has_target else None
@@ -97,6 +115,10 @@ class Engine:
         # DFlash 2 draft convolutions: on when the workload has them (the
         # weights sit in the draft layers as conv_w1 / conv_w2)
         self.conv_rank = w.conv_rank
+        self.tree = None  # (parent, rank) of the tree template, once set_tree was called
+        self.tree_rows = 0
+        if kv8 and self.has_target:
+            self._tree_buffers(max(B, self.chunk))
         self.ws_bytes = 0
         self._size_workspace(fuse_rows)
         st = torch.cuda.current_stream()
@@ -151,6 +173,8 @@ class Engine:
         else:
             k, v, cap, win = self.caches.dk[j], self.caches.dv[j], self.dcap, self.w.window
         kv = D.dflash_kv(_ptr(k), _ptr(v), cap, win)
+        if kind == "t" and self.kv8:
+            kv.k_exp, kv.v_exp = _ptr(self.caches.tke[j]), _ptr(self.caches.tve[j])
         if kind in self.paging:
             table, ps, mp, pool = self.paging[kind]
             kv.pages, kv.page_size, kv.max_pages, kv.pool_pages = _ptr(table), ps, mp, pool
@@ -180,11 +204,17 @@ class Engine:
                     p = torch.zeros(pool, nkv, page_size, d, dtype=c.dtype, device=self.dev)
                     p[idx] = pages
                     lst[j] = p
+            for lst in (self.caches.tke, self.caches.tve) if kind == "t" else ():
+                for j, c in enumerate(lst):
+                    pages = c.view(S, nkv, mp, page_size).permute(0, 2, 1, 3).reshape(S * mp, nkv, page_size)
+                    p = torch.zeros(pool, nkv, page_size, dtype=c.dtype, device=self.dev)
+                    p[idx] = pages
+                    lst[j] = p
             self.paging[kind] = (table.to(self.dev), page_size, mp, pool)
 
     def unpaged_caches(self):
         """The caches' contents in the contiguous layout [S][n_kv][cap][d]
-        (copies when paged)."""
+        (copies when paged; the codes of 8-bit ones)."""
         out = {}
         for kind, ks, vs, cap in (("t", self.caches.tk, self.caches.tv, self.cap),
                                   ("d", self.caches.dk, self.caches.dv, self.dcap)):
@@ -262,6 +292,166 @@ class Engine:
         a.h = _ptr(h)
         return a
 
+    # ------------------------------------------------------------- tree calls
+
+    def _tree_buffers(self, rows: int):
+        """Buffers of target forwards over up to `rows` tree rows a sequence."""
+        if rows <= self.tree_rows:
+            return
+        t, S = self.w.target, self.S
+        self.tree_rows = rows
+        new = lambda *shape, dt=torch.int32: torch.zeros(shape, dtype=dt, device=self.dev)
+        self.tkb = [new(S * rows, t.n_kv, t.head_dim, dt=self.dt) for _ in range(t.layers)]
+        self.tvb = [new(S * rows, t.n_kv, t.head_dim, dt=self.dt) for _ in range(t.layers)]
+        self.steps = torch.arange(rows, dtype=torch.int32, device=self.dev)
+
+    def tree_layer_args(self, li: int, rows: int, h, pos, parent=None, tap=None, tap_offset=0, base_pos=None):
+        a = self.target_layer_args(li, rows, h, tap, tap_offset, base_pos)
+        a.attn_mode = D.DFLASH_ATTN_TREE
+        a.tree_parent, a.tree_pos = _ptr(parent), _ptr(pos)
+        a.out_kb, a.out_vb = _ptr(self.tkb[li]), _ptr(self.tvb[li])
+        return a
+
+    def kv_write_args(self, j0: int, n: int, rows: int, base_pos, valid=None, row_index=None):
+        """Commits rows of the target's layers [j0, j0 + n), n <= DFLASH_KV_MAX_LAYERS."""
+        a = D.dflash_kv_write_args()
+        a.dims = self.tdims
+        a.n_layers = n
+        kb = (C.c_void_p * n)(*[_ptr(x) for x in self.tkb[j0:j0 + n]])
+        vb = (C.c_void_p * n)(*[_ptr(x) for x in self.tvb[j0:j0 + n]])
+        kv = (D.dflash_kv * n)(*[self._kv("t", j) for j in range(j0, j0 + n)])
+        a._keep = (kb, vb, kv)  # host arrays, read during the call
+        a.kb, a.vb, a.kv_layers = (C.cast(x, C.c_void_p) for x in a._keep)
+        a.n_seqs, a.rows = self.S, rows
+        a.base_pos, a.valid, a.row_index = _ptr(base_pos), _ptr(valid), _ptr(row_index)
+        return a
+
+    def tree_forward(self, rows: int, tokens, pos, parent=None, taps=True, base_pos=None):
+        """Embed tokens [S][rows] and run every target layer over them as a
+        tree (parent [S][rows]; None: a chain) at the positions pos [S*rows];
+        the caches are read only.  Keys and values go to self.tkb / self.tvb,
+        tap features to self.feats."""
+        self._tree_buffers(rows)
+        e = self.embed_args(self.tdims, 1, self.h, tokens)
+        e.n_seqs = self.S * rows
+        D.dflash_embed(e, self.ws_ptr, self.ws_bytes)
+        for li in range(self.w.target.layers):
+            tapped = taps and li in self.w.taps
+            off = self.w.taps.index(li) * self.w.target.hidden if tapped else 0
+            D.dflash_decoder_layer_forward(
+                self.tree_layer_args(li, rows, self.h, pos, parent, self.feats if tapped else None, off, base_pos),
+                self.ws_ptr, self.ws_bytes)
+
+    def tree_commit(self, rows: int, base_pos, valid=None, row_index=None):
+        """Write the last tree forward's rows (row_index [S][rows]: those, in
+        that order) to the target caches from position base_pos on."""
+        L = self.w.target.layers
+        for j in range(0, L, D.DFLASH_KV_MAX_LAYERS):
+            n = min(D.DFLASH_KV_MAX_LAYERS, L - j)
+            D.dflash_kv_write(self.kv_write_args(j, n, rows, base_pos, valid, row_index), self.ws_ptr, self.ws_bytes)
+
+    def set_tree(self, parent, rank):
+        """The template of tree_cycle: node i >= 1 hangs below node parent[i]
+        and takes candidate rank[i] of its position (0: the best); parent[0]
+        = -1 is the anchor.  Candidates beyond the first need the workload's
+        path selector, which lists path_topk of them."""
+        n = len(parent)
+        assert n == len(rank) and 1 <= n <= D.DFLASH_MAX_TREE and parent[0] == -1
+        S = self.S
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=self.dev)
+        self.tree = tuple(torch.tensor(x, dtype=torch.int32, device=self.dev) for x in (parent, rank))
+        self.t_parent, self.t_tokens, self.t_pos = i32(S, n), i32(S, n), i32(S * n)
+        self.t_path, self.t_out, self.t_argmax = i32(S, n), i32(S, n), i32(S, n)
+        self.t_zero = i32(S, n)
+        self.t_dummy = i32(S), i32(S, n)
+        if self.w.path_topk:
+            self.t_cand = i32(S, self.B - 1, self.w.path_topk)
+        self._tree_buffers(n)
+        if self.h.shape[0] < S * n:
+            self.h = torch.zeros(S * n, self.h.shape[1], dtype=torch.float32, device=self.dev)
+            self.feats = torch.zeros(S * n, *self.feats.shape[1:], dtype=self.dt, device=self.dev)
+        need = max(self.ws_bytes,
+                   D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, self.tree_layer_args(0, n, self.h, self.t_pos,
+                                                                                    self.t_parent)),
+                   D.dflash_workspace_bytes(D.DFLASH_OP_FUSE, self.fuse_args(n, self.feats, self.base_pos, None)),
+                   D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.tree_verify_args(0, min(S, self._verify_seqs()))))
+        if need > self.ws_bytes:
+            self._new_workspace(int(need))
+
+    def _verify_seqs(self) -> int:
+        """Sequences per verification call, which takes 1024 rows at most."""
+        return max(1, 1024 // self.tree[0].numel())
+
+    def tree_verify_args(self, s0: int, n: int, logits=None):
+        """The target's argmax (and logits) at the tree rows of sequences [s0, s0 + n)."""
+        N = self.tree[0].numel()
+        a = self.verify_args(N, self.h[s0 * N:], self.t_zero[s0:], None if logits is None else logits[s0 * N:],
+                             update=False)
+        a.n_seqs = n
+        a.argmax, a.margin = _ptr(self.t_argmax[s0:]), 0
+        a.accept_len, a.out_tokens = _ptr(self.t_dummy[0]), _ptr(self.t_dummy[1])  # (of a chain: not used)
+        return a
+
+    def tree_cycle(self, T: float = 0.0, u=None, noise=None):
+        """One draft-and-verify cycle over the tree set by set_tree.  T = 0
+        accepts the target's greedy tokens; T > 0 the draft's candidates by
+        the random numbers u [S][rows] in [0, 1) and noise [S][V] (draws of
+        an Exp(1) distribution), which leaves every token distributed as the
+        target's softmax at temperature T."""
+        parent, rank = self.tree
+        S, N, V = self.S, parent.numel(), self.w.vocab
+        a = self.draft_args()
+        cand, topk = self.drafts, 1
+        if self.w.path_topk:
+            cand, topk = self.t_cand, self.w.path_topk
+            a.path_cand_out = _ptr(cand)
+        D.dflash_draft_block(a, self.ws_ptr, self.ws_bytes)
+        b = D.dflash_tree_build_args()
+        b.n_seqs, b.rows, b.levels, b.topk = S, N, self.B - 1, topk
+        b.parent, b.rank, b.cand = _ptr(parent), _ptr(rank), _ptr(cand)
+        b.anchor, b.base_pos = _ptr(self.anchor), _ptr(self.base_pos)
+        b.parent_out, b.tokens_out, b.pos_out = _ptr(self.t_parent), _ptr(self.t_tokens), _ptr(self.t_pos)
+        D.dflash_tree_build(b, self.ws_ptr, self.ws_bytes)
+        self.tree_forward(N, self.t_tokens, self.t_pos, self.t_parent)
+        if T > 0 and (getattr(self, "t_logits", None) is None or self.t_logits.shape[0] < S * N):
+            self.t_logits = torch.zeros(S * N, V, dtype=torch.float32, device=self.dev)
+        step = self._verify_seqs()
+        for s0 in range(0, S, step):
+            D.dflash_verify_accept(self.tree_verify_args(s0, min(step, S - s0), self.t_logits if T > 0 else None),
+                                   self.ws_ptr, self.ws_bytes)
+        c = D.dflash_tree_accept_args()
+        c.dims = self.tdims
+        c.n_seqs, c.rows, c.temperature = S, N, T
+        c.parent, c.tokens = _ptr(self.t_parent), _ptr(self.t_tokens)
+        if T > 0:
+            c.target_logits, c.u, c.noise = _ptr(self.t_logits), _ptr(u), _ptr(noise)
+        else:
+            c.target_argmax = _ptr(self.t_argmax)
+        c.base_pos, c.update_base_pos = _ptr(self.base_pos), 1
+        c.accept_len, c.path, c.out_tokens = _ptr(self.accept_len), _ptr(self.t_path), _ptr(self.t_out)
+        c.next_anchor = _ptr(self.anchor)
+        c.commit_base, c.commit_count = _ptr(self.commit_base), _ptr(self.commit_count)
+        D.dflash_tree_accept(c, self.ws_ptr, self.ws_bytes)
+        self.tree_commit(N, self.commit_base, self.commit_count, self.t_path)
+        # the accepted rows' features, in order (rows past the path: not injected)
+        rows = min(N, self.B)
+        f = self.feats[:S * N].view(S, N, -1)
+        idx = self.t_path[:, :rows].clamp(min=0).long()[:, :, None].expand(S, rows, f.shape[2])
+        self.fuse_with(f.gather(1, idx).view(S * rows, *self.feats.shape[1:]), rows, self.commit_base, self.commit_count)
+
+    def tree_generate(self, prompts: torch.Tensor, n_new: int):
+        """Greedy generation by tree cycles: the tokens and, per cycle, the accepted counts."""
+        self.prefill(prompts)
+        outs = [[int(a)] for a in self.anchor.cpu()]
+        accepts = []
+        while min(len(o) for o in outs) < n_new:
+            self.tree_cycle()
+            k, toks = self.accept_len.cpu(), self.t_out.cpu()
+            accepts.append(k.clone())
+            for s in range(self.S):
+                outs[s].extend(int(t) for t in toks[s, :int(k[s]) + 1])
+        return torch.tensor([o[:n_new] for o in outs], dtype=torch.int32), torch.stack(accepts, 1)
+
     def _size_workspace(self, fuse_rows: int):
         need = D.dflash_workspace_bytes(D.DFLASH_OP_DRAFT, self.draft_args())
         rows_list = [self.B, 1, min(self.chunk, self.cap)]
@@ -272,9 +462,14 @@ class Engine:
             need = max(need, D.dflash_workspace_bytes(D.DFLASH_OP_FUSE, self.fuse_args(rows, self.feats,
                                                                                       self.base_pos, None)))
             if self.has_target:
-                need = max(need, D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, self.target_layer_args(0, rows, self.h)))
+                layer = (self.tree_layer_args(0, rows, self.h, self.h) if self.kv8 else
+                         self.target_layer_args(0, rows, self.h))
+                need = max(need, D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, layer))
                 need = max(need, D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.verify_args(rows, self.h)))
-        self.ws_bytes = int(need)
+        self._new_workspace(int(need))
+
+    def _new_workspace(self, n: int):
+        self.ws_bytes = n
         self.ws = torch.zeros(self.ws_bytes + 256, dtype=torch.uint8, device=self.dev)
         self.ws_ptr = (self.ws.data_ptr() + 255) & ~255
         D.dflash_workspace_init(self.ws_ptr, self.ws_bytes)
@@ -288,6 +483,13 @@ class Engine:
         """Embed the rows and run every target layer causally; keeps tap
         features (rows x F x H) in self.feats."""
         t = self.w.target
+        if self.kv8:  # a chain, committed after the forward
+            base = self.base_pos if base_pos is None else base_pos
+            tokens = first.view(self.S, 1) if rows == 1 else torch.cat([first.view(self.S, 1), rest], 1)
+            pos = (base[:, None] + self.steps[:rows]).view(-1)
+            self.tree_forward(rows, tokens.contiguous(), pos, None, taps, base)
+            self.tree_commit(rows, base)
+            return
         D.dflash_embed(self.embed_args(self.tdims, rows, self.h, first, rest), self.ws_ptr, self.ws_bytes)
         for li in range(t.layers):
             tap = None
