@@ -906,33 +906,34 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
 #pragma unroll 8
           for (int ch = 0; ch < D / 8; ++ch)
             *reinterpret_cast<uint4*>(qd + tt_off(r, ch)) = has_row ? __ldg(src + ch) : make_uint4(0, 0, 0, 0);
+          __syncwarp();
         }
         if constexpr (Q8) {
-          float mx = 0.f;
-#pragma unroll 4
-          for (int ch = 0; ch < D / 8; ++ch) {
-            float v[8];
-            load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(r, ch)), v);
-            mx = fmaxf(mx, tt_finite_max(v));
-          }
-          const int e = tt_exp8_of(mx);
-          sh->qe[seg_no & 3][NT == 2 ? t : 0][r] = (int8_t)e;
-          // 32 dims (64 bytes) at a time, in place: 32 codes, then the codes of what those left
+          // A warp's 32 rows, D / 16 lanes to a row, 16 dims to a lane: two
+          // codes each, in place.  Of every 32 dims (64 bytes) the first half
+          // takes the codes, the second the codes of what those left.
+          constexpr int LR = D / 16, RW = 32 / LR;
+          const int wr = (warp & 3) * 32, jl = (lane % LR) >> 1, hl = lane & 1;
 #pragma unroll 1
-          for (int j = 0; j < D / 32; ++j) {
-            uint2 h[4], l[4];
+          for (int r0 = wr; r0 < wr + 32 && qv - lane + (r0 - wr) < nqv; r0 += RW) {
+            const int row = r0 + lane / LR;
+            float v[2][8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[8];
-              load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(r, 4 * j + c)), v);
-              tt_split8(v, e, h[c], l[c]);
-            }
+            for (int c = 0; c < 2; ++c)
+              load8(reinterpret_cast<const __nv_bfloat16*>(qd + tt_off(row, 4 * jl + 2 * hl + c)), v[c]);
+            float mx = fmaxf(tt_finite_max(v[0]), tt_finite_max(v[1]));
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              *reinterpret_cast<uint4*>(qd + tt_off(r, 4 * j + c)) = make_uint4(h[2 * c].x, h[2 * c].y, h[2 * c + 1].x, h[2 * c + 1].y);
-              *reinterpret_cast<uint4*>(qd + tt_off(r, 4 * j + 2 + c)) = make_uint4(l[2 * c].x, l[2 * c].y, l[2 * c + 1].x, l[2 * c + 1].y);
-            }
+            for (int o = LR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = tt_exp8_of(mx);
+            if (lane % LR == 0) sh->qe[seg_no & 3][NT == 2 ? t : 0][row] = (int8_t)e;
+            uint2 h[2], l[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tt_split8(v[c], e, h[c], l[c]);
+            __syncwarp();  // the row has been read
+            *reinterpret_cast<uint4*>(qd + tt_off(row, 4 * jl + hl)) = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+            *reinterpret_cast<uint4*>(qd + tt_off(row, 4 * jl + 2 + hl)) = make_uint4(l[0].x, l[0].y, l[1].x, l[1].y);
           }
+          __syncwarp();
         }
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&sh->qfull[NT == 2 ? t : 0]);
@@ -1351,7 +1352,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             auto load_rows = [&](int v, int r0) {
               const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(v ? a.vb : a.kb) + off;
 #pragma unroll
-              for (int u = 0; u < U; ++u)
+              for (int u = 0; u < U; ++u)  // (zeros past the last row)
                 x[u] = r0 + u * RS + ct / CPR < nk ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(r0 + u * RS) * rstr))
                                                    : make_uint4(0, 0, 0, 0);
             };
@@ -1365,11 +1366,13 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               }
             };
             if (nt > 0) wait_warp(&sh->tkempty, (uint32_t)(nt - 1));
+            if (ct >= nk) sh->kf[i & 3][ct] = 127 << 7;  // (a hidden key: any finite scale, for -inf times it)
 #pragma unroll 1
             for (int r0 = 0; r0 < nk; r0 += RN) {
               load_rows(0, r0);
 #pragma unroll
               for (int u = 0; u < U; ++u) {
+                if (r0 + u * RS >= nk) break;
                 const int row = r0 + u * RS + ct / CPR;
                 float y[8];
                 unpack(x[u], y);
@@ -1382,7 +1385,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;
                 *reinterpret_cast<uint2*>(q) = hi;
                 *reinterpret_cast<uint2*>(q + RAW) = lo;
-                if (ct % CPR == 0) sh->kf[i & 3][row] = (uint16_t)((127 + e) << 7);
+                if (ct % CPR == 0 && row < nk) sh->kf[i & 3][row] = (uint16_t)((127 + e) << 7);
               }
             }
             tc::fence_proxy_async_smem();
@@ -1394,6 +1397,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               load_rows(1, r0);
 #pragma unroll
               for (int u = 0; u < U; ++u) {
+                if (r0 + u * RS >= nk) break;
                 float y[8];
                 unpack(x[u], y);
                 mv = fmaxf(mv, tt_finite_max(y));
@@ -1412,6 +1416,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                   const int row = r0 + u * RS + ct / CPR;
+                  if (r0 + u * RS >= (nk + 15 & ~15)) break;  // (the product reads 16 keys at a time)
                   float y[8];
                   unpack(x[u], y);
                   // a NaN or infinity must not meet a hidden row's weight 0
