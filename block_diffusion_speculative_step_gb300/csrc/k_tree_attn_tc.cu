@@ -20,32 +20,48 @@
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
 // With NT = 2 the streams' softmaxes take turns, so that one stream's products
 // run beside the other's softmax (left alone both fall in step and wait for
-// their products together).  The reference m stays while the weights' sum
+// their products together: 196 us instead of 162 for 32 sequences x 64 rows,
+// 8k, bf16; 8-bit, whose softmax is longer, they overlap from the second
+// quarter of a chunk on, 259 us against 291 in strict turns).  The reference m stays while the weights' sum
 // suits the 16-bit type, so the usual chunk needs no maximum and no rescaling
 // of O: bf16, which has fp32's exponents, starts at m = 0 and takes sums of
 // 2^-60 .. 2^60; fp16 (8-bit cache) starts at the first chunk's maximum and
 // takes sums up to 2^15.  Otherwise the chunk is done again with its maximum:
 // the scores stay until the sum is known.
 //
-// Eight softmax warps with many registers (scores in flight while others are
-// exponentiated) measured faster than sixteen: two threads a row spend more
-// instructions on exchanging maxima and votes than they save.
+// Roles: warp 0 K/V copies; warps 1, 2 the products of stream 0, 1 (a job's
+// waits and commits take about 600 cycles of one thread, so each stream has a
+// warp); warp 3 query copies, the tree's ancestor masks, rows of V to clear;
+// warps 4..11 the softmax, a query vector per thread; 8-bit: warps 12..15
+// convert.  Eight softmax warps with many registers measured faster than
+// sixteen: two threads a row spend more instructions on exchanging maxima and
+// votes than they save.  Registers are what the softmax is short of: shared
+// memory leaves the first-level cache next to nothing, so a spilled value is
+// an L2 access (a softmax that spilled 300 bytes took 3.5k cycles a chunk
+// instead of 1.6k).  Hence scores in 16-column pieces, and an 8-bit chunk in
+// quarters.
 //
 // P is rounded to 16 bits for its product: bf16 next to a bf16 V (2^-8
 // relative per weight, as the output itself is rounded), fp16 with an 8-bit
 // cache (2^-11).  The sum l uses the unrounded weights.
 //
-// 8-bit cache: K and V arrive as e4m3 codes (half the bytes), and four warps
-// rewrite each tile as fp16 operands: code * 2^(e_row - E) with E the chunk's
-// largest exponent, exact but for rows 2^-15 and more below it (whose low
-// bits, 2^-24 of the chunk's largest element, go).  E of a K chunk joins the
-// score scale; E of a V chunk joins the exponent of P.  The tree's bf16 rows
-// and the queries become fp16 the same way (power-of-two scale per chunk /
-// per query vector: bf16's 8 bits fit in fp16's 11).
+// 8-bit cache: K's codes go to the product as they are (kind::f8f6f4, the
+// codes' rate is twice the 16-bit one), with the query vector as the sum of
+// two e4m3 codes an element (4 + 4 significant bits hold bf16's 8; see
+// tt_split8) and the tree's keys as two codes too; the keys' scales 2^e are
+// multiplied to the scores.  V is rewritten to fp16 by four warps: code *
+// 2^(e_row - E), E the chunk's largest exponent, exact but for rows 2^-15 and
+// more below it (whose low bits, 2^-24 of the chunk's largest element, go); E
+// joins the exponent of P.  (Rewriting K as well made each chunk's scores
+// wait for a conversion: 365 us where this takes 260, 32 sequences x 64 rows
+// over 8k contexts.)  Two codes for P as well would spare V's conversion but
+// cost the softmax, which has no time to spare, a second rounding per weight.
 //
-// Bound by HBM (K/V bytes) up to 256 query vectors per KV head: per 128-key
-// chunk an SM's share of the bandwidth takes 2.8k cycles in bf16 (1.4k in 8
-// bits), the two products 1.0k per query tile.
+// What bounds it, per 128-key chunk and SM at NT = 2: HBM 2.9k cycles in
+// bf16, 1.5k in 8 bits; the tensor core 2.1k (4 x 8 products of 67 cycles);
+// the softmax 1.6k a stream in turns, 3.3k for both; measured 3.6k in bf16
+// and about 6k in 8 bits, where the scales (two more instructions a pair of
+// scores and four loads) and the conversion share the issue slots.
 #include <math.h>
 
 #include "common.cuh"

@@ -281,3 +281,19 @@ def test_build():
             assert int(out[0][s, i]) == (parent[i] if dp is not None else D.DFLASH_TREE_PAD), i
             assert int(out[1][s, i]) == (cand[s, dp - 1, rank[i]] if dp else 7 + s)
             assert int(out[2][s, i]) == [100, 0, 5][s] + (dp or 0)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("V", [1536, 1537, 2048, 10240, 10241, 25000])
+def test_slices_of_several_batches(drawn, V):
+    """More sequences than a device holds clusters of: a CTA per sequence walks
+    the whole row, in one batch of its registers or several; candidates sit on
+    both sides of the batches' borders."""
+    S = 81
+    p = Accept(S, 9, V, levels=4, drawn=drawn, seed=V)
+    for s, x in enumerate((0, V - 1, min(10239, V - 1), min(10240, V - 1), min(20480, V - 1))):
+        p.tokens[s, 1] = x
+        p.target[s, :, x] += 6.0
+    p.put()
+    p.run()
+    p.check(seqs=[0, 1, 2, 3, 4, 40, 79, 80], unsure=1)
