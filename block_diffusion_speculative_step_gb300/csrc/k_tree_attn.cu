@@ -12,7 +12,7 @@ namespace dfl {
 // ------------------------------------------------------ CUDA-core path
 //
 // One CTA per (split, KV head x query tile, sequence): 32 query vectors
-// against 256 key slots (the last split: the tree's rows), 64 keys at a time.
+// against 64 to 256 key slots (the last split: the tree's rows), 64 keys at a time.
 // S = Q K^T and O += P V are register-blocked 4 x 4 and 4 x (d / 16) tiles
 // per thread, the online softmax's maximum and sum are shared by the 16
 // threads of a row.  Splits sit at fixed slot offsets, so a row's bits depend
@@ -21,17 +21,21 @@ namespace dfl {
 constexpr int kTsThreads = 128;
 constexpr int kTsQT = 32;     // query vectors per CTA
 constexpr int kTsKT = 64;     // keys per step
-constexpr int kTsSplit = 256; // key slots per split
 
 struct TsGeom {
-  int grp, nqv, n_qt, n_split;  // n_split: context splits + the tree's
+  int grp, nqv, n_qt, split, n_split;  // key slots per split; context splits + the tree's
 };
 __host__ __device__ inline TsGeom ts_geom(const TreeAttnDesc& a) {
   TsGeom g;
   g.grp = a.nq / a.nkv;
   g.nqv = a.rows * g.grp;
   g.n_qt = (g.nqv + kTsQT - 1) / kTsQT;
-  g.n_split = (a.max_pos + kTsSplit - 1) / kTsSplit + 1;
+  // Short contexts want many CTAs, long ones few partials.  By the bound of the
+  // contexts, not by the batch: a row's bits do not depend on what runs beside
+  // it.  64 / 256 slots measured: 3 sequences up to 131 slots 11.1 / 13.4 us, 2 of
+  // 1000 17.3 / 28.0 us, 4 of 8190 110 / 65 us (128: 13.4, 19.2, 79.5 us).
+  g.split = a.max_pos <= 1024 ? 64 : a.max_pos <= 4096 ? 128 : 256;
+  g.n_split = (a.max_pos + g.split - 1) / g.split + 1;
   return g;
 }
 
@@ -54,9 +58,9 @@ __global__ void __launch_bounds__(kTsThreads) tree_simt_kernel(const __grid_cons
   const int sp = blockIdx.x, g = blockIdx.y / gm.n_qt, qt = blockIdx.y % gm.n_qt, s = blockIdx.z;
   const bool tree = sp == gm.n_split - 1;
   const int n_ctx = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
-  const int j0 = sp * kTsSplit;
+  const int j0 = sp * gm.split;
   if (!tree && j0 >= n_ctx) return;  // the merge knows which splits hold keys
-  const int n_keys = tree ? a.rows : min(kTsSplit, n_ctx - j0);
+  const int n_keys = tree ? a.rows : min(gm.split, n_ctx - j0);
   const int tid = threadIdx.x;
   const int qv0 = qt * kTsQT, nq_tile = min(kTsQT, gm.nqv - qv0);
   const int QD = a.nq * D;
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(256) tree_simt_merge_kernel(const __grid_const
   const int qv = (int)(w % gm.nqv), g = (int)(w / gm.nqv % a.nkv), s = (int)(w / gm.nqv / a.nkv);
   const int qt = qv / kTsQT, qi = qv % kTsQT;
   const int n_ctx = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
-  const int n_sp = (n_ctx + kTsSplit - 1) / kTsSplit;  // context splits that hold keys
+  const int n_sp = (n_ctx + gm.split - 1) / gm.split;  // context splits that hold keys
   const size_t slot0 = (((size_t)s * a.nkv + g) * gm.n_qt + qt) * gm.n_split;
   const float* base = static_cast<const float*>(a.work);
   constexpr size_t PS = kTsQT * (D + 2);
