@@ -122,7 +122,7 @@ struct TtShared {  // after the tiles
   float xm[2][128], xl[2][128], xu[2][128];  // a segment's stream statistics (NT = 1): maximum, sum, unit of O
   int par[DFLASH_MAX_TREE];
   uint32_t mask[4][DFLASH_MAX_TREE][4];      // the tree rows' ancestors and themselves (none: padding)
-  uint16_t kf[4][kTtCH];          // 8-bit: the keys' scales 2^e as bf16, by chunk counter (two V slots keep the converters at most 3 ahead)
+  float kf[4][kTtCH];             // 8-bit: the keys' scales 2^e, by chunk counter (two V slots keep the converters at most 3 ahead)
   int ev[kTtRing];                // 8-bit: the chunk's V exponent
   uint32_t badv[kTtRing][4];      // tree rows whose V holds a NaN or infinity, by chunk counter
   int cmax[2][4];                 // converters: the warps' maxima, by chunk & 1
@@ -340,17 +340,18 @@ struct Seg {
 //            per = ceil(total / nb): every CTA the same number.  An item has
 //            kTtSetup positions before its chunks', for what it costs besides
 //            them (queries, masks, first chunk, output: about 8k cycles);
-//   aligned  every item gets sp = nb / items CTAs of its own, each
-//            ceil(chunks / sp) chunks: no CTA has parts of two items, which
-//            costs a second query load, prologue and partial (about 6 us).
-// Aligned where its longest run is at most one chunk longer than the flat
-// one, i.e. for few sequences of similar lengths: 8 items of 33 chunks take
-// 2 chunks on 136 CTAs, flat 2 on 132 of which 7 straddle two items (batch 1,
-// 4k context: 12 us against 18).
+//   aligned  an item's chunks are cut into runs of `per` and every run has a
+//            CTA of its own, per the smallest for which nb CTAs suffice: no
+//            CTA has parts of two items, which costs a second query load,
+//            prologue and partial (about 6 us).
+// Aligned where its runs are at most one chunk longer than the flat ones, i.e.
+// for few items: 8 items of 33 chunks take 2 chunks on 136 CTAs, flat 2 on
+// 132 of which 7 straddle two items (batch 1, 4k context: 12 us against 18).
 constexpr int kTtSetup = 2;
 struct Part {
-  int aligned, per, sp;  // flat: positions per CTA; aligned: CTAs per item
-  int total;             // positions
+  int aligned, per;  // flat: positions per CTA; aligned: chunks
+  int sp;            // aligned: CTAs of every item, or 0: as many as its own chunks need
+  int total;         // positions (flat)
 };
 
 __device__ __forceinline__ int tt_chunks(const TreeAttnDesc& a, int s, int* n) {
@@ -363,24 +364,48 @@ __device__ __forceinline__ Part tt_part(const TreeAttnDesc& a, int ips, int nb) 
   int t = 0, mx = 0, n;
   for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
     const int k = tt_chunks(a, s, &n);
-    t += k + kTtSetup;
+    t += k;
     mx = max(mx, k);
   }
   Part p;
-  p.total = __reduce_add_sync(0xffffffffu, t) * ips;
+  t = __reduce_add_sync(0xffffffffu, t);
   mx = __reduce_max_sync(0xffffffffu, mx);
+  p.total = (t + a.n_seqs * kTtSetup) * ips;
   p.per = (p.total + nb - 1) / nb;
-  p.sp = nb / (a.n_seqs * ips);
-  p.aligned = p.sp > 0 && (mx + p.sp - 1) / p.sp <= p.per + 1;
+  p.aligned = p.sp = 0;
+  if (a.n_seqs * ips > nb) return p;
+  const int least = (t * ips + nb - 1) / nb, sp = nb / (a.n_seqs * ips), even = (mx + sp - 1) / sp;
+  if (even <= least + 1) {  // the same number for every item is as good: no search, no scan
+    p.sp = sp;
+    p.aligned = even <= p.per + 1;
+    if (p.aligned) p.per = even;
+    return p;
+  }
+  auto fits = [&](int per) {  // do nb CTAs suffice for runs of per chunks?
+    int r = 0;
+    for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) r += (tt_chunks(a, s, &n) + per - 1) / per;
+    return __reduce_add_sync(0xffffffffu, r) * ips <= nb;
+  };
+  int lo = least, hi = even;
+  while (lo < hi) {
+    const int mid = hi - lo > 4 ? (lo + hi) >> 1 : lo;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo <= p.per + 1) {
+    p.aligned = 1;
+    p.per = lo;
+  }
   return p;
 }
 
 // The sequence, item, position in the item, context length and number of
-// chunks at position x of the flat order.
+// chunks at position x of the flat order; aligned (run > 0): position = run
+// of the item, x = CTA.
 struct Spot {
   int s, it, c, n, nch;
 };
-__device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x) {
+__device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x, int run) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   Spot p = {a.n_seqs, 0, 0, 0, 1};
@@ -388,7 +413,7 @@ __device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x)
     const int s = b + lane;
     int n = 0;
     const int nch = s < a.n_seqs ? tt_chunks(a, s, &n) : 0;
-    const int len = s < a.n_seqs ? nch + kTtSetup : 0;
+    const int len = s >= a.n_seqs ? 0 : run ? (nch + run - 1) / run : nch + kTtSetup;
     int inc = len * ips;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -399,7 +424,7 @@ __device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x)
     if (hit) {
       const int w = __ffs(hit) - 1;
       p.nch = __shfl_sync(0xffffffffu, nch, w);
-      const int k = p.nch + kTtSetup, at = x - (before + __shfl_sync(0xffffffffu, inc, w) - k * ips);
+      const int k = __shfl_sync(0xffffffffu, len, w), at = x - (before + __shfl_sync(0xffffffffu, inc, w) - k * ips);
       p.s = b + w;
       p.it = at / k;
       p.c = at % k;
@@ -407,6 +432,20 @@ __device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x)
       return p;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return p;
+}
+
+// The run of CTA b (aligned): its item, number in the item (c), lengths.
+__device__ __forceinline__ Spot tt_run(const TreeAttnDesc& a, int ips, int b, const Part& pt) {
+  if (!pt.sp) return tt_locate(a, ips, b, pt.per);
+  Spot p = {a.n_seqs, 0, 0, 0, 1};
+  const int item = b / pt.sp;
+  if (item < a.n_seqs * ips) {
+    p.s = item / ips;
+    p.it = item % ips;
+    p.c = b % pt.sp;
+    p.nch = tt_chunks(a, p.s, &p.n);
   }
   return p;
 }
@@ -558,19 +597,15 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     Spot sp = {0, 0, 0, 0, 1};
     int len = 0;
     if (pt.aligned) {
-      const int item = (int)blockIdx.x / pt.sp;
-      if (item < a.n_seqs * ips) {
-        sp.s = item / ips;
-        sp.it = item % ips;
-        sp.nch = tt_chunks(a, sp.s, &sp.n);
-        const int per = (sp.nch + pt.sp - 1) / pt.sp;
-        sp.c = (int)blockIdx.x % pt.sp * per;
-        len = min(per, sp.nch - sp.c);
+      sp = tt_run(a, ips, blockIdx.x, pt);
+      if (sp.s < a.n_seqs && sp.c * pt.per < sp.nch) {
+        sp.c *= pt.per;
+        len = min(pt.per, sp.nch - sp.c);
       }
     } else {
       const int x0 = min((int)blockIdx.x * pt.per, pt.total);  // (nb * per < total + nb: no overflow)
       len = min(pt.per, pt.total - x0);
-      if (len > 0) sp = tt_locate(a, ips, x0);
+      if (len > 0) sp = tt_locate(a, ips, x0, 0);
     }
     if (lane == 0) {
       sh->s0 = sp.s;
@@ -1015,25 +1050,26 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               for (int k = 0; k < W; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
             }
           };
-          const uint4* kf4 = reinterpret_cast<const uint4*>(sh->kf[cc & 3]);
+          const float4* kf4 = reinterpret_cast<const float4*>(sh->kf[cc & 3]);
           // the keys' scales of step i; read a step ahead (shared memory is busy
           // with the products' operands, and a wait for scores holds loads back)
           struct Scales {
-            uint32_t w[Q8 ? W / 2 : 1];
+            float4 f[Q8 ? W / 4 : 1];
           };
           auto load_kf = [&](int i, Scales& f) {
             if constexpr (Q8) {
 #pragma unroll
-              for (int k = 0; k < W / 8; ++k) {
-                const uint4 y = kf4[i * (W / 8) + k];
-                f.w[4 * k] = y.x, f.w[4 * k + 1] = y.y, f.w[4 * k + 2] = y.z, f.w[4 * k + 3] = y.w;
-              }
+              for (int k = 0; k < W / 4; ++k) f.f[k] = kf4[i * (W / 4) + k];
             }
           };
           auto scale2 = [&](const Scales& f, int k) {  // the score scales of columns 2 k, 2 k + 1
             const unsigned long long cs2 = tt_pair(cs, cs);
-            if constexpr (Q8) return tt_mul2(tt_pair(__uint_as_float(f.w[k] << 16), __uint_as_float(f.w[k] & 0xFFFF0000u)), cs2);
-            else return cs2;
+            if constexpr (Q8) {
+              const float4& y = f.f[k >> 1];
+              return tt_mul2(k & 1 ? tt_pair(y.z, y.w) : tt_pair(y.x, y.y), cs2);
+            } else {
+              return cs2;
+            }
           };
           auto cols_max = [&](int i0, int n) {  // the largest score of n steps
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1053,12 +1089,18 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           };
           unsigned long long sa, sb;
-          auto piece = [&](float (&x)[W], const Scales& f, uint32_t* pk, float m0) {  // weights 2^(scale x + m0), packed; their sums
+          // weights 2^(scale x + m0) of a step, packed, and their sums; `next` starts
+          // the next step's loads once the scores have been taken
+          auto piece = [&](float (&x)[W], const Scales& f, uint32_t* pk, float m0, auto next) {
             const unsigned long long m2 = tt_pair(m0, m0);
+            unsigned long long y[W / 2];
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) y[k] = tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), scale2(f, k), m2);
+            next();
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {
               float lo, hi;
-              tt_unpair(tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), scale2(f, k), m2), lo, hi);
+              tt_unpair(y[k], lo, hi);
               lo = tt_ex2(lo);
               hi = tt_ex2(hi);
               if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
@@ -1132,19 +1174,20 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             for (;;) {
               const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
               sa = sb = tt_pair(0.f, 0.f);
-              float x[2][W];
-              Scales f[2];
-              tmem_ld_async(ts + HC * h, x[0]);
-              load_kf(h * (HC / W), f[0]);
+              float x[W];
+              Scales f;
+              tmem_ld_async(ts + HC * h, x);
+              load_kf(h * (HC / W), f);
 #pragma unroll
               for (int i = 0; i < HC / W; ++i) {  // the next scores arrive while these are exponentiated
-                tmem_wait(x[i & 1]);
-                if (i + 1 < HC / W) {
-                  tmem_ld_async(ts + HC * h + W * (i + 1), x[(i + 1) & 1]);
-                  load_kf(h * (HC / W) + i + 1, f[(i + 1) & 1]);
-                }
-                hide(x[i & 1], h * (HC / W) + i);
-                piece(x[i & 1], f[i & 1], pk[i * W >> 5] + (i * W / 2 & 15), m0);
+                tmem_wait(x);
+                hide(x, h * (HC / W) + i);
+                piece(x, f, pk[i * W >> 5] + (i * W / 2 & 15), m0, [&]() {
+                  if (i + 1 < HC / W) {
+                    tmem_ld_async(ts + HC * h + W * (i + 1), x);
+                    load_kf(h * (HC / W) + i + 1, f);
+                  }
+                });
               }
               float s0, s1;
               tt_unpair(tt_add2(sa, sb), s0, s1);
@@ -1321,7 +1364,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (c + 1 < sg.c1 && !sg.is_tree(c + 1)) load_exp(c + 1, g);
             const int rv = max(group_max(ev), e_top - 30);  // (O's unit never lies 2^30 above a chunk's: see the sums)
             e_top = max(e_top, rv);
-            sh->kf[i & 3][ct] = (uint16_t)((127 + ek) << 7);
+            sh->kf[i & 3][ct] = __int_as_float((127 + ek) << 23);
             if (ct == 0) sh->ev[i % kTtRing] = rv;
             tc::mbar_arrive(&sh->kfr[i % kTtRing]);
             sh->fac[ct] = tt_half_pow2(max(ev - rv, -1000));
@@ -1382,7 +1425,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               }
             };
             if (nt > 0) wait_warp(&sh->tkempty, (uint32_t)(nt - 1));
-            if (ct >= nk) sh->kf[i & 3][ct] = 127 << 7;  // (a hidden key: any finite scale, for -inf times it)
+            if (ct >= nk) sh->kf[i & 3][ct] = 1.f;  // (a hidden key: any finite scale, for -inf times it)
 #pragma unroll 1
             for (int r0 = 0; r0 < nk; r0 += RN) {
               load_rows(0, r0);
@@ -1401,7 +1444,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;
                 *reinterpret_cast<uint2*>(q) = hi;
                 *reinterpret_cast<uint2*>(q + RAW) = lo;
-                if (ct % CPR == 0 && row < nk) sh->kf[i & 3][row] = (uint16_t)((127 + e) << 7);
+                if (ct % CPR == 0 && row < nk) sh->kf[i & 3][row] = __int_as_float((127 + e) << 23);
               }
             }
             tc::fence_proxy_async_smem();
@@ -1470,39 +1513,41 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
 // contiguous bytes; the loads of U partials are in flight at once.
 template <int D, int NT, int CW, int U>
 __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constant__ TreeAttnDesc a, int n_pt, int nb) {
-  pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int ips = a.nkv * n_pt, grp = a.nq / a.nkv, nqv = a.rows * grp;
   constexpr int CG = D / CW;
   const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int cg = w % CG, rg = w / CG;
-  if (rg >= min(NT * 4, (nqv + 31) / 32)) return;
-  const Part pt = tt_part(a, ips, nb);
-  int s, it, b0, b1, X = 0, per;
-  if (pt.aligned) {
-    const int item = blockIdx.y;
-    if (item >= a.n_seqs * ips) return;
-    s = item / ips;
-    it = item % ips;
-    int n;
-    const int nch = tt_chunks(a, s, &n);
-    per = (nch + pt.sp - 1) / pt.sp;
-    b0 = item * pt.sp;
-    b1 = b0 + (nch - 1) / per;
-  } else {
-    per = pt.per;
-    const int x = (int)(blockIdx.y + 1) * per;
-    if (x >= pt.total) return;
-    const Spot sp = tt_locate(a, ips, x);
-    s = sp.s;
-    it = sp.it;
-    X = x - sp.c + kTtSetup;  // the item's chunks are [X, X + nch)
-    b0 = X / per;
-    b1 = (X + sp.nch - 1) / per;
-    if (x <= X || b0 != (int)blockIdx.y) return;  // no item cut here, or not its first cut
+  // Which item, if any: found beside the attention kernel's last CTAs, for the
+  // lengths it goes by were there before that kernel's own wait ended.
+  int s = 0, it = 0, b0 = 0, b1 = 0;
+  if (rg < min(NT * 4, (nqv + 31) / 32)) {
+    const Part pt = tt_part(a, ips, nb);
+    if (pt.aligned) {
+      const Spot sp = tt_run(a, ips, blockIdx.y, pt);
+      if (sp.s < a.n_seqs && sp.c == 0) {  // an item's first run
+        s = sp.s;
+        it = sp.it;
+        b0 = blockIdx.y;
+        b1 = b0 + (sp.nch - 1) / pt.per;
+      }
+    } else {
+      const int per = pt.per, x = (int)(blockIdx.y + 1) * per;
+      if (x < pt.total) {
+        const Spot sp = tt_locate(a, ips, x, 0);
+        const int X = x - sp.c + kTtSetup;  // the item's chunks are [X, X + nch)
+        if (x > X && X / per == (int)blockIdx.y) {  // an item is cut here, for the first time
+          s = sp.s;
+          it = sp.it;
+          b0 = blockIdx.y;
+          b1 = (X + sp.nch - 1) / per;
+        }
+      }
+    }
   }
-  if (b0 == b1) return;  // written by its CTA
+  pdl_wait();  // (every CTA: who waits for this kernel waits for the attention too)
+  if (b0 == b1) return;  // none, or written by its CTA
   const int g = it / n_pt, qv = (it % n_pt) * (NT * kTtRows) + rg * 32 + lane;
   if (qv - lane >= nqv) return;
   const int tile = rg >> 2, prow = (rg & 3) * 32 + lane;
