@@ -45,14 +45,18 @@ constexpr int kTaWarps = kTaThreads / 32;
 constexpr int kTaE = 20, kTaShortE = 4;
 constexpr int kTaMaxCluster = 16;
 
+__device__ __forceinline__ float ta_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Weight exp((l - m) / T) = 2^(c (l - m)) of logit l against the row's maximum
 // m, c = log2(e) / T (l == m also when both are infinite: the weight is then 1
 // and the caller reports the row).  Beside the argument's rounding, which
 // exp((l - m) * (1 / T)) has too, the hardware's 2^x adds 2^-22.
 __device__ __forceinline__ float ta_weight(float l, float m, float c) {
-  float w;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((l - m) * c));
-  return l == m ? 1.f : w;
+  return l == m ? 1.f : ta_ex2((l - m) * c);
 }
 
 struct TaSum {  // maximum and sum of weights against it
@@ -63,7 +67,7 @@ __device__ __forceinline__ TaSum ta_join(TaSum a, float c) {
   float m = a.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = a.s > 0.f ? a.s * ta_weight(a.m, m, c) : 0.f;
+  float s = a.s == 0.f ? 0.f : a.s * ta_weight(a.m, m, c);  // (a NaN stays)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return {m, s};
@@ -140,9 +144,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
   // coalesced whatever the row's alignment (rows of an odd V)
   auto load = [&](const float* row, int b, float (&x)[E]) __attribute__((always_inline)) {
     const int v = v0 + b * BATCH + tid;
+    if (v0 + (b + 1) * BATCH <= v1) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      x[j] = v + j * kTaThreads < v1 ? __ldg(row + v + j * kTaThreads) : -INFINITY;
+      for (int j = 0; j < E; ++j) x[j] = __ldg(row + v + j * kTaThreads);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = v + j * kTaThreads < v1 ? __ldg(row + v + j * kTaThreads) : -INFINITY;
     }
   };
 
@@ -215,34 +222,34 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     __syncthreads();
 
     // ---- maxima and sums over the slice, the children's tokens left out
-    bool nan = false;
-    auto clean = [&](int b, float (&x)[E]) __attribute__((always_inline)) {  // NaN and the children's tokens: weight 0
+    // (a NaN or +inf logit makes the sum NaN, or the maximum infinite: reported
+    // below; every test then fails and the draw falls to token 0)
+    auto clean = [&](int b, float (&x)[E]) __attribute__((always_inline)) {  // the children's tokens: weight 0
       uint32_t mine = 0u;  // bit j: entry j is a child's token
       for (int c = 0; c < n_child; ++c) {
         const int x0 = sh.ctok[c];
         const unsigned rel = (unsigned)(x0 - v0 - b * BATCH);
         if (x0 >= 0 && rel < (unsigned)BATCH && (int)(rel % kTaThreads) == tid) mine |= 1u << (rel / kTaThreads);
       }
+      if (!__any_sync(0xffffffffu, mine != 0u)) return;
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        if (!(x[j] < INFINITY)) nan = true;
-        x[j] = x[j] == x[j] && !((mine >> j) & 1u) ? x[j] : -INFINITY;
-      }
+      for (int j = 0; j < E; ++j) x[j] = (mine >> j) & 1u ? -INFINITY : x[j];
     };
     auto add = [&](TaSum& a, float (&x)[E]) __attribute__((always_inline)) {  // logits -> weights against the maximum so far
       float m = a.m;
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        m = fmaxf(m, x[j]);
-      }
-      if (a.s > 0.f) a.s *= ta_weight(a.m, m, c2);
+      for (int j = 0; j < E; ++j) m = fmaxf(m, x[j]);
+      if (a.s != 0.f) a.s *= ta_weight(a.m, m, c2);
       a.m = m;
-      const bool any = m > -INFINITY;
+      const float ref = m > -INFINITY ? m : 0.f;  // (all -inf: weights 0)
+      float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        x[j] = any ? ta_weight(x[j], m, c2) : 0.f;
-        a.s += x[j];
+        x[j] = ta_ex2((x[j] - ref) * c2);
+        if (j & 1) s1 += x[j];
+        else s0 += x[j];
       }
+      a.s += s0 + s1;
     };
     auto row_sum = [&](const float* row, float (&w)[E], float* m0) __attribute__((always_inline)) {
       TaSum a = {-INFINITY, 0.f};
@@ -266,7 +273,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     const TaSum ap = row_sum(l, lw, &ml);
     TaSum aq = {-INFINITY, 0.f};
     if (Drawn && g) aq = row_sum(g, gw, &mg);
-    if (nan) raise_status(d.status, ST_NUMERIC);
     if (lane == 0) {
       sh.wp[warp] = ap;
       sh.wq[warp] = aq;
@@ -288,7 +294,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       mp = fmaxf(mp, sh.cl[c]);
       if (Drawn) mq = fmaxf(mq, sh.cg[c]);
     }
-    if (mp == -INFINITY && rank == 0 && tid == 0) raise_status(d.status, ST_NUMERIC);
+    // no logit above -inf, +inf, or a NaN
+    const bool bad = !(mp > -INFINITY && mp < INFINITY) || P.s != P.s || (Drawn && (mq == INFINITY || Q.s != Q.s));
+    if (bad && rank == 0 && tid == 0) raise_status(d.status, ST_NUMERIC);
     if (tid < n_child) {
       sh.cp[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cl[tid], mp, c2);
       if (Drawn) sh.cq[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cg[tid], mq, c2);
