@@ -64,9 +64,9 @@ struct TaSum {  // maximum and sum of weights against it
 };
 // Joined over the warp, bitwise the same in every lane.
 __device__ __forceinline__ TaSum ta_join(TaSum a, float c) {
-  float m = a.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // (an integer reduction: floats order as their bits, negative ones with the others flipped)
+  const int i = __float_as_int(a.m), r = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+  const float m = __int_as_float(r ^ ((r >> 31) & 0x7FFFFFFF));
   float s = a.s == 0.f ? 0.f : a.s * ta_weight(a.m, m, c);  // (a NaN stays)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -181,45 +181,37 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         if (c) sh.child[n + __popc(bal & ((1u << lane) - 1u))] = i;
         n += __popc(bal);
       }
+      if (deep) {
+        if (n > 0 && rank == 0 && lane == 0) raise_status(d.status, ST_RANGE);
+        n = 0;
+      }
       if (lane == 0) sh.n_child = n;
-    }
-    __syncthreads();
-    int n_child = sh.n_child;
-    if (deep) {
-      if (n_child > 0 && rank == 0 && tid == 0) raise_status(d.status, ST_RANGE);
-      n_child = 0;
-    }
-    const float* g = Drawn && n_child > 0 ? draft + (size_t)k * V : nullptr;
-    if (Drawn) {
-      if (!g) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          gw[j] = -INFINITY;
+      __syncwarp();
+      for (int c = lane; c < n; c += 32) {
+        const int i = sh.child[c];
+        int x = sh.tok[i];
+        if (x < 0 || x >= V) {
+          if (rank == 0) raise_status(d.status, ST_RANGE);
+          x = -1;  // never accepted, nothing to remove
         }
+        sh.ctok[c] = x;
+        sh.cu[c] = sh.u[i];
+        const float a = x >= 0 ? l[x] : -INFINITY, b = Drawn && x >= 0 ? draft[(size_t)k * V + x] : -INFINITY;
+        if (!(a < INFINITY) || !(b < INFINITY)) raise_status(d.status, ST_NUMERIC);
+        sh.cl[c] = a == a ? a : -INFINITY;
+        if (Drawn) sh.cg[c] = b == b ? b : -INFINITY;
+        int dup = x < 0;
+        for (int e = 0; e < c; ++e) dup |= sh.tok[sh.child[e]] == x;
+        sh.cdup[c] = dup;
       }
-    }
-    if (tid < n_child) {
-      const int i = sh.child[tid];
-      int x = sh.tok[i];
-      if (x < 0 || x >= V) {
-        if (rank == 0) raise_status(d.status, ST_RANGE);
-        x = -1;  // never accepted, nothing to remove
-      }
-      sh.ctok[tid] = x;
-      sh.cu[tid] = sh.u[i];
-      const float a = x >= 0 ? l[x] : -INFINITY;
-      if (!(a < INFINITY)) raise_status(d.status, ST_NUMERIC);
-      sh.cl[tid] = a == a ? a : -INFINITY;
-      if (Drawn) {
-        const float b = x >= 0 ? g[x] : -INFINITY;
-        if (!(b < INFINITY)) raise_status(d.status, ST_NUMERIC);
-        sh.cg[tid] = b == b ? b : -INFINITY;
-      }
-      int dup = x < 0;
-      for (int e = 0; e < tid; ++e) dup |= sh.tok[sh.child[e]] == x;
-      sh.cdup[tid] = dup;
     }
     __syncthreads();
+    const int n_child = sh.n_child;
+    const float* g = Drawn && n_child > 0 ? draft + (size_t)k * V : nullptr;
+    if (Drawn && !g) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) gw[j] = -INFINITY;
+    }
 
     // ---- maxima and sums over the slice, the children's tokens left out
     // (a NaN or +inf logit makes the sum NaN, or the maximum infinite: reported
@@ -278,17 +270,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       sh.wq[warp] = aq;
     }
     __syncthreads();
-    float4 xs = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    if (warp == 0) {
-      const TaSum none = {-INFINITY, 0.f};
-      const TaSum a = ta_join(lane < kTaWarps ? sh.wp[lane] : none, c2);
-      const TaSum b = Drawn ? ta_join(lane < kTaWarps ? sh.wq[lane] : none, c2) : none;
-      xs = make_float4(a.m, a.s, b.m, b.s);
+    TaSum P = {-INFINITY, 0.f}, Q = {-INFINITY, 0.f};
+    if (NC == 1 || warp == 0) {  // (a CTA alone: every warp for itself)
+      P = ta_join(lane < kTaWarps ? sh.wp[lane] : P, c2);
+      if (Drawn) Q = ta_join(lane < kTaWarps ? sh.wq[lane] : Q, c2);
     }
-    xs = exchange(xs);
-    TaSum P = ta_join({xs.x, xs.y}, c2), Q = {-INFINITY, 0.f};
-    if (Drawn) Q = ta_join({xs.z, xs.w}, c2);
-    // every thread forms the rows' maxima, one thread the totals, with the children in order
+    if (NC > 1) {
+      const float4 xs = exchange(make_float4(P.m, P.s, Q.m, Q.s));
+      P = ta_join({xs.x, xs.y}, c2);
+      if (Drawn) Q = ta_join({xs.z, xs.w}, c2);
+    }
+    // every thread forms the rows' maxima, one warp the totals, with the children in order
     float mp = P.m, mq = Q.m;
     for (int c = 0; c < n_child; ++c) {
       mp = fmaxf(mp, sh.cl[c]);
@@ -297,23 +289,30 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     // no logit above -inf, +inf, or a NaN
     const bool bad = !(mp > -INFINITY && mp < INFINITY) || P.s != P.s || (Drawn && (mq == INFINITY || Q.s != Q.s));
     if (bad && rank == 0 && tid == 0) raise_status(d.status, ST_NUMERIC);
-    if (tid < n_child) {
-      sh.cp[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cl[tid], mp, c2);
-      if (Drawn) sh.cq[tid] = sh.cdup[tid] && sh.ctok[tid] < 0 ? 0.f : ta_weight(sh.cg[tid], mq, c2);
-    }
-    __syncthreads();
     // a token is gone once its first child was rejected, so what is left
     // after t rejections is a suffix sum over the first children from t on
-    if (tid == 0) {
-      double z = P.s > 0.f ? (double)(P.s * ta_weight(P.m, mp, c2)) : 0.0;
-      sh.sufP[n_child] = z;
-      for (int c = n_child - 1; c >= 0; --c) sh.sufP[c] = z += sh.cdup[c] ? 0.0 : (double)sh.cp[c];
-    }
-    if (Drawn && tid == 32) {
-      double z = Q.s > 0.f ? (double)(Q.s * ta_weight(Q.m, mq, c2)) : 0.0;
-      for (int c = n_child - 1; c >= 0; --c) {
-        z += sh.cdup[c] ? 0.0 : (double)sh.cq[c];
-        sh.invY[c] = z > 0.0 ? 1.f / (float)z : 0.f;
+    if (warp == 0) {
+      for (int c = lane; c < n_child; c += 32) {
+        sh.cp[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cl[c], mp, c2);
+        if (Drawn) sh.cq[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cg[c], mq, c2);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        double z = P.s > 0.f ? (double)(P.s * ta_weight(P.m, mp, c2)) : 0.0;
+        sh.sufP[n_child] = z;
+        for (int c = n_child - 1; c >= 0; --c) sh.sufP[c] = z += sh.cdup[c] ? 0.0 : (double)sh.cp[c];
+      }
+      if (Drawn && lane == 1) {
+        double z = Q.s > 0.f ? (double)(Q.s * ta_weight(Q.m, mq, c2)) : 0.0;
+        for (int c = n_child - 1; c >= 0; --c) {
+          z += sh.cdup[c] ? 0.0 : (double)sh.cq[c];
+          sh.invY[c] = z > 0.0 ? 1.f / (float)z : 0.f;
+        }
+      }
+      __syncwarp();
+      if constexpr (Drawn) {
+        const float z = (float)sh.sufP[0], f = z > 0.f ? 1.f / z : 0.f;
+        for (int c = lane; c < n_child; c += 32) sh.cp[c] *= f;
       }
     }
     __syncthreads();
@@ -329,8 +328,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         lw[j] *= fp;
         gw[j] = g ? gw[j] * fq : 0.f;
       }
-      if (tid < n_child) sh.cp[tid] *= invP;
-      __syncthreads();
     }
     // p_t (and q's weights) of a later batch, from the logits
     auto reload = [&](int b, int t, float (&p)[E], float (&q)[E]) __attribute__((always_inline)) {
@@ -389,9 +386,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
           z = warp_sum(z);
           if (lane == 0) sh.wb[warp] = z;
           __syncthreads();
-          if (warp == 0) z = warp_sum(lane < kTaWarps ? sh.wb[lane] : 0.f);
-          const float4 xz = exchange(make_float4(0.f, z, 0.f, 0.f));
-          const float zz = warp_sum(lane < NC ? xz.y : 0.f);
+          float zz = NC == 1 || warp == 0 ? warp_sum(lane < kTaWarps ? sh.wb[lane] : 0.f) : 0.f;
+          if (NC > 1) {
+            const float4 xz = exchange(make_float4(0.f, zz, 0.f, 0.f));
+            zz = warp_sum(lane < NC ? xz.y : 0.f);
+          }
           // nothing left: p stays (the caller's q covers all of p, up to rounding)
           const float iz = zz > 0.f ? 1.f / zz : 0.f;
           if (iz > 0.f) {
