@@ -97,7 +97,7 @@ struct TaShared {
   int cdup[DFLASH_MAX_TREE];    // an earlier sibling has the same token, or the token is out of range
   float cp[DFLASH_MAX_TREE];    // p_t of the child's token (drawn) or its weight; its weight in the draft row, 0 once removed
   float cq[DFLASH_MAX_TREE];
-  double sufP[DFLASH_MAX_TREE + 1];  // mass of the target row without the tokens of children [0, t)
+  float sufP[DFLASH_MAX_TREE + 1];  // mass of the target row without the tokens of children [0, t)
   float invZ[DFLASH_MAX_TREE];  // 1 / Z_t, 0: nothing left, p stays
   float invY[DFLASH_MAX_TREE];  // 1 / (remaining mass of q before step t), in q's weights
   TaSum wp[kTaWarps], wq[kTaWarps];
@@ -296,27 +296,37 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         sh.cp[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cl[c], mp, c2);
         if (Drawn) sh.cq[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cg[c], mq, c2);
       }
-      __syncwarp();
-      if (lane == 0) {
-        double z = P.s > 0.f ? (double)(P.s * ta_weight(P.m, mp, c2)) : 0.0;
-        sh.sufP[n_child] = z;
-        for (int c = n_child - 1; c >= 0; --c) sh.sufP[c] = z += sh.cdup[c] ? 0.0 : (double)sh.cp[c];
-      }
-      if (Drawn && lane == 1) {
-        double z = Q.s > 0.f ? (double)(Q.s * ta_weight(Q.m, mq, c2)) : 0.0;
-        for (int c = n_child - 1; c >= 0; --c) {
-          z += sh.cdup[c] ? 0.0 : (double)sh.cq[c];
-          sh.invY[c] = z > 0.0 ? 1.f / (float)z : 0.f;
+      // (a suffix scan of the warp per 32 children, the last ones first)
+      float zp = P.s > 0.f ? P.s * ta_weight(P.m, mp, c2) : 0.f, zq = Drawn && Q.s > 0.f ? Q.s * ta_weight(Q.m, mq, c2) : 0.f;
+      if (lane == 0) sh.sufP[n_child] = zp;
+      for (int c0 = (n_child - 1) & ~31; c0 >= 0; c0 -= 32) {
+        const int c = c0 + lane;
+        const bool on = c < n_child && !sh.cdup[c];
+        float a = on ? sh.cp[c] : 0.f, b = Drawn && on ? sh.cq[c] : 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float a2 = __shfl_down_sync(0xffffffffu, a, o), b2 = Drawn ? __shfl_down_sync(0xffffffffu, b, o) : 0.f;
+          if (lane + o < 32) {
+            a += a2;
+            b += b2;
+          }
         }
+        a += zp;
+        b += zq;
+        if (c < n_child) {
+          sh.sufP[c] = a;
+          if (Drawn) sh.invY[c] = b > 0.f ? 1.f / b : 0.f;
+        }
+        zp = __shfl_sync(0xffffffffu, a, 0);
+        zq = __shfl_sync(0xffffffffu, b, 0);
       }
-      __syncwarp();
       if constexpr (Drawn) {
-        const float z = (float)sh.sufP[0], f = z > 0.f ? 1.f / z : 0.f;
+        const float f = zp > 0.f ? 1.f / zp : 0.f;
         for (int c = lane; c < n_child; c += 32) sh.cp[c] *= f;
       }
     }
     __syncthreads();
-    const float Zp = (float)sh.sufP[0];
+    const float Zp = sh.sufP[0];
     const float invP = Zp > 0.f ? 1.f / Zp : 0.f;
     float fp = 0.f, fq = 0.f;  // a row's weights -> p, q's weights
     if constexpr (Drawn) {
@@ -407,7 +417,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
           __syncthreads();
         }
       } else {
-        ok = !sh.cdup[t] && (double)sh.cu[t] * sh.sufP[t] < (double)sh.cp[t];
+        ok = !sh.cdup[t] && sh.cu[t] * sh.sufP[t] < sh.cp[t];
       }
       if (ok) {
         went = sh.child[t];
@@ -431,15 +441,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     float best = -INFINITY;
     int bi = INT_MAX;
     auto offer = [&](float p, float n, int v) __attribute__((always_inline)) {
-      const float r = p / n;
+      const float r = __fdividef(p, n);  // (2 units in the last place; 0 for n beyond 2^126)
       if (r > best || (r == best && v < bi)) {
         best = r;
         bi = v;
       }
     };
-    auto draw = [&](int b, const float (&p)[E]) __attribute__((always_inline)) {
-      float n[E];
-      load(noise, b, n);
+    auto draw = [&](int b, const float (&p)[E], const float (&n)[E]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int v = v0 + b * BATCH + j * kTaThreads + tid;
@@ -453,11 +461,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         lw[j] *= f;
       }
     }
-    draw(0, lw);
+    {
+      float n[E];
+      load(noise, 0, n);
+      draw(0, lw, n);
+    }
     for (int b = 1; v0 + b * BATCH < v1; ++b) {
-      float p[E], q[E];
+      float p[E], q[E], n[E];
+      load(noise, b, n);
       reload(b, t, p, q);
-      draw(b, p);
+      draw(b, p, n);
     }
     if (Drawn && rank == 0 && tid < n_child && sh.ctok[tid] >= 0)
       offer(sh.cp[tid], noise[sh.ctok[tid]], sh.ctok[tid]);
