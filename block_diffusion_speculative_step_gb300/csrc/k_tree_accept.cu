@@ -22,10 +22,17 @@
 // p(x) is close to 1.
 //
 // A walk is a chain of row passes and exchanges, each waiting for the one
-// before: latency bounds it, not bytes.  So a thread has kTaE loads in flight
-// at once, and the weights of a slice's first batch (10240 entries) stay in
-// registers from the row sums to the tests and the draw; a slice's rest is
-// read again, from L2.
+// before: latency bounds it for few sequences, the row's bytes for many (a
+// CTA's slice at its SM's share of the bandwidth).  So a thread has a batch of
+// loads in flight at once (and the next one's during its sums), and the
+// weights of a slice's first batch (10240 entries) stay in registers from the
+// row sums to the tests and the draw; a slice's rest is read again, from L2.
+// Measured, per level: about 1.2 us over 1021 entries (a third each: the loads
+// and the children, the row sums, the remaining masses; a warp scan in fp32,
+// as chains of fp64 additions took twice all that), 8 us over 37984 entries a
+// CTA, the draw 10 us there.  151936 entries: one sequence 23 us, 32 sequences
+// 54 us (the longest walk of five levels), with the row passes unbatched and
+// partial sums pulled by every CTA 104 and 253 us.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -62,11 +69,15 @@ __device__ __forceinline__ float ta_weight(float l, float m, float c) {
 struct TaSum {  // maximum and sum of weights against it
   float m, s;
 };
+// The warp's maximum (no NaN), by an integer reduction: floats order as their
+// bits, negative ones with all but the sign flipped.
+__device__ __forceinline__ float ta_max(float x) {
+  const int i = __float_as_int(x), r = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+  return __int_as_float(r ^ ((r >> 31) & 0x7FFFFFFF));
+}
 // Joined over the warp, bitwise the same in every lane.
 __device__ __forceinline__ TaSum ta_join(TaSum a, float c) {
-  // (an integer reduction: floats order as their bits, negative ones with the others flipped)
-  const int i = __float_as_int(a.m), r = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
-  const float m = __int_as_float(r ^ ((r >> 31) & 0x7FFFFFFF));
+  const float m = ta_max(a.m);
   float s = a.s == 0.f ? 0.f : a.s * ta_weight(a.m, m, c);  // (a NaN stays)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -97,6 +108,7 @@ struct TaShared {
   int cdup[DFLASH_MAX_TREE];    // an earlier sibling has the same token, or the token is out of range
   float cp[DFLASH_MAX_TREE];    // p_t of the child's token (drawn) or its weight; its weight in the draft row, 0 once removed
   float cq[DFLASH_MAX_TREE];
+  float mp, mq;                 // the rows' maxima, children included
   float sufP[DFLASH_MAX_TREE + 1];  // mass of the target row without the tokens of children [0, t)
   float invZ[DFLASH_MAX_TREE];  // 1 / Z_t, 0: nothing left, p stays
   float invY[DFLASH_MAX_TREE];  // 1 / (remaining mass of q before step t), in q's weights
@@ -216,17 +228,21 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     // ---- maxima and sums over the slice, the children's tokens left out
     // (a NaN or +inf logit makes the sum NaN, or the maximum infinite: reported
     // below; every test then fails and the draw falls to token 0)
-    auto clean = [&](int b, float (&x)[E]) __attribute__((always_inline)) {  // the children's tokens: weight 0
-      uint32_t mine = 0u;  // bit j: entry j is a child's token
+    auto find = [&](int b) __attribute__((always_inline)) {  // bit j: entry j of the batch is a child's token
+      uint32_t mine = 0u;
       for (int c = 0; c < n_child; ++c) {
         const int x0 = sh.ctok[c];
         const unsigned rel = (unsigned)(x0 - v0 - b * BATCH);
         if (x0 >= 0 && rel < (unsigned)BATCH && (int)(rel % kTaThreads) == tid) mine |= 1u << (rel / kTaThreads);
       }
+      return mine;
+    };
+    auto clean = [&](uint32_t mine, float (&x)[E]) __attribute__((always_inline)) {  // those: weight 0
       if (!__any_sync(0xffffffffu, mine != 0u)) return;
 #pragma unroll
       for (int j = 0; j < E; ++j) x[j] = (mine >> j) & 1u ? -INFINITY : x[j];
     };
+    const uint32_t mine0 = find(0);
     auto add = [&](TaSum& a, float (&x)[E]) __attribute__((always_inline)) {  // logits -> weights against the maximum so far
       float m = a.m;
 #pragma unroll
@@ -248,13 +264,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       float x[E];
       const bool more = v1 - v0 > BATCH;
       if (more) load(row, 1, x);
-      clean(0, w);
+      clean(mine0, w);
       add(a, w);
       *m0 = a.m;
       for (int b = 1; v0 + b * BATCH < v1; ++b) {
         float y[E];
         load(row, b + 1, y);
-        clean(b, x);
+        clean(find(b), x);
         add(a, x);
 #pragma unroll
         for (int j = 0; j < E; ++j) x[j] = y[j];
@@ -280,18 +296,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       P = ta_join({xs.x, xs.y}, c2);
       if (Drawn) Q = ta_join({xs.z, xs.w}, c2);
     }
-    // every thread forms the rows' maxima, one warp the totals, with the children in order
-    float mp = P.m, mq = Q.m;
-    for (int c = 0; c < n_child; ++c) {
-      mp = fmaxf(mp, sh.cl[c]);
-      if (Drawn) mq = fmaxf(mq, sh.cg[c]);
-    }
-    // no logit above -inf, +inf, or a NaN
-    const bool bad = !(mp > -INFINITY && mp < INFINITY) || P.s != P.s || (Drawn && (mq == INFINITY || Q.s != Q.s));
-    if (bad && rank == 0 && tid == 0) raise_status(d.status, ST_NUMERIC);
+    // one warp forms the rows' maxima and totals with the children
     // a token is gone once its first child was rejected, so what is left
     // after t rejections is a suffix sum over the first children from t on
     if (warp == 0) {
+      float cm = P.m, cn = Q.m;
+      for (int c = lane; c < n_child; c += 32) {
+        cm = fmaxf(cm, sh.cl[c]);
+        if (Drawn) cn = fmaxf(cn, sh.cg[c]);
+      }
+      const float mp = ta_max(cm), mq = Drawn ? ta_max(cn) : -INFINITY;
+      // no logit above -inf, +inf, or a NaN
+      const bool bad = !(mp > -INFINITY && mp < INFINITY) || P.s != P.s || (Drawn && (mq == INFINITY || Q.s != Q.s));
+      if (bad && rank == 0 && lane == 0) raise_status(d.status, ST_NUMERIC);
+      if (lane == 0) {
+        sh.mp = mp;
+        sh.mq = mq;
+      }
       for (int c = lane; c < n_child; c += 32) {
         sh.cp[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cl[c], mp, c2);
         if (Drawn) sh.cq[c] = sh.ctok[c] < 0 ? 0.f : ta_weight(sh.cg[c], mq, c2);
@@ -326,7 +347,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       }
     }
     __syncthreads();
-    const float Zp = sh.sufP[0];
+    const float mp = sh.mp, mq = sh.mq, Zp = sh.sufP[0];
     const float invP = Zp > 0.f ? 1.f / Zp : 0.f;
     float fp = 0.f, fq = 0.f;  // a row's weights -> p, q's weights
     if constexpr (Drawn) {
@@ -339,12 +360,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         gw[j] = g ? gw[j] * fq : 0.f;
       }
     }
-    // p_t (and q's weights) of a later batch, from the logits
+    // p_t (and q's weights) of a later batch, from the logits (the target row's given in p)
     auto reload = [&](int b, int t, float (&p)[E], float (&q)[E]) __attribute__((always_inline)) {
-      load(l, b, p);
-      if (Drawn && g) load(g, b, q);
-      clean(b, p);
-      if (Drawn && g) clean(b, q);
+      const uint32_t mine = find(b);
+      clean(mine, p);
+      if (Drawn && g) {
+        load(g, b, q);
+        clean(mine, q);
+      }
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         p[j] = p[j] > -INFINITY ? ta_weight(p[j], mp, c2) : 0.f;
@@ -383,6 +406,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
           }
           for (int b = 1; v0 + b * BATCH < v1; ++b) {
             float p[E], q[E];
+            load(l, b, p);
             reload(b, t, p, q);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
@@ -469,6 +493,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     for (int b = 1; v0 + b * BATCH < v1; ++b) {
       float p[E], q[E], n[E];
       load(noise, b, n);
+      load(l, b, p);
       reload(b, t, p, q);
       draw(b, p, n);
     }
