@@ -208,11 +208,20 @@ def _check(rc: int):
         raise DFlashError(rc, lib().dflash_last_error().decode())
 
 
+_torch_c = None  # torch._C once CUDA is initialised
+
+
 def _stream(stream) -> int:
     """Raw cudaStream_t of a torch stream (or an int handle)."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle itself: making a Stream object costs 3 us a call, as
+        # much as the launch
+        global _torch_c
+        if _torch_c is None:
+            import torch
+            torch.cuda.init()
+            _torch_c = torch._C
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -257,7 +266,9 @@ def dflash_read_status(ws_ptr: int, stream=None) -> int:
 
 
 def _call(name: str, args, ws_ptr: int, ws_bytes: int, stream):
-    _check(getattr(lib(), name)(C.byref(args), ws_ptr, ws_bytes, _stream(stream)))
+    rc = getattr(_lib or lib(), name)(C.byref(args), ws_ptr, ws_bytes, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def dflash_embed(args: dflash_embed_args, ws_ptr: int, ws_bytes: int, stream=None):
