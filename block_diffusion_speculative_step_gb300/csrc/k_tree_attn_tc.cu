@@ -338,8 +338,11 @@ struct Seg {
 // that their number fits 31 bits):
 //   flat     CTA b takes positions [b per, (b + 1) per) of all items in a row,
 //            per = ceil(total / nb): every CTA the same number.  An item has
-//            kTtSetup positions before its chunks', for what it costs besides
-//            them (queries, masks, first chunk, output: about 8k cycles);
+//            tt_setup positions before its chunks', for what it costs besides
+//            them (queries, masks, first chunk, output: about 8k cycles, and
+//            an 8-bit cache's conversion of queries and tree).  32 sequences
+//            x 64 rows, 8k: 1 / 2 / 3 positions 167 / 159 / 161 us in bf16, 271
+//            / 252 / 243 us in 8 bits;
 //   aligned  an item's chunks are cut into runs of `per` and every run has a
 //            CTA of its own, per the smallest for which nb CTAs suffice: no
 //            CTA has parts of two items, which costs a second query load,
@@ -347,7 +350,7 @@ struct Seg {
 // Aligned where its runs are at most one chunk longer than the flat ones, i.e.
 // for few items: 8 items of 33 chunks take 2 chunks on 136 CTAs, flat 2 on
 // 132 of which 7 straddle two items (batch 1, 4k context: 12 us against 18).
-constexpr int kTtSetup = 2;
+__device__ __forceinline__ int tt_setup(const TreeAttnDesc& a) { return a.k_exp ? 3 : 2; }
 struct Part {
   int aligned, per;  // flat: positions per CTA; aligned: chunks
   int sp;            // aligned: CTAs of every item, or 0: as many as its own chunks need
@@ -370,7 +373,7 @@ __device__ __forceinline__ Part tt_part(const TreeAttnDesc& a, int ips, int nb) 
   Part p;
   t = __reduce_add_sync(0xffffffffu, t);
   mx = __reduce_max_sync(0xffffffffu, mx);
-  p.total = (t + a.n_seqs * kTtSetup) * ips;
+  p.total = (t + a.n_seqs * tt_setup(a)) * ips;
   p.per = (p.total + nb - 1) / nb;
   p.aligned = p.sp = 0;
   if (a.n_seqs * ips > nb) return p;
@@ -413,7 +416,7 @@ __device__ __forceinline__ Spot tt_locate(const TreeAttnDesc& a, int ips, int x,
     const int s = b + lane;
     int n = 0;
     const int nch = s < a.n_seqs ? tt_chunks(a, s, &n) : 0;
-    const int len = s >= a.n_seqs ? 0 : run ? (nch + run - 1) / run : nch + kTtSetup;
+    const int len = s >= a.n_seqs ? 0 : run ? (nch + run - 1) / run : nch + tt_setup(a);
     int inc = len * ips;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       sh->c0 = sp.c;
       sh->n0 = sp.n;
       sh->len = len;
-      sh->setup = pt.aligned ? 0 : kTtSetup;
+      sh->setup = pt.aligned ? 0 : tt_setup(a);
     }
   }
   tc::tc_fence_before();
@@ -1536,7 +1539,7 @@ __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constan
       const int per = pt.per, x = (int)(blockIdx.y + 1) * per;
       if (x < pt.total) {
         const Spot sp = tt_locate(a, ips, x, 0);
-        const int X = x - sp.c + kTtSetup;  // the item's chunks are [X, X + nch)
+        const int X = x - sp.c + tt_setup(a);  // the item's chunks are [X, X + nch)
         if (x > X && X / per == (int)blockIdx.y) {  // an item is cut here, for the first time
           s = sp.s;
           it = sp.it;
