@@ -36,6 +36,8 @@
 #include <cooperative_groups.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -585,27 +587,11 @@ __global__ void __launch_bounds__(32) tree_greedy_kernel(const __grid_constant__
   }
 }
 
-cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_t st) {
-  if (d.invT == 0.f) return launch_pdl(tree_greedy_kernel, dim3(d.n_seqs), dim3(32), 0, st, d);
-  // As many CTAs per sequence as run at once, a CTA per SM, each with at least
-  // 1024 vocabulary entries.  Clusters of 16 are beyond the portable size and
-  // need one GPC's SMs, so only few of them run at once.
-  int nc = 1;
-  while (nc < 8 && d.n_seqs * nc * 2 <= num_sms && d.V >= nc * 2 * 1024) nc *= 2;
-  const bool big = nc == 8 && d.n_seqs * 32 <= num_sms && d.V >= 16 * 1024;
-  const bool brief = d.V <= (big ? 16 : nc) * kTaThreads * kTaShortE - 16 * 32;  // (slices are rounded up to 32)
-  auto* kernel = d.draft ? (brief ? tree_accept_kernel<true, kTaShortE> : tree_accept_kernel<true, kTaE>)
-                         : (brief ? tree_accept_kernel<false, kTaShortE> : tree_accept_kernel<false, kTaE>);
-  if (big) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    nc = 16;
-  }
+static cudaLaunchConfig_t ta_config(int n_seqs, int nc, cudaStream_t st, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(d.n_seqs * nc);
+  cfg.gridDim = dim3(n_seqs * nc);
   cfg.blockDim = dim3(kTaThreads);
   cfg.stream = st;
-  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
@@ -614,6 +600,49 @@ cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Does the device run clusters of 16 of this kernel?  (Asked once per device.)
+static bool ta_wide(void (*kernel)(TreeAcceptDesc)) {
+  static std::atomic<int> known[64];  // 0: not asked, 1: no, 2: yes (the kernels' sizes are alike)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (!k) {
+    cudaLaunchAttribute at[2];
+    const cudaLaunchConfig_t cfg = ta_config(1, kTaMaxCluster, nullptr, at);
+    int n = 0;
+    k = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? 2 : 1;
+    if (k == 1) cudaGetLastError();
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k == 2;
+}
+
+cudaError_t launch_tree_accept(const TreeAcceptDesc& d, int num_sms, cudaStream_t st) {
+  if (d.invT == 0.f) return launch_pdl(tree_greedy_kernel, dim3(d.n_seqs), dim3(32), 0, st, d);
+  // As many CTAs per sequence as run at once, a CTA per SM, each with at least
+  // 1024 vocabulary entries.  Clusters of 16 are beyond the portable size and
+  // need one GPC's SMs, so only few of them run at once.
+  int nc = 1;
+  while (nc < 8 && d.n_seqs * nc * 2 <= num_sms && d.V >= nc * 2 * 1024) nc *= 2;
+  auto pick = [&]() {
+    const bool brief = d.V <= nc * (kTaThreads * kTaShortE - 32);  // (slices are rounded up to 32)
+    return d.draft ? (brief ? tree_accept_kernel<true, kTaShortE> : tree_accept_kernel<true, kTaE>)
+                   : (brief ? tree_accept_kernel<false, kTaShortE> : tree_accept_kernel<false, kTaE>);
+  };
+  auto* kernel = pick();
+  if (nc == 8 && d.n_seqs * 32 <= num_sms && d.V >= 16 * 1024) {
+    nc = kTaMaxCluster;
+    kernel = pick();
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess || !ta_wide(kernel)) {
+      nc = 8;
+      kernel = pick();
+    }
+  }
+  cudaLaunchAttribute at[2];
+  const cudaLaunchConfig_t cfg = ta_config(d.n_seqs, nc, st, at);
   trace_kernel();
   return cudaLaunchKernelEx(&cfg, kernel, d);
 }

@@ -573,6 +573,9 @@ int dflash_tree_build(const dflash_tree_build_args* a, void* ws, size_t ws_bytes
  * temperature == 0: the accepted child is the first whose token equals
  * target_argmax[node] (dflash_verify_accept's argmax), the last token is the
  * last node's argmax; logits, u and noise are not read.
+ * p, q and their sums are fp32; how a row is cut into partial sums depends on
+ * n_seqs, so a decision within their rounding (about 1e-6 relative) of its
+ * border may differ with the batch.  A call is deterministic.
  * A token outside [0, V), or children below depth `levels`, raise
  * DFLASH_ERR_INVALID_ARG in the status word and are not accepted.
  * Outputs: accept_len[s] = accepted tokens k; path[s][0..k] = the accepted
