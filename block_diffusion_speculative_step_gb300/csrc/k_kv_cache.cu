@@ -18,18 +18,17 @@
 
 namespace dfl {
 
-constexpr int kKvThreads = 256;
+constexpr int kKvThreads = 128;
 constexpr int kKvHeads = 4;
 constexpr int kKvExpLim = 60;
 constexpr int kKvExpBias = 127;
 
 __device__ __forceinline__ float pow2_f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// Slot of row i (position base_pos[s] + i) of sequence s, as the cache row of
+// Slot of row i (position base + i) of sequence s, as the cache row of
 // KV head 0; false when the row is skipped.
-__device__ __forceinline__ bool kv_row(const KvRowsDesc& k, const int32_t* pages, int s, int i, int n, size_t* row,
+__device__ __forceinline__ bool kv_row(const KvRowsDesc& k, const int32_t* pages, int s, int base, int i, int n, size_t* row,
                                        uint32_t* head_rows) {
-  const int base = __ldg(k.base_pos + s);
   if (k.window > 0 && i + k.window < n) return false;  // a later row of this call takes the same slot
   const uint32_t pos = (uint32_t)base + (uint32_t)i;   // (i < 2^27: from base >= 0 no wrap)
   const uint32_t slot = k.window > 0 ? pos % (uint32_t)k.window : pos;
@@ -62,9 +61,9 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
 // with a head per thread the issue slots went to addresses -- position, page,
 // divisions -- and to frexp and shuffles; so an address serves four heads,
 // whose loads are in flight together.  32 sequences x 16 rows x 8 heads of 128
-// x 36 layers, written in 8 bits and read back: 77 -> 43 us, and 33 us with
-// the maxima taken on bit patterns (write 22, read 18 with a cold cache; the
-// rows' bytes alone would take 18).
+// x 36 layers, written in 8 bits and read back: 77 -> 43 us, 33 us with the
+// maxima taken on bit patterns, 31 us in blocks of 128 (the rows' bytes alone
+// would take 18).  Two and eight heads a thread: 41 and 33 us against 32.
 struct KvUnit {
   int s, i, m, head, heads, e0, layer;
   bool is_v, on;
@@ -145,15 +144,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
   pdl_wait();
   pdl_launch_dependents();
   KvUnit u(k);
+  // (the count, the row's index and the position in one round trip)
   const int n = u.on ? (k.valid ? min(__ldg(k.valid + u.s), k.rows) : k.rows) : 0;
-  int src = u.i;
+  const int src = u.on && k.row_index ? __ldg(k.row_index + u.m) : u.i;
+  const int base = u.on ? __ldg(k.base_pos + u.s) : 0;
   u.on = u.on && u.i < n;
-  if (u.on && k.row_index) {
-    src = __ldg(k.row_index + u.m);
-    if (src < 0 || src >= k.rows) {
-      raise_status(k.status, ST_RANGE);
-      u.on = false;
-    }
+  if (u.on && (src < 0 || src >= k.rows)) {
+    raise_status(k.status, ST_RANGE);
+    u.on = false;
   }
   KvRow8<T> v[kKvHeads];
 #pragma unroll
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
   }
   size_t row = 0;
   uint32_t hr = 0;
-  u.on = u.on && kv_row(k, l.pages[u.layer], u.s, u.i, n, &row, &hr);
+  u.on = u.on && kv_row(k, l.pages[u.layer], u.s, base, u.i, n, &row, &hr);
   row += (size_t)u.head * hr;
   void* dst = u.is_v ? l.dst_v[u.layer] : l.dst_k[u.layer];
   if constexpr (!Q8) {
@@ -240,11 +238,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
   pdl_launch_dependents();
   const KvUnit u(k);
   if (!u.on) return;
-  const int n = k.valid ? min(__ldg(k.valid + u.s), k.rows) : k.rows;
+  const int n = k.valid ? min(__ldg(k.valid + u.s), k.rows) : k.rows, base = __ldg(k.base_pos + u.s);
   if (u.i >= n) return;
   size_t row;
   uint32_t hr;
-  if (!kv_row(k, l.pages[u.layer], u.s, u.i, 0, &row, &hr)) return;
+  if (!kv_row(k, l.pages[u.layer], u.s, base, u.i, 0, &row, &hr)) return;
   row += (size_t)u.head * hr;
   const void* src = u.is_v ? l.src_v[u.layer] : l.src_k[u.layer];
   T* out = reinterpret_cast<T*>(u.is_v ? l.dst_v[u.layer] : l.dst_k[u.layer]) +
