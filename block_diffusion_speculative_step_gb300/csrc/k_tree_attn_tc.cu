@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       const int head = g * grp + (has_row ? qv - node * grp : 0);
       if ((Q8 || !p.q_tma) && (NT == 2 || t == 0)) {
         // ---- the thread's row of the query tile: loaded where it is no TMA
-        // box, scaled to fp16 in place with an 8-bit cache
+        // box, split into e4m3 codes in place with an 8-bit cache
         uint8_t* qd = Qs + (NT == 2 ? t * TILE : 0);
         if (p.q_tma) {
           wait(&sh->qraw[NT == 2 ? t : 0], (uint32_t)seg_no);
