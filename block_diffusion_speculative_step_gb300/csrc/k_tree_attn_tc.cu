@@ -20,7 +20,7 @@
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
 // With NT = 2 the streams' softmaxes take turns, so that one stream's products
 // run beside the other's softmax (left alone both fall in step and wait for
-// their products together: 196 us instead of 162 for 32 sequences x 64 rows,
+// their products together: 196 us instead of 160 for 32 sequences x 64 rows,
 // 8k, bf16; 8-bit, whose softmax is longer, they overlap from the second
 // quarter of a chunk on, 259 us against 291 in strict turns).  The reference m stays while the weights' sum
 // suits the 16-bit type, so the usual chunk needs no maximum and no rescaling
@@ -53,7 +53,7 @@
 // 2^(e_row - E), E the chunk's largest exponent, exact but for rows 2^-15 and
 // more below it (whose low bits, 2^-24 of the chunk's largest element, go); E
 // joins the exponent of P.  (Rewriting K as well made each chunk's scores
-// wait for a conversion: 365 us where this takes 260, 32 sequences x 64 rows
+// wait for a conversion: 365 us where this takes 243, 32 sequences x 64 rows
 // over 8k contexts.)  Two codes for P as well would spare V's conversion but
 // cost the softmax, which has no time to spare, a second rounding per weight.
 //
