@@ -22,12 +22,13 @@
 // run beside the other's softmax (left alone both fall in step and wait for
 // their products together: 196 us instead of 160 for 32 sequences x 64 rows,
 // 8k, bf16; 8-bit, whose softmax is longer, they overlap from the second
-// quarter of a chunk on, 259 us against 291 in strict turns).  The reference m stays while the weights' sum
-// suits the 16-bit type, so the usual chunk needs no maximum and no rescaling
-// of O: bf16, which has fp32's exponents, starts at m = 0 and takes sums of
-// 2^-60 .. 2^60; fp16 (8-bit cache) starts at the first chunk's maximum and
-// takes sums up to 2^15.  Otherwise the chunk is done again with its maximum:
-// the scores stay until the sum is known.
+// quarter of a chunk on, 259 us against 291 in strict turns).  The reference m
+// stays while the weights' sum suits the 16-bit type, so the usual chunk needs
+// no maximum and no rescaling of O: bf16, which has fp32's exponents, starts
+// at m = 0 and takes sums of 2^-60 .. 2^60; fp16 (8-bit cache) starts at the
+// first chunk's maximum and takes sums up to 2^15.  Otherwise the part of the
+// chunk (a half; 8-bit a quarter) is done again with its maximum: its scores
+// stay until its sum is known.
 //
 // Roles: warp 0 K/V copies; warps 1, 2 the products of stream 0, 1 (a job's
 // waits and commits take about 600 cycles of one thread, so each stream has a
