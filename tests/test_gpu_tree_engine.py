@@ -252,3 +252,49 @@ def test_two_calls_at_once():
                 p.run()
     for p in ps:
         p.check()
+
+
+@pytest.mark.parametrize("cache,cap", [("bf16", 2_200_064), ("e4m3", 4_400_128)])
+def test_offsets_past_32_bits(cache, cap):
+    """A cache whose last heads lie more than 2^32 bytes in: the attention over
+    it, and rows written to its last slots and read back."""
+    nkv, d, n = 8, 128, 200
+    p = Tree([n], trees(3, [9], 9), 16, nkv, d, "bf16", cache, cap=256)
+    big = {}
+    for x in ("k", "v", "ke", "ve"):
+        small_x = p.dev[x]
+        if small_x is None:
+            big[x] = None
+            continue
+        big[x] = torch.zeros((1, nkv, cap) + small_x.shape[3:], dtype=small_x.dtype, device="cuda")
+        big[x][:, :, :256] = small_x
+    assert big["k"].numel() * big["k"].element_size() > 1 << 32
+    p.a.kv = R.kv_desc(cap, big["k"], big["v"], big["ke"], big["ve"])
+    p.run()
+    p.check()
+    rows = 3
+    base = torch.tensor([cap - rows], dtype=torch.int32, device="cuda")
+    src = [torch.randn(rows, nkv, d, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in range(2)]
+    out = [torch.zeros_like(x) for x in src]
+    kv = (D.dflash_kv * 1)(p.a.kv)
+    arrays = [R.host_array([x]) for x in (*src, *out)]
+    w, r = D.dflash_kv_write_args(), D.dflash_kv_read_args()
+    for a in (w, r):
+        a.dims, a.n_layers, a.n_seqs, a.rows = p.a.dims, 1, 1, rows
+        a.base_pos, a.kv_layers = R.ptr(base), D.C.cast(kv, D.C.c_void_p)
+    w.kb, w.vb, r.k_out, r.v_out = (D.C.cast(x, D.C.c_void_p) for x in arrays)
+    ws = R.Workspace(D.DFLASH_OP_KV_WRITE, w)
+    D.dflash_kv_write(w, ws.ptr, ws.bytes)
+    D.dflash_kv_read(r, ws.ptr, ws.bytes)
+    torch.cuda.synchronize()
+    assert ws.status() == D.DFLASH_OK
+    for x, y, c, e in zip(src, out, (big["k"], big["v"]), (big["ke"], big["ve"])):
+        if e is None:
+            assert torch.equal(x, y) and torch.equal(c[0, :, cap - rows:], x.transpose(0, 1))
+            continue
+        for i in range(rows):
+            for g in range(nkv):
+                codes, ex = R.quantise_row(x[i, g].double().cpu().numpy())
+                assert int(e[0, g, cap - rows + i]) == ex
+                np.testing.assert_array_equal(R.E4M3[c[0, g, cap - rows + i].cpu().numpy()], R.E4M3[codes])
+                np.testing.assert_array_equal(y[i, g].double().cpu().numpy(), R.E4M3[codes] * 2.0 ** (ex - 127))
