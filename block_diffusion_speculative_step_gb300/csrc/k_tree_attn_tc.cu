@@ -18,11 +18,12 @@
 //   S = Q K^T        tcgen05.mma, both operands in shared memory
 //   P = 2^(c S - m)  one thread per query vector, written over S as 16-bit
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
-// With NT = 2 the streams' softmaxes take turns, so that one stream's products
-// run beside the other's softmax (left alone both fall in step and wait for
-// their products together: 196 us instead of 160 for 32 sequences x 64 rows,
-// 8k, bf16; 8-bit, whose softmax is longer, they overlap from the second
-// quarter of a chunk on, 259 us against 291 in strict turns).  The reference m
+// With NT = 2 the streams' softmaxes take turns, the next one's from the
+// second part of this one's chunk on, so that one stream's products run beside
+// the other's softmax (left alone both fall in step and wait for their
+// products together).  32 sequences x 64 rows, 8k: 196 us without turns, 160
+// in strict ones, 159 so in bf16; 268, 291, 259 over an 8-bit cache, whose
+// softmax is longer (then; 243 since).  The reference m
 // stays while the weights' sum suits the 16-bit type, so the usual chunk needs
 // no maximum and no rescaling of O: bf16, which has fp32's exponents, starts
 // at m = 0 and takes sums of 2^-60 .. 2^60; fp16 (8-bit cache) starts at the
@@ -1211,7 +1212,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
             if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
-            if (NT == 2 && h + 1 == (Q8 ? 1 : np)) named_arrive(t == 0 ? 7 : 6, 256);
+            if (NT == 2 && h == 0) named_arrive(t == 0 ? 7 : 6, 256);
 #pragma unroll
             for (int i = 0; i < HC / 32; ++i) tmem_st16u(ts + HC / 2 * h + 16 * i, pk[i]);
           }
