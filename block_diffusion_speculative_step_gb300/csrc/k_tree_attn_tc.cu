@@ -16,14 +16,14 @@
 // both hold the same tile and take chunks alternately, and are joined when
 // the segment ends.  Per chunk and stream (128 query vectors x 128 keys):
 //   S = Q K^T        tcgen05.mma, both operands in shared memory
-//   P = 2^(c S - m)  one thread per query vector, written over S as 16-bit
+//   P = 2^(c S - m)  one thread per query vector, written over S
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
-// With NT = 2 the streams' softmaxes take turns, the next one's from the
-// second part of this one's chunk on, so that one stream's products run beside
-// the other's softmax (left alone both fall in step and wait for their
-// products together).  32 sequences x 64 rows, 8k: 196 us without turns, 160
-// in strict ones, 159 so in bf16; 268, 291, 259 over an 8-bit cache, whose
-// softmax is longer (then; 243 since).  The reference m
+// With NT = 2 the streams' softmaxes take turns, so that one stream's products
+// run beside the other's softmax (left alone both fall in step and wait for
+// their products together); over an 8-bit cache, whose softmax is longer, the
+// next one starts from the second part of this one's chunk on.  32 sequences x
+// 64 rows, 8k: 247 us without turns, 187 so, 213 from the second half on in
+// bf16; 258 and 243 in 8 bits.  The reference m
 // stays while the weights' sum suits the 16-bit type, so the usual chunk needs
 // no maximum and no rescaling of O: bf16, which has fp32's exponents, starts
 // at m = 0 and takes sums of 2^-60 .. 2^60; fp16 (8-bit cache) starts at the
@@ -43,9 +43,13 @@
 // instead of 1.6k).  Hence scores in 16-column pieces, and an 8-bit chunk in
 // quarters.
 //
-// P is rounded to 16 bits for its product: bf16 next to a bf16 V (2^-8
-// relative per weight, as the output itself is rounded), fp16 with an 8-bit
-// cache (2^-11).  The sum l uses the unrounded weights.
+// The softmax is no rounding point: next to a bf16 V the weights enter their
+// product as two bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products
+// share V's tile and the accumulator; one rounding to bf16 alone moved outputs
+// by 0.16% (2-norm), as much as their own rounding.  The second product costs
+// 187 us against 160 (32 sequences x 64 rows, 8k).  Starting a half's product
+// beside the other half's weights: 185, and not worth its barriers.  With an
+// 8-bit cache P is fp16 (2^-11).  The sum l uses the unrounded weights.
 //
 // 8-bit cache: K's codes go to the product as they are (kind::f8f6f4, the
 // codes' rate is twice the 16-bit one), with the query vector as the sum of
@@ -60,9 +64,10 @@
 // cost the softmax, which has no time to spare, a second rounding per weight.
 //
 // What bounds it, per 128-key chunk and SM at NT = 2: HBM 2.9k cycles in
-// bf16, 1.5k in 8 bits; the tensor core 2.1k (4 x 8 products of 67 cycles);
-// the softmax 1.6k a stream in turns, 3.3k for both; measured 3.6k in bf16
-// and about 6k in 8 bits, where the scales (two more instructions a pair of
+// bf16, 1.5k in 8 bits; the tensor core 3.2k in bf16 (6 x 8 products of 67
+// cycles), 2.1k in 8 bits; measured 4.1k in bf16 -- a stream's scores, softmax
+// and products are one chain, and the other stream's products stand in its way
+// -- and about 6k in 8 bits, where the scales (two more instructions a pair of
 // scores and four loads) and the conversion share the issue slots.
 #include <math.h>
 
@@ -230,6 +235,19 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
+// The same for the 32 columns r[0 .. 31].
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
 // Packed fp32 pairs (two fused multiply-adds / additions per instruction).
 __device__ __forceinline__ unsigned long long tt_pair(float lo, float hi) {
   unsigned long long r;
@@ -271,6 +289,16 @@ __device__ __forceinline__ uint32_t tt_pack(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
+}
+
+// The pair (lo, hi) as bf16 values h and the bf16 values l of what they left:
+// h + l carries it to 2^-16 relative (half a step of half a step).
+__device__ __forceinline__ void tt_split_bf16(float lo, float hi, uint32_t& h, uint32_t& l) {
+  h = tt_pack<false>(lo, hi);
+  const unsigned long long r = tt_fma2(tt_pair(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)),
+                                       tt_pair(-1.f, -1.f), tt_pair(lo, hi));
+  tt_unpair(r, lo, hi);
+  l = tt_pack<false>(lo, hi);
 }
 
 // Byte offset of (row, 16-byte piece) in a 16-bit tile of 128 rows kept as
@@ -810,7 +838,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         if (tt_elect()) {
 #pragma unroll
           for (int j = 0; j < kTtCH / 16; ++j)  // (16 keys a step; of a short chunk only those that hold some)
-            if (16 * j < nk) mma_ts(tm_o, tm_s + 8 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+            if (16 * j < nk) {
+              mma_ts(tm_o, tm_s + (Q8 ? 8 : 16) * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+              if (!Q8) mma_ts(tm_o, tm_s + 16 * j + 8, v + (uint64_t)(j * 128), idV, 1u);  // what P's first part left
+            }
           // the stream's last job of the segment: its output is complete
           if (last) {
             tc::mma_commit(&sh->ofull[t]);
@@ -1048,6 +1079,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return w;
           };
           constexpr int W = 16, HC = Q8 ? 32 : 64;  // columns per step, per part
+          constexpr int PC = Q8 ? W / 2 : W;        // columns of P per step (bf16: first parts, then what they left)
           auto hide = [&](float (&x)[W], int i) {  // columns W i ..
             if (masked) {
               const uint32_t w = seen(i * W >> 5) >> (W * i & 31);
@@ -1094,7 +1126,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           };
           unsigned long long sa, sb;
-          // weights 2^(scale x + m0) of a step, packed, and their sums; `next` starts
+          // weights 2^(scale x + m0) of a step, as the product takes them, and their sums; `next` starts
           // the next step's loads once the scores have been taken
           auto piece = [&](float (&x)[W], const Scales& f, uint32_t* pk, float m0, auto next) {
             const unsigned long long m2 = tt_pair(m0, m0);
@@ -1110,30 +1142,33 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               hi = tt_ex2(hi);
               if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
               else sa = tt_add2(sa, tt_pair(lo, hi));
-              pk[k] = tt_pack<Q8>(lo, hi);
+              if constexpr (Q8) pk[k] = tt_pack<true>(lo, hi);
+              else tt_split_bf16(lo, hi, pk[k], pk[W / 2 + k]);
             }
           };
-          // the weights of the chunk's first n columns, packed in n / 2
+          // the weights of the chunk's first n keys
           auto rescale_p = [&](float f, int n) {
             if (!__any_sync(0xffffffffu, f != 1.f)) return;
 #pragma unroll 1
-            for (int q = 0; q < n / 32; ++q) {
+            for (int q = 0; q < n * PC / (16 * W); ++q) {
               float w[16];
               uint32_t v[16];
               tc::tmem_ld16(ts + 16 * q, w);
+              if constexpr (Q8) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const uint32_t u = __float_as_uint(w[k]);
-                float lo, hi;
-                if constexpr (Q8) {
+                for (int k = 0; k < 16; ++k) {
+                  const uint32_t u = __float_as_uint(w[k]);
                   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u));
-                  lo = y.x;
-                  hi = y.y;
-                } else {
-                  lo = __uint_as_float(u << 16);
-                  hi = __uint_as_float(u & 0xFFFF0000u);
+                  v[k] = tt_pack<true>(y.x * f, y.y * f);
                 }
-                v[k] = tt_pack<Q8>(lo * f, hi * f);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t h = __float_as_uint(w[k]), l = __float_as_uint(w[8 + k]);
+                  const float lo = __uint_as_float(h << 16) + __uint_as_float(l << 16);
+                  const float hi = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
+                  tt_split_bf16(lo * f, hi * f, v[k], v[8 + k]);
+                }
               }
               tmem_st16u(ts + 16 * q, v);
             }
@@ -1172,7 +1207,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           float sum0 = 0.f;
 #pragma unroll 1
           for (int h = 0; h < np; ++h) {
-            uint32_t pk[HC / 32][16];
+            uint32_t pk[HC / W * PC];
             float sum;
             bool again = false;
 #pragma unroll 1
@@ -1187,7 +1222,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               for (int i = 0; i < HC / W; ++i) {  // the next scores arrive while these are exponentiated
                 tmem_wait(x);
                 hide(x, h * (HC / W) + i);
-                piece(x, f, pk[i * W >> 5] + (i * W / 2 & 15), m0, [&]() {
+                piece(x, f, pk + i * PC, m0, [&]() {
                   if (i + 1 < HC / W) {
                     tmem_ld_async(ts + HC * h + W * (i + 1), x);
                     load_kf(h * (HC / W) + i + 1, f);
@@ -1212,9 +1247,13 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
             if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
-            if (NT == 2 && h == 0) named_arrive(t == 0 ? 7 : 6, 256);
+            if (NT == 2 && h == (Q8 ? 0 : np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
+            if constexpr (Q8) {
+              tmem_st16u(ts + HC / 2 * h, pk);
+            } else {
 #pragma unroll
-            for (int i = 0; i < HC / 32; ++i) tmem_st16u(ts + HC / 2 * h + 16 * i, pk[i]);
+              for (int i = 0; i < HC; i += 32) tmem_st32u(ts + HC * h + i, pk + i);
+            }
           }
           l_run += Q8 ? tt_scale(sum0, -dv) : sum0;
         } else if constexpr (NT == 2) {

@@ -1,0 +1,114 @@
+"""dflash_tree_attention held to fp32-like weights: cancelling values, so that
+the output's own rounding does not cover the weights' errors."""
+import numpy as np
+import pytest
+import torch
+
+from tests import tree_ref as R
+from tests.test_gpu_tree_attn import FILL, Tree, trees
+
+pytestmark = pytest.mark.gpu
+
+
+def rel_bound(p, s, i):
+    """Row i's bound, per query head: the relative error of a weight p_j / sum, plus what
+    the sum over p_j v_j adds to it (against sum_j p_j |v_j|):
+      score        fp32 sums of d products of each operand's one or two parts:
+                   at most 4 d additions and 8 roundings of scaling and
+                   argument, each 2^-23 of sum |q k| scale (truncation counted);
+                   with an 8-bit cache also queries' and tree keys' elements
+                   held to 2^-10 of a scale that takes their largest to 224 at
+                   least;
+      exponential  2^-22, twice (weight and sum);
+      split        hi + lo of a weight in bf16: 2^-8 of 2^-8;
+      sums         n weights, 2 n products: 2^-23 each;
+      rescalings   eight roundings of 2^-23: 2^-20."""
+    n, grp, sc = p.lens[s] + p.rows, p.nq // p.nkv, p.scale or p.d ** -0.5
+    see = sorted(R.sees(p.parents[s])[i])
+    q = p.q[s * p.rows + i].double().view(p.nq, p.d).abs()
+    kb = p.kb[s * p.rows:(s + 1) * p.rows].double().abs()[see]  # [visible][nkv][d]
+    k = torch.cat([p.ctx["k"][s].double().abs(), kb.transpose(0, 1)], 1).repeat_interleave(grp, 0)
+    eps = (4 * p.d + 8) * 2.0 ** -23 * torch.einsum("hd,hnd->hn", q, k).amax(-1) * sc
+    if p.cache == "e4m3" and p.dtype == "bf16":
+        dl = 2.0 ** -10 / 224
+        kt = kb.transpose(0, 1).repeat_interleave(grp, 0)
+        eps = eps + dl * sc * (q.amax(-1) * k.sum(-1).amax(-1) + kt.amax((1, 2)) * q.sum(-1))
+    rel = torch.expm1(2 * eps) + 2 * 2.0 ** -22 + 2.0 ** -16 + 3 * n * 2.0 ** -23 + 2.0 ** -20
+    return rel.numpy()[:, None]
+
+
+def check(p, skip=()):
+    torch.cuda.synchronize()
+    assert p.ws.status() == 0
+    got = p.out.cpu().double().view(p.S, p.rows, p.nq, p.d).numpy()
+    sc = p.scale or p.d ** -0.5
+    rnd = 2.0 ** -8 if p.dtype == "bf16" else 2.0 ** -24
+    for s in range(p.S):
+        sl = slice(s * p.rows, (s + 1) * p.rows)
+        out, mag, _ = R.attention(p.q[sl].double().view(p.rows, p.nq, p.d).numpy(), p.ctx["k"][s].double().numpy(),
+                                  p.ctx["v"][s].double().numpy(), p.kb[sl].double().numpy(), p.vb[sl].double().numpy(),
+                                  p.parents[s], sc)
+        for i in range(p.rows):
+            if (s, i) in skip:
+                continue
+            if np.isnan(out[i]).all():
+                assert (got[s, i] == FILL).all(), (s, i, "a padding row was written")
+                continue
+            tol = (rnd * np.abs(out[i]) + rel_bound(p, s, i) * mag[i]) * (1 + rnd)
+            err = np.abs(got[s, i] - out[i])
+            assert (err <= tol).all(), (s, i, float((err / tol).max()))
+
+
+def cancel(p):
+    """Slots 2 j + 1 of every context repeat 2 j with one dimension of the key
+    negated (another, near weight) and the value negated; small tree values."""
+    for x, dims in (("k", [5]), ("v", list(range(p.d)))):
+        t = p.dev[x]
+        for s, n in enumerate(p.lens):
+            m = n // 2 * 2
+            a = t[s, :, 0:m:2].clone()
+            if t.dtype == torch.uint8:
+                a[..., dims] ^= 128
+                p.dev[x + "e"][s, :, 1:m:2] = p.dev[x + "e"][s, :, 0:m:2]
+            else:
+                a[..., dims] = -a[..., dims]
+            t[s, :, 1:m:2] = a
+            b = p.ctx[x][s][:, 0:m:2].clone()
+            b[..., dims] = -b[..., dims]
+            p.ctx[x][s][:, 1:m:2] = b
+    p.vb = (p.vb.float() * 2.0 ** -6).to(p.dt)
+    p.vb_d.copy_(p.vb)
+
+
+CACHES = ["bf16"]
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nkv,rows", [(8, 2, 5), (16, 2, 17), (7, 1, 40), (4, 4, 33)])
+def test_weights_keep_their_digits(cache, d, nq, nkv, rows):
+    p = Tree([2, 6, 20, 44, 0], trees(d + nq, [rows, 1, rows, max(1, rows - 2), 3], rows), nq, nkv, d, "bf16", cache,
+             q_amp=0.1, seed=rows)
+    cancel(p)
+    p.run()
+    check(p)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("nq,rows", [(4, 9), (16, 33)])
+def test_weights_keep_their_digits_over_many_chunks(cache, nq, rows):
+    """Contexts cut into pieces of several CTAs, joined from their partials."""
+    p = Tree([130, 1400, 260], trees(nq, [rows] * 3, rows), nq, 2, 128, "bf16", cache, q_amp=0.1, seed=rows)
+    cancel(p)
+    p.run()
+    check(p)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("nq,rows", [(4, 9), (16, 33)])
+def test_scores_that_move_the_reference(cache, nq, rows):
+    """Scores of a few hundred, growing along the context: the reference of the
+    weights moves, and with it what is already summed."""
+    p = Tree([400, 261], trees(nq + 1, [rows] * 2, rows), nq, 2, 64, "bf16", cache, q_amp=4.0, scale=0.5, seed=rows)
+    p.run()
+    check(p)
