@@ -20,14 +20,13 @@
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
 // With NT = 2 the streams' softmaxes take turns, so that one stream's products
 // run beside the other's softmax (left alone both fall in step and wait for
-// their products together); over an 8-bit cache, whose softmax is longer, the
-// next one starts from the second part of this one's chunk on.  32 sequences x
-// 64 rows, 8k: 247 us without turns, 187 so, 213 from the second half on in
-// bf16; 258 and 243 in 8 bits.  The reference m
-// stays while the weights' sum suits the 16-bit type, so the usual chunk needs
-// no maximum and no rescaling of O: bf16, which has fp32's exponents, starts
-// at m = 0 and takes sums of 2^-60 .. 2^60; fp16 (8-bit cache) starts at the
-// first chunk's maximum and takes sums up to 2^15.  Otherwise the part of the
+// their products together): the next one starts after this one's second part
+// (bf16: its last; 8-bit, whose softmax is longer: of four).  32 sequences x 64
+// rows, 8k: 247 us without turns, 183 so, 213 from the second half on in bf16;
+// after one, two, three, four quarters 281, 261, 268, 282 in 8 bits.
+// The reference m stays while the weights' sum suits bf16, which has fp32's
+// exponents: it starts at m = 0 and takes sums of 2^-60 .. 2^60, so the usual
+// chunk needs no maximum and no rescaling of O.  Otherwise the part of the
 // chunk (a half; 8-bit a quarter) is done again with its maximum: its scores
 // stay until its sum is known.
 //
@@ -43,32 +42,30 @@
 // instead of 1.6k).  Hence scores in 16-column pieces, and an 8-bit chunk in
 // quarters.
 //
-// The softmax is no rounding point: next to a bf16 V the weights enter their
-// product as two bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products
-// share V's tile and the accumulator; one rounding to bf16 alone moved outputs
-// by 0.16% (2-norm), as much as their own rounding.  The second product costs
-// 187 us against 160 (32 sequences x 64 rows, 8k).  Starting a half's product
-// beside the other half's weights: 185, and not worth its barriers.  With an
-// 8-bit cache P is fp16 (2^-11).  The sum l uses the unrounded weights.
+// The softmax is no rounding point: the weights enter their product as two
+// bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products share V's tile
+// and the accumulator; one rounding to bf16 alone moved outputs by 0.16%
+// (2-norm), as much as their own rounding.  The second product costs 183 us
+// against 160 (32 sequences x 64 rows, 8k).  Starting a part's product beside
+// the next part's weights: 185, and not worth its barriers.  The sum l uses the
+// unrounded weights.
 //
 // 8-bit cache: K's codes go to the product as they are (kind::f8f6f4, the
 // codes' rate is twice the 16-bit one), with the query vector as the sum of
 // two e4m3 codes an element (4 + 4 significant bits hold bf16's 8; see
 // tt_split8) and the tree's keys as two codes too; the keys' scales 2^e are
-// multiplied to the scores.  V is rewritten to fp16 by four warps: code *
-// 2^(e_row - E), E the chunk's largest exponent, exact but for rows 2^-15 and
-// more below it (whose low bits, 2^-24 of the chunk's largest element, go); E
-// joins the exponent of P.  (Rewriting K as well made each chunk's scores
-// wait for a conversion: 365 us where this takes 243, 32 sequences x 64 rows
-// over 8k contexts.)  Two codes for P as well would spare V's conversion but
-// cost the softmax, which has no time to spare, a second rounding per weight.
+// multiplied to the scores.  V is rewritten to bf16 by four warps: code * 2^e,
+// exact whatever the rows' exponents.  (As fp16, over a scale per chunk, small
+// rows beside large ones -- hidden rows and padding among the tree's -- lost
+// their digits or vanished: 243 us where this takes 265.  Rewriting K as well
+// made each chunk's scores wait for a conversion: 365 against 243.)
 //
 // What bounds it, per 128-key chunk and SM at NT = 2: HBM 2.9k cycles in
-// bf16, 1.5k in 8 bits; the tensor core 3.2k in bf16 (6 x 8 products of 67
-// cycles), 2.1k in 8 bits; measured 4.1k in bf16 -- a stream's scores, softmax
-// and products are one chain, and the other stream's products stand in its way
-// -- and about 6k in 8 bits, where the scales (two more instructions a pair of
-// scores and four loads) and the conversion share the issue slots.
+// bf16, 1.5k in 8 bits; the tensor core 3.2k (6 x 8 products of 67
+// cycles); measured 4.1k in bf16 -- a stream's scores, softmax and products are
+// one chain, and the other stream's products stand in its way -- and about 6.4k
+// in 8 bits, where the chain has the scales' loads and multiplications in it and
+// 128 registers a thread leave little in flight.
 #include <math.h>
 
 #include "common.cuh"
@@ -126,19 +123,17 @@ struct TtCfg {
 };
 
 struct TtShared {  // after the tiles
-  float xm[2][128], xl[2][128], xu[2][128];  // a segment's stream statistics (NT = 1): maximum, sum, unit of O
+  float xm[2][128], xl[2][128];  // a segment's stream statistics (NT = 1): maximum, sum
   int par[DFLASH_MAX_TREE];
   uint32_t mask[4][DFLASH_MAX_TREE][4];      // the tree rows' ancestors and themselves (none: padding)
   float kf[4][kTtCH];             // 8-bit: the keys' scales 2^e, by chunk counter (two V slots keep the converters at most 3 ahead)
-  int ev[kTtRing];                // 8-bit: the chunk's V exponent
   uint32_t badv[kTtRing][4];      // tree rows whose V holds a NaN or infinity, by chunk counter
-  int cmax[2][4];                 // converters: the warps' maxima, by chunk & 1
-  __half2 fac[128];               // converters: the V rows' factors
+  float fac[2][kTtCH];            // converters: the V rows' scales 2^e, by chunk & 1
   int s0, it0, c0, len, n0;       // the CTA's run: first item, position in it, number of positions; context of s0
   int setup;
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t rvfull[2], rvempty[2];
-  uint64_t kfr[kTtRing];          // kf and ev written
+  uint64_t kfr[kTtRing];          // kf written
   uint64_t tkfull[2], tkempty;    // the tree's K tiles (NT = 1: by the stream that takes them)
   uint64_t sfull[2], pdone[2], ofull[2], qraw[2], qfull[2], qfree[2];
   uint64_t mready[4];             // ancestor masks written, by buffer
@@ -199,11 +194,9 @@ __device__ __forceinline__ uint32_t tt_off8(int row, int ch) {
   return ROW == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
 }
 
-// kind::f16 with both operands fp16 (type code 0) instead of bf16 (1).
-template <bool F16>
-__host__ __device__ constexpr uint32_t tt_idesc(int M, int N, bool b_mn) {
-  const uint32_t base = b_mn ? tc::idesc_bf16_f32_bmn(M, N) : tc::idesc_bf16_f32(M, N);
-  return F16 ? base & ~((7u << 7) | (7u << 10)) : base;
+// Both operands e4m3 (type code 0 of kind::f8f6f4) instead of bf16 (1 of kind::f16).
+__host__ __device__ constexpr uint32_t tt_idesc_e4m3(int M, int N) {
+  return tc::idesc_bf16_f32(M, N) & ~((7u << 7) | (7u << 10));
 }
 
 // 16 columns of this thread's lane, not waited for: the registers hold them
@@ -280,25 +273,19 @@ __device__ __forceinline__ float tt_ex2(float x) {
   return y;
 }
 
-template <bool F16>
 __device__ __forceinline__ uint32_t tt_pack(float lo, float hi) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The pair (lo, hi) as bf16 values h and the bf16 values l of what they left:
 // h + l carries it to 2^-16 relative (half a step of half a step).
 __device__ __forceinline__ void tt_split_bf16(float lo, float hi, uint32_t& h, uint32_t& l) {
-  h = tt_pack<false>(lo, hi);
+  h = tt_pack(lo, hi);
   const unsigned long long r = tt_fma2(tt_pair(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)),
                                        tt_pair(-1.f, -1.f), tt_pair(lo, hi));
   tt_unpair(r, lo, hi);
-  l = tt_pack<false>(lo, hi);
+  l = tt_pack(lo, hi);
 }
 
 // Byte offset of (row, 16-byte piece) in a 16-bit tile of 128 rows kept as
@@ -371,8 +358,8 @@ struct Seg {
 //            tt_setup positions before its chunks', for what it costs besides
 //            them (queries, masks, first chunk, output: about 8k cycles, and
 //            an 8-bit cache's conversion of queries and tree).  32 sequences
-//            x 64 rows, 8k: 1 / 2 / 3 positions 167 / 159 / 161 us in bf16, 271
-//            / 252 / 243 us in 8 bits;
+//            x 64 rows, 8k: 1 / 2 / 3 positions 190 / 186 / 187 us in bf16, 279
+//            / 265 / 266 us in 8 bits;
 //   aligned  an item's chunks are cut into runs of `per` and every run has a
 //            CTA of its own, per the smallest for which nb CTAs suffice: no
 //            CTA has parts of two items, which costs a second query load,
@@ -483,21 +470,6 @@ __device__ __forceinline__ Spot tt_run(const TreeAttnDesc& a, int ips, int b, co
   return p;
 }
 
-// Scale 2^d as fp16 (d <= 0; 0 below the subnormals).
-__device__ __forceinline__ __half2 tt_half_pow2(int d) {
-  const uint32_t h = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-  const uint32_t w = h | (h << 16);
-  return *reinterpret_cast<const __half2*>(&w);
-}
-
-// Exponent e with |x| * 2^-e <= 2^8 for |x| up to mx, at least -120.
-__device__ __forceinline__ int tt_exp_of(float mx) {
-  if (!(mx > 0.f)) return -120;
-  int k;
-  frexpf(mx, &k);
-  return max(k - 8, -120);
-}
-
 // x * 2^e for |e| <= 250 (two factors: one alone may leave the fp32 range).
 __device__ __forceinline__ float tt_scale(float x, int e) {
   const int h = e / 2;
@@ -520,7 +492,7 @@ __device__ __forceinline__ int tt_exp8_of(float mx) {
 // Eight elements over 2^e as the sum of two e4m3 codes each: 4 significant
 // bits, then 4 of what is left.  A bf16's 8 are kept down to 2^-10 of the
 // largest element's power of two; below, the second code's smallest step bounds
-// the error by 2^-18 of the largest.  NaN and infinite elements give NaN.
+// the error by 2^-10 / 224 of the largest.  NaN and infinite elements give NaN.
 __device__ __forceinline__ void tt_split8(const float (&v)[8], int e, uint2& hi, uint2& lo) {
   const float s = __int_as_float((127 - e) << 23);
   uint32_t h[4], l[4];
@@ -537,27 +509,41 @@ __device__ __forceinline__ void tt_split8(const float (&v)[8], int e, uint2& hi,
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
-// Eight elements scaled by 2^-e to fp16.
-__device__ __forceinline__ uint4 tt_to_half(const float (&v)[8], int e) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = tt_pack<true>(tt_scale(v[2 * i], -e), tt_scale(v[2 * i + 1], -e));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 16 e4m3 codes times f -> 16 fp16 values (two 16-byte pieces).
-__device__ __forceinline__ void tt_codes_to_half(const uint4& c, __half2 f, uint4& lo, uint4& hi) {
+// 16 e4m3 codes times f -> 16 bf16 values (two 16-byte pieces): exact, for a
+// code has 4 significant bits and f is a power of two.
+__device__ __forceinline__ void tt_codes_to_bf16(const uint4& c, float f, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const unsigned long long f2 = tt_pair(f, f);
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-    const __half2 m = __hmul2(__half2(h), f);
-    o[i] = *reinterpret_cast<const uint32_t*>(&m);
+    const float2 x = __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3)));
+    float a, b;
+    tt_unpair(tt_mul2(tt_pair(x.x, x.y), f2), a, b);
+    o[i] = tt_pack(a, b);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Bits 15 and 31: a bf16 element whose exponent is all ones (NaN or infinite).
+__device__ __forceinline__ uint32_t tt_odd(const uint4& x) {
+  const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+  uint32_t odd = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  return odd;
+}
+// Those elements cleared.
+__device__ __forceinline__ uint4 tt_clear_odd(const uint4& x) {
+  uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+    if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
+  }
+  return make_uint4(e[0], e[1], e[2], e[3]);
 }
 
 // Where a segment's partial lies: slot 0 of CTA b when the item began in an
@@ -744,8 +730,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     // stream: a job's waits and commits (about 700 cycles in one thread) then
     // run beside the other stream's.
     const int t = warp - 1;
-    constexpr uint32_t idS = tt_idesc<Q8>(kTtRows, kTtCH, false);  // (8-bit: e4m3 has fp16's type code)
-    constexpr uint32_t idV = tt_idesc<Q8>(kTtRows, D, true);
+    constexpr uint32_t idS = Q8 ? tt_idesc_e4m3(kTtRows, kTtCH) : tc::idesc_bf16_f32(kTtRows, kTtCH);
+    constexpr uint32_t idV = tc::idesc_bf16_f32_bmn(kTtRows, D);
     const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
     const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + (NT == 2 ? ut * TILE : 0u)),
                    dk = tt_sdesc<Q8 ? D : 128>(tc::smem_u32(Ks)), dt = tt_sdesc<Q8 ? D : 128>(tc::smem_u32(Ts)),
@@ -839,8 +825,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
 #pragma unroll
           for (int j = 0; j < kTtCH / 16; ++j)  // (16 keys a step; of a short chunk only those that hold some)
             if (16 * j < nk) {
-              mma_ts(tm_o, tm_s + (Q8 ? 8 : 16) * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
-              if (!Q8) mma_ts(tm_o, tm_s + 16 * j + 8, v + (uint64_t)(j * 128), idV, 1u);  // what P's first part left
+              mma_ts(tm_o, tm_s + 16 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+              mma_ts(tm_o, tm_s + 16 * j + 8, v + (uint64_t)(j * 128), idV, 1u);  // what P's first part left
             }
           // the stream's last job of the segment: its output is complete
           if (last) {
@@ -920,30 +906,17 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           uint8_t* vt = Vs + slot * TILE;
           auto at = [&](int i) { return reinterpret_cast<uint4*>(vt + tt_off(i / CPR, i % CPR)); };
           if (tree) {
-            auto odd_of = [](const uint4& x) {  // bits 15, 31: an exponent of all ones
-              const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-              uint32_t odd = 0u;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              return odd;
-            };
             uint32_t any = 0u;
 #pragma unroll 8
-            for (int i = lane; i < nk * CPR; i += 32) any |= odd_of(*at(i));
+            for (int i = lane; i < nk * CPR; i += 32) any |= tt_odd(*at(i));
             if (lane < 4) sh->badv[vc % kTtRing][lane] = 0u;
             __syncwarp();
             if (__any_sync(0xffffffffu, any != 0u)) {
 #pragma unroll 1
               for (int i = lane; i < nk * CPR; i += 32) {
                 const uint4 x = *at(i);
-                if (odd_of(x)) {
-                  uint32_t e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-                    if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0xFFFFu;
-                  }
-                  *at(i) = make_uint4(e[0], e[1], e[2], e[3]);
+                if (tt_odd(x)) {
+                  *at(i) = tt_clear_odd(x);
                   atomicOr(&sh->badv[vc % kTtRing][i / CPR >> 5], 1u << (i / CPR & 31));
                 }
               }
@@ -1028,7 +1001,6 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
       const bool has_tree = sg.c1 == sg.nch;  // the segment ends with the tree's rows
       const int tree_ring = (cc + sg.c1 - 1 - sg.c0) % kTtRing;
       float m_run = -INFINITY, l_run = 0.f;
-      int e_run = 0;      // O is kept in units of 2^e_run (8-bit cache)
       const int nj0 = nj;
       uint32_t tm[4] = {0u, 0u, 0u, 0u};  // the row's own ancestors, once the tree's chunk comes
       auto load_mask = [&]() {
@@ -1057,19 +1029,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         __syncwarp();
         tc::tc_fence_after();
         float cs = a.scale;  // score scale (log2 units)
-        int dv = 0;          // exponent of the chunk's V against O's unit
-        int up = 0;          // how far O's unit moves first
-        if constexpr (Q8) {
-          cs = tt_scale(a.scale, sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
-          const int ev = sh->ev[cc % kTtRing];
-          if (nj == nj0) e_run = ev;
-          dv = ev - e_run;
-          if (dv > 6) {  // P reaches 2^(8 + dv): fp16 holds 2^15
-            up = dv;
-            e_run = ev;
-            dv = 0;
-          }
-        }
+        if constexpr (Q8) cs = tt_scale(a.scale, sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
         if (warp_on) {
           // keys 32 i .. of the chunk that the row sees, as bits
           auto seen = [&](int i) {
@@ -1079,7 +1039,6 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return w;
           };
           constexpr int W = 16, HC = Q8 ? 32 : 64;  // columns per step, per part
-          constexpr int PC = Q8 ? W / 2 : W;        // columns of P per step (bf16: first parts, then what they left)
           auto hide = [&](float (&x)[W], int i) {  // columns W i ..
             if (masked) {
               const uint32_t w = seen(i * W >> 5) >> (W * i & 31);
@@ -1126,7 +1085,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           };
           unsigned long long sa, sb;
-          // weights 2^(scale x + m0) of a step, as the product takes them, and their sums; `next` starts
+          // weights 2^(scale x + m0) of a step, as the product takes them (W / 2
+          // columns of their first parts, then what those left), and their sums; `next` starts
           // the next step's loads once the scores have been taken
           auto piece = [&](float (&x)[W], const Scales& f, uint32_t* pk, float m0, auto next) {
             const unsigned long long m2 = tt_pair(m0, m0);
@@ -1142,33 +1102,23 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               hi = tt_ex2(hi);
               if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
               else sa = tt_add2(sa, tt_pair(lo, hi));
-              if constexpr (Q8) pk[k] = tt_pack<true>(lo, hi);
-              else tt_split_bf16(lo, hi, pk[k], pk[W / 2 + k]);
+              tt_split_bf16(lo, hi, pk[k], pk[W / 2 + k]);
             }
           };
           // the weights of the chunk's first n keys
           auto rescale_p = [&](float f, int n) {
             if (!__any_sync(0xffffffffu, f != 1.f)) return;
 #pragma unroll 1
-            for (int q = 0; q < n * PC / (16 * W); ++q) {
+            for (int q = 0; q < n / 16; ++q) {
               float w[16];
               uint32_t v[16];
               tc::tmem_ld16(ts + 16 * q, w);
-              if constexpr (Q8) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const uint32_t u = __float_as_uint(w[k]);
-                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u));
-                  v[k] = tt_pack<true>(y.x * f, y.y * f);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t h = __float_as_uint(w[k]), l = __float_as_uint(w[8 + k]);
-                  const float lo = __uint_as_float(h << 16) + __uint_as_float(l << 16);
-                  const float hi = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
-                  tt_split_bf16(lo * f, hi * f, v[k], v[8 + k]);
-                }
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t h = __float_as_uint(w[k]), l = __float_as_uint(w[8 + k]);
+                const float lo = __uint_as_float(h << 16) + __uint_as_float(l << 16);
+                const float hi = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
+                tt_split_bf16(lo * f, hi * f, v[k], v[8 + k]);
               }
               tmem_st16u(ts + 16 * q, v);
             }
@@ -1194,11 +1144,6 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             m_run = m_new;
             return alpha;
           };
-          if (Q8 && (nj == nj0 || up)) {  // (fp16 needs a reference near a row's maximum)
-            const float alpha = refer(0, (nk + W - 1) / W);
-            rescale(up ? tt_scale(alpha, -up) : alpha);
-            l_run *= alpha;
-          }
           // A part of a chunk at a time, whose weights stay in registers until
           // their sum shows that the reference suits them.  (8-bit: 16 warps'
           // 128 registers hold a quarter; what spills goes to L2, for shared
@@ -1207,12 +1152,12 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           float sum0 = 0.f;
 #pragma unroll 1
           for (int h = 0; h < np; ++h) {
-            uint32_t pk[HC / W * PC];
+            uint32_t pk[HC];
             float sum;
             bool again = false;
 #pragma unroll 1
             for (;;) {
-              const float m0 = m_run == -INFINITY ? (float)dv : (float)dv - m_run;
+              const float m0 = m_run == -INFINITY ? 0.f : -m_run;
               sa = sb = tt_pair(0.f, 0.f);
               float x[W];
               Scales f;
@@ -1222,7 +1167,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               for (int i = 0; i < HC / W; ++i) {  // the next scores arrive while these are exponentiated
                 tmem_wait(x);
                 hide(x, h * (HC / W) + i);
-                piece(x, f, pk + i * PC, m0, [&]() {
+                piece(x, f, pk + i * W, m0, [&]() {
                   if (i + 1 < HC / W) {
                     tmem_ld_async(ts + HC * h + W * (i + 1), x);
                     load_kf(h * (HC / W) + i + 1, f);
@@ -1233,8 +1178,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               tt_unpair(tt_add2(sa, sb), s0, s1);
               sum = s0 + s1;
               // too large for the reference; or a row's first keys, which reference 0 does not suit
-              const bool over = Q8 ? sum > 0x1p15f || (m_run == -INFINITY && sum > 0.f)
-                                   : sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
+              const bool over = sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
               if (again || !__any_sync(0xffffffffu, over)) break;
               again = true;
               const float alpha = refer(h * (HC / W), HC / W);
@@ -1245,17 +1189,13 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 rescale_p(alpha, HC * h);
               }
             }
-            if (!Q8 && !again && m_run == -INFINITY) m_run = 0.f;
+            if (!again && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
-            if (NT == 2 && h == (Q8 ? 0 : np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
-            if constexpr (Q8) {
-              tmem_st16u(ts + HC / 2 * h, pk);
-            } else {
+            if (NT == 2 && h == min(1, np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
 #pragma unroll
-              for (int i = 0; i < HC; i += 32) tmem_st32u(ts + HC * h + i, pk + i);
-            }
+            for (int i = 0; i < HC; i += 32) tmem_st32u(ts + HC * h + i, pk + i);
           }
-          l_run += Q8 ? tt_scale(sum0, -dv) : sum0;
+          l_run += sum0;
         } else if constexpr (NT == 2) {
           named_arrive(t == 0 ? 7 : 6, 256);
         }
@@ -1275,11 +1215,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         if (had[u]) wait(&sh->ofull[u], (uint32_t)no[u]++);
       __syncwarp();
       tc::tc_fence_after();
-      float M = m_run, L = l_run, f_own = Q8 ? tt_scale(1.f, e_run) : 1.f, f_oth = 0.f;
+      float M = m_run, L = l_run, f_own = 1.f, f_oth = 0.f;
       if constexpr (NT == 1) {
         sh->xm[t][r] = m_run;
         sh->xl[t][r] = l_run;
-        sh->xu[t][r] = f_own;
         tc::named_bar(4, 256);
         const float mo = sh->xm[t ^ 1][r], lo = sh->xl[t ^ 1][r];
         M = fmaxf(m_run, mo);
@@ -1287,7 +1226,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         // (both streams' threads form the same sum: stream 0's term first)
         L = t == 0 ? l_run * as + lo * ao : lo * ao + l_run * as;
         f_own *= as;
-        f_oth = ao * sh->xu[t ^ 1][r];
+        f_oth = ao;
       }
       if (warp_on) {
         const bool whole = sg.c0 == 0 && has_tree;
@@ -1349,9 +1288,9 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (write) {
 #pragma unroll
               for (int k = 0; k < W / 8; ++k)
-                out4[col / 8 + k] = make_uint4(tt_pack<false>(o[8 * k], o[8 * k + 1]), tt_pack<false>(o[8 * k + 2], o[8 * k + 3]),
-                                               tt_pack<false>(o[8 * k + 4], o[8 * k + 5]),
-                                               tt_pack<false>(o[8 * k + 6], o[8 * k + 7]));
+                out4[col / 8 + k] = make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
+                                               tt_pack(o[8 * k + 4], o[8 * k + 5]),
+                                               tt_pack(o[8 * k + 6], o[8 * k + 7]));
             }
           } else if (has_row) {
             float4* p4 = reinterpret_cast<float4*>(part) + (size_t)(prow >> 7) * (kTtRows * D / 4);
@@ -1372,57 +1311,45 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     }
     if (NT == 2 && t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
   } else {
-    // ---------------------------------------------------- 8-bit cache: tiles to fp16 operands
+    // ---------------------------------------------------- 8-bit cache: V's codes and the tree's rows to operands
     // (after a wait gave up the loops run on without work, to meet the barriers)
     if constexpr (Q8) {
-      const int ct = tid - 384, cw = warp - 12;
+      const int ct = tid - 384;
       constexpr int LPR = D / 16;                     // lanes per code row (16 codes each)
       constexpr int RPP = 128 / LPR, NP = 128 / RPP;  // rows per pass, passes
       const int cr = ct / LPR, pc = ct % LPR;
       int i = 0, nr = 0, nt = 0;              // chunks, raw chunks, trees
-      int ekn = 0, evn = 0;                   // the next chunk's exponents of row ct
+      float kfn = 1.f, vfn = 0.f;             // the next chunk's scales of row ct
       auto load_exp = [&](int c, int g) {
         bool badp = false;
         const size_t row = (size_t)km.row0(sg.s, c * kTtCH, &badp) + (size_t)g * km.head_rows() + ct;
         const bool in = ct < sg.keys(c);
-        ekn = in ? (int)__ldg(a.k_exp + row) - 127 : 0;
-        evn = in ? (int)__ldg(a.v_exp + row) - 127 : -1000;
-      };
-      // The largest x of the 128 threads, through shared memory.
-      auto group_max = [&](int x) {
-        const int wx = __reduce_max_sync(0xffffffffu, x);
-        if (lane == 0) sh->cmax[i & 1][cw] = wx;
-        tc::named_bar(5, 128);
-        const int* em = sh->cmax[i & 1];
-        return max(max(em[0], em[1]), max(em[2], em[3]));
+        kfn = in ? __int_as_float((int)__ldg(a.k_exp + row) << 23) : 1.f;  // (a hidden key: any finite scale)
+        vfn = in ? __int_as_float((int)__ldg(a.v_exp + row) << 23) : 0.f;
       };
       for (bool on = sg.begin(&a, ips, sh); on; on = sg.next()) {
         const int g = sg.it / p.n_pt;
-        int e_top = -1000;                    // the largest V exponent of the segment so far
         for (int c = sg.c0; c < sg.c1; ++c, ++i) {
           const int nk = sg.keys(c), slot = i % NSV;
           uint8_t* dst = Vs + slot * TILE;
           if (!sg.is_tree(c)) {
             if (c == sg.c0) load_exp(c, g);
-            const int ek = ekn, ev = evn;
+            const float kf = kfn, vf = vfn;
             if (c + 1 < sg.c1 && !sg.is_tree(c + 1)) load_exp(c + 1, g);
-            const int rv = max(group_max(ev), e_top - 30);  // (O's unit never lies 2^30 above a chunk's: see the sums)
-            e_top = max(e_top, rv);
-            sh->kf[i & 3][ct] = __int_as_float((127 + ek) << 23);
-            if (ct == 0) sh->ev[i % kTtRing] = rv;
+            sh->kf[i & 3][ct] = kf;
             tc::mbar_arrive(&sh->kfr[i % kTtRing]);
-            sh->fac[ct] = tt_half_pow2(max(ev - rv, -1000));
+            sh->fac[i & 1][ct] = vf;          // (its readers two chunks ago are past the last chunk's barrier)
             tc::named_bar(5, 128);
             const int rs = nr % Cfg::NRV;
             const uint8_t* raw = Rv + rs * RAW + cr * D + pc * 16;
-            const __half2* fac = sh->fac + cr;
+            const float* fac = sh->fac[i & 1] + cr;
             if (i >= NSV) wait_warp(&sh->vempty[slot], (uint32_t)(i / NSV - 1));
             if (wait_warp(&sh->rvfull[rs], (uint32_t)(nr / Cfg::NRV))) {
               // all reads of the tile before the first write (one warp per
               // scheduler: nothing else hides their latency); rows past the
               // last key zero, their codes may be the NaN code
               uint4 code[NP];
-              __half2 f[NP];
+              float f[NP];
 #pragma unroll
               for (int b = 0; b < NP; ++b) {
                 if (b * RPP >= nk) break;  // (the product reads 16 keys at a time, a pass's rows or half of them)
@@ -1436,7 +1363,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 const int row = b * RPP + cr;
                 uint4 lo, hi;
                 if (row >= nk) code[b] = make_uint4(0, 0, 0, 0);
-                tt_codes_to_half(code[b], f[b], lo, hi);
+                tt_codes_to_bf16(code[b], f[b], lo, hi);
                 *reinterpret_cast<uint4*>(dst + tt_off(row, 2 * pc)) = lo;
                 *reinterpret_cast<uint4*>(dst + tt_off(row, 2 * pc + 1)) = hi;
               }
@@ -1446,8 +1373,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             ++nr;
           } else {
             // the tree's bf16 rows: K as two e4m3 codes with a scale per row, V
-            // with one scale per chunk from its largest finite element.  Eight
-            // 16-byte pieces per thread and round, in flight at once.
+            // as it is.  Eight 16-byte pieces per thread and round, in flight
+            // at once.
             constexpr int CPR = D / 8, RS = 128 / CPR, U = 8, RN = RS * U;  // rows per step, per round
             const size_t rstr = (size_t)a.nkv * D;
             const size_t off = ((size_t)sg.s * a.rows * a.nkv + g) * D + (size_t)(ct / CPR) * rstr + (ct % CPR) * 8;
@@ -1493,22 +1420,9 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&sh->tkfull[NT == 1 ? i & 1 : 0]);
-            ++nt;
-            float mv = 0.f;
-#pragma unroll 1
-            for (int r0 = (nk - 1) / RN * RN; r0 >= 0; r0 -= RN) {  // (the first round stays in registers)
-              load_rows(1, r0);
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                if (r0 + u * RS >= nk) break;
-                float y[8];
-                unpack(x[u], y);
-                mv = fmaxf(mv, tt_finite_max(y));
-              }
-            }
-            const int rv = max(group_max(tt_exp_of(mv)), e_top - 30);
-            if (ct == 0) sh->ev[i % kTtRing] = rv;
             tc::mbar_arrive(&sh->kfr[i % kTtRing]);
+            ++nt;
+            load_rows(1, 0);
             if (ct < 4) sh->badv[i % kTtRing][ct] = 0u;
             tc::named_bar(5, 128);
             if (i >= NSV) wait_warp(&sh->vempty[slot], (uint32_t)(i / NSV - 1));
@@ -1520,18 +1434,12 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 for (int u = 0; u < U; ++u) {
                   const int row = r0 + u * RS + ct / CPR;
                   if (r0 + u * RS >= (nk + 15 & ~15)) break;  // (the product reads 16 keys at a time)
-                  float y[8];
-                  unpack(x[u], y);
                   // a NaN or infinity must not meet a hidden row's weight 0
-                  bool odd = false;
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    if (!(fabsf(y[k]) < INFINITY)) {
-                      y[k] = 0.f;
-                      odd = true;
-                    }
-                  if (odd) atomicOr(&sh->badv[i % kTtRing][row >> 5], 1u << (row & 31));
-                  *reinterpret_cast<uint4*>(dst + tt_off(row, ct % CPR)) = tt_to_half(y, rv);
+                  if (tt_odd(x[u])) {
+                    x[u] = tt_clear_odd(x[u]);
+                    atomicOr(&sh->badv[i % kTtRing][row >> 5], 1u << (row & 31));
+                  }
+                  *reinterpret_cast<uint4*>(dst + tt_off(row, ct % CPR)) = x[u];
                 }
               }
               tc::fence_proxy_async_smem();
@@ -1649,8 +1557,8 @@ __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constan
                                         (size_t)head * D + cg * CW);
 #pragma unroll
   for (int k = 0; k < CW / 8; ++k)
-    out[k] = make_uint4(tt_pack<false>(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack<false>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                        tt_pack<false>(o[8 * k + 4] * inv, o[8 * k + 5] * inv), tt_pack<false>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                        tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv), tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
 }
 
 template <int D, int NT, bool Q8>

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import tree_ref as R
-from tests.test_gpu_tree_attn import FILL, Tree, trees
+from tests.test_gpu_tree_attn import FILL, PAD, TYPES, Tree, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -80,7 +80,7 @@ def cancel(p):
     p.vb_d.copy_(p.vb)
 
 
-CACHES = ["bf16"]
+CACHES = ["bf16", "e4m3"]
 
 
 @pytest.mark.parametrize("cache", CACHES)
@@ -110,5 +110,48 @@ def test_scores_that_move_the_reference(cache, nq, rows):
     """Scores of a few hundred, growing along the context: the reference of the
     weights moves, and with it what is already summed."""
     p = Tree([400, 261], trees(nq + 1, [rows] * 2, rows), nq, 2, 64, "bf16", cache, q_amp=4.0, scale=0.5, seed=rows)
+    p.run()
+    check(p)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("nq,rows", [(4, 9), (16, 33)])
+def test_values_of_very_different_size(dtype, cache, nq, rows):
+    """Rows of V between 2^-25 and 2^25 times the others', those of the tree
+    too: every row counts by its weight times its own size."""
+    p = Tree([0, 3, 200, 390], trees(nq, [rows] * 4, rows), nq, 2, 64, dtype, cache, q_amp=3.0, seed=rows)
+    g = torch.Generator().manual_seed(rows)
+    for s, n in enumerate(p.lens):
+        t = torch.randint(-25, 26, (2, n), generator=g)
+        p.ctx["v"][s] = p.ctx["v"][s].double() * torch.exp2(t.double())[..., None]
+        if cache == "e4m3":
+            p.dev["ve"][s, :, :n] = (p.dev["ve"][s, :, :n].int() + t.cuda()).to(torch.uint8)
+        else:
+            p.dev["v"][s, :, :n] *= torch.exp2(t.float()).cuda()[..., None].to(p.dt)
+    t = torch.randint(-25, 26, (len(p.vb), 2, 1), generator=g)
+    p.vb = (p.vb.float() * torch.exp2(t.float())).to(p.dt)
+    p.vb_d.copy_(p.vb)
+    p.run()
+    check(p)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("big", [1e30, -1e30, 3e4])
+@pytest.mark.parametrize("nq", [4, 64])
+def test_large_finite_rows_reach_their_descendants_only(dtype, cache, big, nq):
+    """Padding rows and rows of other branches may hold any finite number."""
+    par = [-1, 0, 0, 1, 2, 2, PAD]
+    p = Tree([130, 0], [par, par], nq, 2, 128, dtype, cache)
+    for s in (0, 1):
+        for i in (2, 6):  # seen by 2, 4, 5; padding
+            for t in (p.kb, p.kb_d):
+                t[s * 7 + i] = big
+            for t in (p.vb, p.vb_d):
+                t[s * 7 + i, :, 3:70] = big
+    p.run()
+    check(p, skip=[(s, i) for s in (0, 1) for i in (2, 4, 5)])
+    for s in (0, 1):  # the values alone: their descendants too
+        for t in (p.kb, p.kb_d):
+            t[s * 7 + 2] = 0.25
     p.run()
     check(p)
