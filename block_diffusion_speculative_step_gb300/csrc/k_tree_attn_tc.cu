@@ -81,6 +81,7 @@ namespace {
 
 constexpr int kTtCH = 128;      // keys per chunk
 constexpr int kTtRows = 128;    // query vectors per tile
+constexpr int kTtKeyExp = -40;  // 8-bit cache: tree keys' smallest scale (their elements are held to 2^-50)
 constexpr int kTtRing = 8;      // chunks whose scale exponents and bad rows are kept (roles run at most 4 apart)
 
 struct TtTma {
@@ -1029,7 +1030,12 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         __syncwarp();
         tc::tc_fence_after();
         float cs = a.scale;  // score scale (log2 units)
-        if constexpr (Q8) cs = tt_scale(a.scale, sh->qe[seg_no & 3][NT == 2 ? t : 0][r]);
+        // A hidden score is -inf before it is scaled, so no scale may underflow to
+        // 0 (NaN): a query's is 2^-106 at least, next to which scores (sums of
+        // codes below 2^26, times keys' scales) are 0 all the same, and a tree
+        // key's 2^-40 (kTtKeyExp).  (A floor under the products of the two, where
+        // scores are hidden: 277 us instead of 265, 32 sequences x 64 rows, 8k.)
+        if constexpr (Q8) cs = fmaxf(tt_scale(a.scale, sh->qe[seg_no & 3][NT == 2 ? t : 0][r]), 0x1p-106f);
         if (warp_on) {
           // keys 32 i .. of the chunk that the row sees, as bits
           auto seen = [&](int i) {
@@ -1409,7 +1415,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 float m = tt_finite_max(y);
 #pragma unroll
                 for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int e = tt_exp8_of(m);
+                const int e = max(tt_exp8_of(m), kTtKeyExp);
                 uint2 hi, lo;
                 tt_split8(y, e, hi, lo);
                 uint8_t* q = Ts + tt_off8<D>(row, (ct % CPR) >> 1) + (ct & 1) * 8;

@@ -508,8 +508,8 @@ int dflash_sample_accept(const dflash_sample_accept_args* a, void* ws, size_t ws
  * The softmax runs in fp32.  With bf16 the probabilities enter their product
  * with the values as two bf16 terms (2^-16 relative).  With bf16 over an 8-bit
  * cache, queries and the tree's keys are held to 2^-10 / 224 of their row's
- * largest element (exact for elements down to 2^-10 of it), and an infinite
- * one counts as NaN; the values are exact.  Rows that a node does not see,
+ * largest element (exact for elements down to 2^-10 of it; keys to 2^-50 at
+ * best), and an infinite one counts as NaN; the values are exact.  Rows that a node does not see,
  * padding rows among them, may hold anything.  A call's result
  * is deterministic; in bf16 the context is cut into pieces that depend on all
  * the lengths of the launch, so a sequence's last bits may differ with the

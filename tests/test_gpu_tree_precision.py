@@ -155,3 +155,18 @@ def test_large_finite_rows_reach_their_descendants_only(dtype, cache, big, nq):
             t[s * 7 + 2] = 0.25
     p.run()
     check(p)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("nq,rows", [(4, 9), (64, 9)])
+@pytest.mark.parametrize("q,k", [(0.0, 0.0), (1e-20, 0.0), (1e-25, 1e-25), (0.0, 1.0), (1.0, 0.0), (2.0 ** -126, 2.0 ** -126)])
+def test_zero_and_tiny_queries_and_keys(dtype, cache, nq, rows, q, k):
+    """A head whose queries are (next to) zero weighs what it sees alike, and
+    no hidden or padding row changes that."""
+    p = Tree([0, 1, 140], trees(nq, [rows, 2, 5], rows), nq, 2, 64, dtype, cache)
+    for t in (p.q, p.q_d):
+        t.view(-1, nq, 64)[:, 1] *= q
+    for t in (p.kb, p.kb_d):
+        t *= k
+    p.run()
+    check(p)
