@@ -25,8 +25,9 @@
 // rows, 8k: 247 us without turns, 183 so, 213 from the second half on in bf16;
 // after one, two, three, four quarters 281, 261, 268, 282 in 8 bits.
 // The reference m stays while the weights' sum suits bf16, which has fp32's
-// exponents: it starts at m = 0 and takes sums of 2^-60 .. 2^60, so the usual
-// chunk needs no maximum and no rescaling of O.  Otherwise the part of the
+// exponents: it starts at m = 0 and takes sums of 2^-30 .. 2^30, so the usual
+// chunk needs no maximum and no rescaling of O, and O stays in range up to
+// values of 2^97.  Otherwise the part of the
 // chunk (a half; 8-bit a quarter) is done again with its maximum: its scores
 // stay until its sum is known.
 //
@@ -1184,7 +1185,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               tt_unpair(tt_add2(sa, sb), s0, s1);
               sum = s0 + s1;
               // too large for the reference; or a row's first keys, which reference 0 does not suit
-              const bool over = sum > 0x1p60f || (m_run == -INFINITY && sum < 0x1p-60f);
+              const bool over = sum > 0x1p30f || (m_run == -INFINITY && sum < 0x1p-30f);
               if (again || !__any_sync(0xffffffffu, over)) break;
               again = true;
               const float alpha = refer(h * (HC / W), HC / W);

@@ -170,3 +170,18 @@ def test_zero_and_tiny_queries_and_keys(dtype, cache, nq, rows, q, k):
         t *= k
     p.run()
     check(p)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("nq,rows", [(4, 9), (16, 33), (16, 128)])
+def test_large_values_under_large_scores(dtype, cache, nq, rows):
+    """Every score near 50 ln 2, values near 2^85: weights against the
+    reference 0 would leave fp32's range, the output is far inside it."""
+    p = Tree([0, 0], trees(nq, [rows] * 2, rows), nq, 2, 64, dtype, cache, seed=rows)
+    for t in (p.q, p.q_d, p.kb, p.kb_d):
+        t.copy_(t.abs() * 0.5 + 0.5)
+    for t in (p.vb, p.vb_d):
+        t *= 2.0 ** 85
+    p.scale = p.a.scale = float(np.float32(50 * np.log(2) / (0.9 * 0.9 * 64)))
+    p.run()
+    check(p)
