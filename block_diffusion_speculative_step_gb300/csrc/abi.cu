@@ -309,6 +309,8 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
     TreeAttnDesc t = tree_attn_desc(d, L.S, L.rows, L.max_pos - L.rows, kv, 0.f);
     t.base_pos = base_pos;
     t.parent = L.tree_parent;
+    t.pos = L.tree_pos;
+    t.pos_end = rope_max_pos;
     t.q = s.q;
     t.kb = s.kb;
     t.vb = s.vb;
@@ -658,8 +660,9 @@ int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws
     rc = check_tree_kv(a->kv, who);
     if (rc) return rc;
   }
-  DF_CHECK(a->max_pos <= a->rope_max_pos, "%s: max_pos %d beyond the RoPE table (%d)", who, a->max_pos,
-           a->rope_max_pos);
+  // (a tree's positions are its own: the attention checks them)
+  DF_CHECK(tree ? a->rope_max_pos > 0 : a->max_pos <= a->rope_max_pos, "%s: max_pos %d beyond the RoPE table (%d)", who,
+           a->max_pos, a->rope_max_pos);
   {
     const void* st[] = {a->out_x_attn, a->out_q, a->out_kb, a->out_vb, a->out_attn, a->out_x_mlp, a->out_act};
     for (const void* p : st)

@@ -172,6 +172,8 @@ struct TreeAttnDesc {
   const int32_t* pages;
   int ps, max_pages, pool;
   int max_pos;                // bound on base_pos
+  const int32_t* pos;         // [M] or null: the rows' positions, below pos_end
+  int pos_end;
   float scale;                // times log2 e: scores in log2 units
   void* out;                  // [M][nq*d]
   void* work;                 // partials

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_simt_kernel(const __grid_cons
   const TsGeom gm = ts_geom(a);
   const int sp = blockIdx.x, g = blockIdx.y / gm.n_qt, qt = blockIdx.y % gm.n_qt, s = blockIdx.z;
   const bool tree = sp == gm.n_split - 1;
-  const int n_ctx = min(max(__ldg(a.base_pos + s), 0), a.max_pos);
+  const int base = __ldg(a.base_pos + s), n_ctx = min(max(base, 0), a.max_pos);
   const int j0 = sp * gm.split;
   if (!tree && j0 >= n_ctx) return;  // the merge knows which splits hold keys
   const int n_keys = tree ? a.rows : min(gm.split, n_ctx - j0);
@@ -66,13 +66,18 @@ __global__ void __launch_bounds__(kTsThreads) tree_simt_kernel(const __grid_cons
   const int QD = a.nq * D;
 
   if (tree) {
+    if (base != n_ctx && tid == 0) raise_status(a.status, ST_RANGE);
     if (a.parent)
       for (int i = tid; i < a.rows; i += kTsThreads) par[i] = a.parent[(size_t)s * a.rows + i];
     __syncthreads();
     if (tid < kTsQT) {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
       bool ok = false, bad = false;
-      if (tid < nq_tile) ok = tree_row_mask(a.parent ? par : nullptr, (qv0 + tid) / gm.grp, w, &bad);
+      if (tid < nq_tile) {
+        const int row = (qv0 + tid) / gm.grp;
+        ok = tree_row_mask(a.parent ? par : nullptr, row, w, &bad);
+        if (ok && a.pos) bad = (uint32_t)__ldg(a.pos + (size_t)s * a.rows + row) >= (uint32_t)a.pos_end;
+      }
       if (bad) raise_status(a.status, ST_RANGE);
       node_ok[tid] = ok;
       for (int i = 0; i < 4; ++i) mask[tid][i] = w[i];

@@ -381,11 +381,12 @@ __device__ __forceinline__ int tt_chunks(const TreeAttnDesc& a, int s, int* n) {
   return (*n + kTtCH - 1) / kTtCH + 1;
 }
 
-// One warp.
-__device__ __forceinline__ Part tt_part(const TreeAttnDesc& a, int ips, int nb) {
+// One warp.  status (or null): told of lengths outside their bound.
+__device__ __forceinline__ Part tt_part(const TreeAttnDesc& a, int ips, int nb, uint32_t* status) {
   int t = 0, mx = 0, n;
   for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
     const int k = tt_chunks(a, s, &n);
+    if (__ldg(a.base_pos + s) != n) raise_status(status, ST_RANGE);
     t += k;
     mx = max(mx, k);
   }
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
-    const Part pt = tt_part(a, ips, gridDim.x);
+    const Part pt = tt_part(a, ips, gridDim.x, status);
     Spot sp = {0, 0, 0, 0, 1};
     int len = 0;
     if (pt.aligned) {
@@ -889,6 +890,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           uint32_t w[4] = {0u, 0u, 0u, 0u};
           bool bad = false;
           if (!tree_row_mask(a.parent ? sh->par : nullptr, i, w, &bad)) w[0] = w[1] = w[2] = w[3] = 0u;  // padding: sees nothing
+          else if (a.pos) bad = (uint32_t)__ldg(a.pos + (size_t)sg.s * a.rows + i) >= (uint32_t)a.pos_end;
           if (bad) raise_status(status, ST_RANGE);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mb[i][k] = w[k];
@@ -1482,7 +1484,7 @@ __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constan
   // lengths it goes by were there before that kernel's own wait ended.
   int s = 0, it = 0, b0 = 0, b1 = 0;
   if (rg < min(NT * 4, (nqv + 31) / 32)) {
-    const Part pt = tt_part(a, ips, nb);
+    const Part pt = tt_part(a, ips, nb, nullptr);
     if (pt.aligned) {
       const Spot sp = tt_run(a, ips, blockIdx.y, pt);
       if (sp.s < a.n_seqs && sp.c == 0) {  // an item's first run

@@ -308,6 +308,7 @@ class Engine:
     def tree_layer_args(self, li: int, rows: int, h, pos, parent=None, tap=None, tap_offset=0, base_pos=None):
         a = self.target_layer_args(li, rows, h, tap, tap_offset, base_pos)
         a.attn_mode = D.DFLASH_ATTN_TREE
+        a.max_pos = self.cap + rows  # (the rows take no slots: the context may fill the cache)
         a.tree_parent, a.tree_pos = _ptr(parent), _ptr(pos)
         a.out_kb, a.out_vb = _ptr(self.tkb[li]), _ptr(self.tvb[li])
         return a

@@ -199,7 +199,11 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *   cache slots below base_pos[s], its ancestors and itself; kv (also 8-bit)
  *   is not written: the rows' rotated keys and values go to out_kb / out_vb,
  *   here [M][n_kv][d], from which dflash_kv_write commits the accepted path.
- *   kv.window must be 0; rows <= DFLASH_MAX_TREE; max_pos - rows <= capacity.
+ *   kv.window must be 0; rows <= DFLASH_MAX_TREE.  max_pos bounds base_pos[s] +
+ *   rows, max_pos - rows <= capacity (capacity + rows lets the context fill the
+ *   cache), and the positions only need to lie in the RoPE table.  A base_pos[s]
+ *   outside [0, max_pos - rows] or a node's position outside the table raises
+ *   DFLASH_ERR_INVALID_ARG in the status word.
  * tap (optional): writes the layer's output residual, rounded to dims.dtype,
  *   to tap[row * tap_stride + tap_offset + j] (feature taps for fusion).
  * max_pos: host-side bound with base_pos[s] + rows <= max_pos for every s
@@ -526,7 +530,8 @@ typedef struct {
   const void* kb;          /* [M][n_kv][d] rotated keys of the tree rows */
   const void* vb;          /* [M][n_kv][d] */
   dflash_kv kv;            /* the context; contiguous or paged, dims.dtype or 8-bit; window 0 */
-  int32_t max_pos;         /* host-side bound: base_pos[s] <= max_pos <= capacity */
+  int32_t max_pos;         /* host-side bound: base_pos[s] <= max_pos <= capacity; a length outside [0, max_pos]
+                              raises DFLASH_ERR_INVALID_ARG in the status word and is taken as the nearest in it */
   float scale;             /* 0: 1 / sqrt(head_dim) */
   void* out;               /* [M][n_q*d] */
 } dflash_tree_attention_args;

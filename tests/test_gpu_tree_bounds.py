@@ -1,0 +1,68 @@
+"""Tree forwards at the end of a cache, lengths and positions outside their
+bounds, and templates with rows that hold no node."""
+import pytest
+import torch
+
+from block_diffusion_speculative_step_gb300 import dflash as D
+from tests.test_gpu_tree_attn import PAD, TYPES, Tree, trees
+from tests.test_gpu_tree_engine import engine, prompts_of, small, template
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("nq", [4, 64])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 257, 2 ** 31 - 1])
+def test_length_outside_the_bound_is_reported(dtype, cache, nq, bad):
+    p = Tree([200, 256, 90], trees(2, [5, 5, 4], 5), nq, 2, 128, dtype, cache, cap=300)
+    p.a.max_pos = 256
+    p.run()
+    p.check()
+    p.base[0] = bad
+    p.run()
+    p.check(D.DFLASH_ERR_INVALID_ARG, seqs=[1, 2])
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_tree_cycles_at_the_end_of_the_cache(kv8):
+    """A tree's rows need no slots behind the context: cycles go on while the
+    longest path fits, with every slot seen."""
+    w = small("f32")
+    prompts = prompts_of(w, 2, 100)
+    n, N = 20, 65
+    tree = template(5, N, w.block, 4)
+    wide, eng = (engine(w, 3, 2, cap, tree=tree, kv8=kv8) for cap in (384, 128))
+    for e in (wide, eng):
+        e.prefill(prompts)
+    done = 0
+    while done < n:
+        done += 1
+        for e in (wide, eng):
+            e.tree_cycle()
+            assert e.status() == D.DFLASH_OK
+        assert torch.equal(wide.h[:2 * N], eng.h[:2 * N])  # every row of the last layer's output
+        assert torch.equal(wide.t_out, eng.t_out) and torch.equal(wide.base_pos, eng.base_pos)
+        if int(eng.base_pos.max()) + w.block > 128:
+            break
+    assert int(eng.base_pos.max()) > 128 - N
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [-1, 134, 2 ** 31 - 1])
+def test_position_outside_the_rope_table_is_reported(dtype, bad):
+    """One node's position outside the table of cap + block positions; the
+    same position in a padding row means nothing."""
+    w = small(dtype)
+    eng = engine(w, 3, 2, 128, tree=template(5, 9, w.block, 4))
+    eng.prefill(prompts_of(w, 2))
+    eng.tree_cycle()
+    assert eng.status() == D.DFLASH_OK and eng.rope_max == 134
+    keep = eng.t_pos.clone()
+    for parent, want in ((None, D.DFLASH_ERR_INVALID_ARG), (PAD, D.DFLASH_OK)):
+        eng.t_pos.copy_(keep)
+        eng.t_pos[13] = bad
+        if parent is not None:
+            eng.t_parent[1, 4:] = parent
+        a = eng.tree_layer_args(0, 9, eng.h, eng.t_pos, eng.t_parent)
+        D.dflash_decoder_layer_forward(a, eng.ws_ptr, eng.ws_bytes)
+        assert eng.status() == want
