@@ -111,6 +111,7 @@ struct TaShared {
   float cp[DFLASH_MAX_TREE];    // p_t of the child's token (drawn) or its weight; its weight in the draft row, 0 once removed
   float cq[DFLASH_MAX_TREE];
   float mp, mq;                 // the rows' maxima, children included
+  int bad_child, bad;           // a child's logit, a row of the level is no number or +inf, or a whole row -inf
   float sufP[DFLASH_MAX_TREE + 1];  // mass of the target row without the tokens of children [0, t)
   float invZ[DFLASH_MAX_TREE];  // 1 / Z_t, 0: nothing left, p stays
   float invY[DFLASH_MAX_TREE];  // 1 / (remaining mass of q before step t), in q's weights
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
       }
       if (lane == 0) sh.n_child = n;
       __syncwarp();
+      bool odd = false;
       for (int c = lane; c < n; c += 32) {
         const int i = sh.child[c];
         int x = sh.tok[i];
@@ -211,13 +213,15 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         sh.ctok[c] = x;
         sh.cu[c] = sh.u[i];
         const float a = x >= 0 ? l[x] : -INFINITY, b = Drawn && x >= 0 ? draft[(size_t)k * V + x] : -INFINITY;
-        if (!(a < INFINITY) || !(b < INFINITY)) raise_status(d.status, ST_NUMERIC);
+        odd |= !(a < INFINITY) || !(b < INFINITY);
         sh.cl[c] = a == a ? a : -INFINITY;
         if (Drawn) sh.cg[c] = b == b ? b : -INFINITY;
         int dup = x < 0;
         for (int e = 0; e < c; ++e) dup |= sh.tok[sh.child[e]] == x;
         sh.cdup[c] = dup;
       }
+      odd = __any_sync(0xffffffffu, odd);
+      if (lane == 0) sh.bad_child = odd;
     }
     __syncthreads();
     const int n_child = sh.n_child;
@@ -228,8 +232,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
     }
 
     // ---- maxima and sums over the slice, the children's tokens left out
-    // (a NaN or +inf logit makes the sum NaN, or the maximum infinite: reported
-    // below; every test then fails and the draw falls to token 0)
+    // (a NaN or +inf logit makes the sum NaN, or the maximum infinite)
     auto find = [&](int b) __attribute__((always_inline)) {  // bit j: entry j of the batch is a child's token
       uint32_t mine = 0u;
       for (int c = 0; c < n_child; ++c) {
@@ -308,10 +311,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
         if (Drawn) cn = fmaxf(cn, sh.cg[c]);
       }
       const float mp = ta_max(cm), mq = Drawn ? ta_max(cn) : -INFINITY;
-      // no logit above -inf, +inf, or a NaN
-      const bool bad = !(mp > -INFINITY && mp < INFINITY) || P.s != P.s || (Drawn && (mq == INFINITY || Q.s != Q.s));
+      // no logit above -inf, +inf, or a NaN: the row is no distribution, and the
+      // walk ends here.  (The last token is then some token: of the weights that
+      // are numbers the largest over its noise, token 0 where there is none.)
+      const bool bad = sh.bad_child || !(mp > -INFINITY && mp < INFINITY) || P.s != P.s ||
+                       (Drawn && g && (!(mq > -INFINITY && mq < INFINITY) || Q.s != Q.s));
       if (bad && rank == 0 && lane == 0) raise_status(d.status, ST_NUMERIC);
       if (lane == 0) {
+        sh.bad = bad;
         sh.mp = mp;
         sh.mq = mq;
       }
@@ -393,7 +400,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_accept_kernel(const __grid
 
     // ---- the tests, in order
     int went = -1, t = 0;
-    for (; t < n_child; ++t) {
+    const int n_test = sh.bad ? 0 : n_child;
+    for (; t < n_test; ++t) {
       bool ok;
       if constexpr (Drawn) {
         const float y = sh.invY[t];

@@ -575,7 +575,10 @@ int dflash_tree_build(const dflash_tree_build_args* a, void* ws, size_t ws_bytes
  * p(v) / noise[s][v] (an exponential race: a draw from p when noise holds
  * Exp(1) numbers; the lowest v on equal values), so the emitted tokens follow
  * the target's distribution exactly.  Logits may be -inf (probability 0); a
- * NaN or +inf in a visited row raises DFLASH_ERR_NUMERIC in the status word.
+ * NaN or +inf in a visited row (of the target, or of the draft where the node
+ * has children), or a row of nothing but -inf, raises DFLASH_ERR_NUMERIC in the
+ * status word: none of the node's children is accepted and the last token is
+ * unspecified, in [0, V).
  * temperature == 0: the accepted child is the first whose token equals
  * target_argmax[node] (dflash_verify_accept's argmax), the last token is the
  * last node's argmax; logits, u and noise are not read.
