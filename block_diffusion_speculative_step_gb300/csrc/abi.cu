@@ -311,6 +311,7 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
     t.parent = L.tree_parent;
     t.pos = L.tree_pos;
     t.pos_end = rope_max_pos;
+    t.zero_pad = 1;  // (what the workspace held would reach the residual as NaN or infinity)
     t.q = s.q;
     t.kb = s.kb;
     t.vb = s.vb;

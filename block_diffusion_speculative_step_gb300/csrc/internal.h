@@ -174,6 +174,7 @@ struct TreeAttnDesc {
   int max_pos;                // bound on base_pos
   const int32_t* pos;         // [M] or null: the rows' positions, below pos_end
   int pos_end;
+  int zero_pad;               // write 0 to padding rows, instead of leaving them as they were
   float scale;                // times log2 e: scores in log2 units
   void* out;                  // [M][nq*d]
   void* work;                 // partials

@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(256) tree_simt_merge_kernel(const __grid_const
   const float* base = static_cast<const float*>(a.work);
   constexpr size_t PS = kTsQT * (D + 2);
   auto part = [&](int i) { return base + (slot0 + (i < n_sp ? i : gm.n_split - 1)) * PS; };
-  if (part(n_sp)[kTsQT * D + kTsQT + qi] < 0.f) return;  // a padding row: left as it was
+  const bool pad = part(n_sp)[kTsQT * D + kTsQT + qi] < 0.f;
+  if (pad && !a.zero_pad) return;  // left as it was
   float M = -INFINITY;
   for (int i = 0; i <= n_sp; ++i) M = fmaxf(M, part(i)[kTsQT * D + qi]);
   float L = 0.f, O[E];
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(256) tree_simt_merge_kernel(const __grid_const
   const int row = qv / gm.grp, head = g * gm.grp + qv % gm.grp;
   T* o = reinterpret_cast<T*>(a.out) + ((size_t)s * a.rows + row) * a.nq * D + (size_t)head * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = from_f<T>(O[e] / L);
+  for (int e = 0; e < E; ++e) o[e] = from_f<T>(pad ? 0.f : O[e] / L);
 }
 
 static size_t ts_workspace(const TreeAttnDesc& a) {

@@ -1254,7 +1254,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         // (16 bytes per lane and store, to 32 rows: more cache-line accesses than
         // rows turned among lanes first, but a quarter of the instructions, and
         // nothing else here uses the load/store unit)
-        const bool write = row_ok && has_row && DFL_CHECK(node < a.rows, status);
+        const bool write = has_row && (row_ok || a.zero_pad) && DFL_CHECK(node < a.rows, status);
         uint4* out4 = reinterpret_cast<uint4*>(a.out) + ((size_t)(sg.s * a.rows + node) * a.nq + head) * (D / 8);
         constexpr int W = NCOL < 32 ? NCOL : 32;  // columns per step
 #pragma unroll 1
@@ -1297,9 +1297,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
             if (write) {
 #pragma unroll
               for (int k = 0; k < W / 8; ++k)
-                out4[col / 8 + k] = make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
-                                               tt_pack(o[8 * k + 4], o[8 * k + 5]),
-                                               tt_pack(o[8 * k + 6], o[8 * k + 7]));
+                out4[col / 8 + k] = !row_ok ? make_uint4(0, 0, 0, 0)
+                                            : make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
+                                                         tt_pack(o[8 * k + 4], o[8 * k + 5]),
+                                                         tt_pack(o[8 * k + 6], o[8 * k + 7]));
             }
           } else if (has_row) {
             float4* p4 = reinterpret_cast<float4*>(part) + (size_t)(prow >> 7) * (kTtRows * D / 4);
@@ -1559,15 +1560,17 @@ __global__ void __launch_bounds__(128) tree_tc_merge_kernel(const __grid_constan
       if (b + u == b1) last = lb[u];  // the tree's partial: negative in a padding row
     }
   }
-  if (qv >= nqv || last < 0.f) return;
+  if (qv >= nqv || (last < 0.f && !a.zero_pad)) return;
   const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
   const int node = qv / grp, head = g * grp + qv % grp;
   uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((size_t)s * a.rows + node) * a.nq * D +
                                         (size_t)head * D + cg * CW);
 #pragma unroll
   for (int k = 0; k < CW / 8; ++k)
-    out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                        tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv), tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    out[k] = last < 0.f ? make_uint4(0, 0, 0, 0)
+                        : make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                     tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                     tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
 }
 
 template <int D, int NT, bool Q8>

@@ -203,7 +203,8 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *   rows, max_pos - rows <= capacity (capacity + rows lets the context fill the
  *   cache), and the positions only need to lie in the RoPE table.  A base_pos[s]
  *   outside [0, max_pos - rows] or a node's position outside the table raises
- *   DFLASH_ERR_INVALID_ARG in the status word.
+ *   DFLASH_ERR_INVALID_ARG in the status word.  A padding row's attention output
+ *   is 0: its residual stays finite and means nothing.
  * tap (optional): writes the layer's output residual, rounded to dims.dtype,
  *   to tap[row * tap_stride + tap_offset + j] (feature taps for fusion).
  * max_pos: host-side bound with base_pos[s] + rows <= max_pos for every s

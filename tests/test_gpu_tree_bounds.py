@@ -66,3 +66,28 @@ def test_position_outside_the_rope_table_is_reported(dtype, bad):
         a = eng.tree_layer_args(0, 9, eng.h, eng.t_pos, eng.t_parent)
         D.dflash_decoder_layer_forward(a, eng.ws_ptr, eng.ws_bytes)
         assert eng.status() == want
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kv8", [False, True])
+def test_template_with_rows_that_hold_no_node(dtype, kv8):
+    """Padding rows (and rows below them) change nothing, whatever the
+    workspace held before: the cycle's tokens are those of the tree without."""
+    w = small(dtype)
+    parent, rank = template(3, 12, w.block, 4)
+    padded = parent + [PAD, PAD, 12], rank + [0, 0, 0]
+    prompts = prompts_of(w, 2)
+    got = []
+    for tree in ((parent, rank), padded):
+        eng = engine(w, 7, 2, tree=tree, kv8=kv8)
+        eng.prefill(prompts)
+        steps = []
+        for _ in range(4):
+            off = eng.ws_ptr - eng.ws.data_ptr() + 256 + (128 << 10)
+            eng.ws[off:] = 0xFF  # NaN as bf16 and as fp32
+            eng.tree_cycle()
+            assert eng.status() == D.DFLASH_OK
+            steps.append((eng.accept_len.cpu().tolist(), eng.t_out[:, :w.block].cpu().tolist(), eng.base_pos.cpu().tolist()))
+        got.append(steps)
+    if dtype == "f32":  # (bf16: the cut of the context goes by the launch)
+        assert got[0] == got[1]
