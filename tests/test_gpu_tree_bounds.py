@@ -91,3 +91,28 @@ def test_template_with_rows_that_hold_no_node(dtype, kv8):
         got.append(steps)
     if dtype == "f32":  # (bf16: the cut of the context goes by the launch)
         assert got[0] == got[1]
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_bound_of_zero(dtype, cache):
+    p = Tree([0, 0], trees(2, [5, 4], 5), 4, 2, 64, dtype, cache, cap=128)
+    p.a.max_pos = 0
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_more_tree_rows_than_one_verification_takes(kv8):
+    """9 sequences x 128 rows: several verification calls a cycle.  Every
+    sequence gets what it gets alone."""
+    w = small("f32")
+    tree = template(4, 128, w.block, 4)
+    prompts = prompts_of(w, 9)
+    many = engine(w, 3, 9, tree=tree, kv8=kv8)
+    out, acc = many.tree_generate(prompts, 6)
+    assert many.status() == D.DFLASH_OK
+    for s in (0, 7, 8):
+        one = engine(w, 3, 1, tree=tree, kv8=kv8)
+        o, a = one.tree_generate(prompts[s:s + 1], 6)
+        assert one.status() == D.DFLASH_OK
+        assert torch.equal(o[0], out[s]) and torch.equal(a[0], acc[s, :a.shape[1]])
