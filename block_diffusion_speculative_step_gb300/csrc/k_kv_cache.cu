@@ -6,8 +6,9 @@
 // largest e4m3 value.  With max |x| = f 2^k, f in [1/2, 1) (frexp) and 448 =
 // 7/8 * 2^9 this is e = k - 9, plus one when f > 7/8.  A power of two scales
 // without rounding (the largest codes land in (224, 448]), so the only error
-// is e4m3's own half step, 2^-4 relative, and elements below 2^-17 of the
-// row's maximum reach e4m3's subnormals.  e is held to [-60, 60]: magnitudes
+// is e4m3's own half step: 2^-4 relative, and for elements below about 2^-14 of
+// the row's maximum, e4m3's subnormals, 2^-10 * 2^e, at most 2^-10 / 224 of the
+// maximum.  e is held to [-60, 60]: magnitudes
 // outside 448 * 2^+-60 do not occur in a trained model's cache, and within it
 // no product of scales that attention forms leaves the fp32 range.
 #include <cuda_fp8.h>

@@ -59,7 +59,9 @@ class Engine:
     kv8: the target's caches hold 8-bit e4m3 rows with a power-of-two scale
     per (slot, KV head), half the bytes of bf16.  Target forwards then run as
     tree forwards (a chain where no tree is given) whose keys and values are
-    committed by dflash_kv_write."""
+    committed by dflash_kv_write.  The rows of one forward see each other
+    unquantised, later ones see them quantised: over an 8-bit cache tree cycles,
+    chain cycles and one-token decoding may part within the quantisation."""
 
     def __init__(self, w: synth.Workload, model: dict, n_seqs: int, cap: int, device="cuda",
                  prefill_chunk: int = 256, fuse_rows: int = 0, kv8: bool = False):
@@ -355,7 +357,8 @@ class Engine:
         """The template of tree_cycle: node i >= 1 hangs below node parent[i]
         and takes candidate rank[i] of its position (0: the best); parent[0]
         = -1 is the anchor.  Candidates beyond the first need the workload's
-        path selector, which lists path_topk of them."""
+        path selector, which lists path_topk of them.  May replace the buffers
+        and the workspace: cycles captured before are to be captured again."""
         n = len(parent)
         assert n == len(rank) and 1 <= n <= D.DFLASH_MAX_TREE and parent[0] == -1
         S = self.S
