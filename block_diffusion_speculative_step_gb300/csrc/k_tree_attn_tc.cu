@@ -137,7 +137,8 @@ struct TtShared {  // after the tiles
   uint64_t rvfull[2], rvempty[2];
   uint64_t kfr[kTtRing];          // kf written
   uint64_t tkfull[2], tkempty;    // the tree's K tiles (NT = 1: by the stream that takes them)
-  uint64_t sfull[2], pdone[2], ofull[2], qraw[2], qfull[2], qfree[2];
+  uint64_t sfull[2], pdone[2], ofull[2], qraw[2];
+  uint64_t qfull[2], qfree[2];    // see tt_qi
   uint64_t mready[4];             // ancestor masks written, by buffer
   uint64_t vraw[4];               // V tiles with rows to clear, copied (at most NSV <= 4 are ahead of their P V)
   uint32_t tslot;
@@ -289,6 +290,19 @@ __device__ __forceinline__ void tt_split_bf16(float lo, float hi, uint32_t& h, u
   tt_unpair(r, lo, hi);
   l = tt_pack(lo, hi);
 }
+
+// Index and phase of the query barriers (qfull, qfree) of stream t's tile in
+// segment `seg`.  NT = 2: a barrier per stream, whose issuer reads the tile in
+// every segment.  NT = 1: both issuers read one tile, but an issuer has no
+// chunk in a segment of one chunk that the other takes (of two such segments in
+// a row it has one).  It lets such a segment go at once, without having waited
+// for its queries, and may so be a segment ahead of the other issuer.  A barrier
+// per segment parity keeps its arrival apart from the other's for the segment
+// before, and the phase that it does wait for next to the one before it.
+template <int NT>
+__device__ __forceinline__ int tt_qi(int t, int seg) { return NT == 2 ? t : seg & 1; }
+template <int NT>
+__device__ __forceinline__ uint32_t tt_qp(int seg) { return (uint32_t)(NT == 2 ? seg : seg >> 1); }
 
 // Byte offset of (row, 16-byte piece) in a 16-bit tile of 128 rows kept as
 // 64-element boxes with the 128-byte swizzle.
@@ -744,14 +758,14 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     // before, whose P lies in the same columns.
     Seg ss;                      // the S side's segment
     int sc = 0, c = 0;           // its chunk counter and chunk
-    int s_seg = 0, q_seen = 0;   // segments walked; query loads waited for (all, in order)
+    int s_seg = 0, q_seen = -1;  // segment; the last one whose queries have been waited for
     int t_seen = 0;              // the tree's K tiles waited for
     bool s_on = ss.begin(&a, ips, sh, true);
     if (s_on) c = ss.c0;
     auto s_next = [&]() {
       ++sc;
       if (++c == ss.c1) {
-        if (tt_elect()) tc::mma_commit(&sh->qfree[NT == 2 ? t : 0]);  // the segment's query tile has been read
+        if (tt_elect()) tc::mma_commit(&sh->qfree[tt_qi<NT>(t, s_seg)]);  // the segment's query tile has been read
         __syncwarp();
         ++s_seg;
         s_on = ss.next();
@@ -760,8 +774,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     };
     if (NT == 1 && s_on && ut == 1u) s_next();  // (stream 1 takes the odd chunks)
     auto wait_s = [&]() {  // the operands of the next S
-      for (; q_seen <= s_seg; ++q_seen)
-        if (!wait_warp(&sh->qfull[NT == 2 ? t : 0], (uint32_t)q_seen)) return;
+      if (q_seen < s_seg) {
+        q_seen = s_seg;
+        if (!wait_warp(&sh->qfull[tt_qi<NT>(t, s_seg)], tt_qp<NT>(s_seg))) return;
+      }
       if (!wait_warp(&sh->kfull[sc % NSK], (uint32_t)(sc / NSK))) return;
       if (Q8 && ss.is_tree(c)) wait_warp(&sh->tkfull[NT == 1 ? t : 0], (uint32_t)t_seen++);
     };
@@ -854,20 +870,20 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     // cleared before the product: of the tree's rows only NaN and infinite
     // elements, which the segment's end adds to the rows that see them.
     // (8-bit: the converters do it.)
-    uint64_t* bar = Q8 ? sh->qraw : sh->qfull;
+    auto bar = [&](int t, int seg) { return Q8 ? &sh->qraw[t] : &sh->qfull[tt_qi<NT>(t, seg)]; };
     int n = 0, vc = 0, nraw = 0, nmask = 0, last_s = -1;
     for (bool on = sg.begin(&a, ips, sh); on && ok; ++n) {
       const int g = sg.it / p.n_pt, qv0 = (sg.it % p.n_pt) * (NT * kTtRows);
 #pragma unroll 1
       for (int t = 0; t < NT; ++t) {
-        if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
+        if (n > 0 && !wait_warp(&sh->qfree[tt_qi<NT>(t, n - 1)], tt_qp<NT>(n - 1))) break;
         // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
         if (p.q_tma && lane == 0) {
-          tc::mbar_arrive_expect_tx(&bar[t], TILE);
+          tc::mbar_arrive_expect_tx(bar(t, n), TILE);
           const int tok = sg.s * a.rows + tt_div_grp(p, qv0 + t * kTtRows, grp);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tc::tma_load_3d(Qs + t * TILE + h * (kTtRows * 128), &p.q3, 64 * h, g * grp, tok, &bar[t]);
+            tc::tma_load_3d(Qs + t * TILE + h * (kTtRows * 128), &p.q3, 64 * h, g * grp, tok, bar(t, n));
         }
       }
       Seg nx = sg;
@@ -938,7 +954,8 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
     }
     // (a copy that was issued lands before the CTA's shared memory goes away)
     if (lane == 0 && p.q_tma && n > 0)
-      for (int t = 0; t < NT; ++t) tc::mbar_wait(&bar[t], (uint32_t)(n - 1) & 1u, nullptr, lim_ns);
+      for (int t = 0; t < NT; ++t)
+        tc::mbar_wait(bar(t, n - 1), (Q8 ? (uint32_t)(n - 1) : tt_qp<NT>(n - 1)) & 1u, nullptr, lim_ns);
   } else if (warp < 12) {
     // ---------------------------------------------------- softmax: stream t, one query vector per thread
     const int t = (warp - 4) >> 2;
@@ -964,7 +981,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
         if (p.q_tma) {
           wait(&sh->qraw[NT == 2 ? t : 0], (uint32_t)seg_no);
         } else {
-          if (seg_no > 0) wait(&sh->qfree[NT == 2 ? t : 0], (uint32_t)(seg_no - 1));
+          if (seg_no > 0) wait(&sh->qfree[tt_qi<NT>(t, seg_no - 1)], tt_qp<NT>(seg_no - 1));
           const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                                             ((size_t)sg.s * a.rows + node) * QD + (size_t)head * D);
 #pragma unroll 8
@@ -1000,7 +1017,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           __syncwarp();
         }
         tc::fence_proxy_async_smem();
-        tc::mbar_arrive(&sh->qfull[NT == 2 ? t : 0]);
+        tc::mbar_arrive(&sh->qfull[tt_qi<NT>(t, seg_no)]);
       }
       const bool has_tree = sg.c1 == sg.nch;  // the segment ends with the tree's rows
       const int tree_ring = (cc + sg.c1 - 1 - sg.c0) % kTtRing;

@@ -185,3 +185,20 @@ def test_large_values_under_large_scores(dtype, cache, nq, rows):
     p.scale = p.a.scale = float(np.float32(50 * np.log(2) / (0.9 * 0.9 * 64)))
     p.run()
     check(p)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nq,nkv", [(16, 8), (56, 8), (64, 1)])
+def test_many_short_items_per_cta(cache, nq, nkv):
+    """More items than CTAs, most of them a chunk or two: every buffer of a
+    CTA's run is used many times over.  Twice, with the same bits."""
+    rng = np.random.default_rng(nq)
+    lens = [int(x) for x in rng.choice([0, 0, 1, 30, 128, 129, 300], 320)]
+    p = Tree(lens, trees(nq, [int(x) for x in rng.integers(1, 4, 320)], 3), nq, nkv, 64, "bf16", cache, seed=nq)
+    p.run()
+    check(p)
+    first = p.out.clone()
+    p.out.fill_(FILL)
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first, p.out)
