@@ -1383,6 +1383,9 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 code[b] = *reinterpret_cast<const uint4*>(raw + b * RPP * D);
                 f[b] = fac[b * RPP];
               }
+              // (the next copy into the slot is the async proxy's: without a fence
+              // the last rows' reads came behind it)
+              tc::fence_proxy_async_smem();
               tc::mbar_arrive(&sh->rvempty[rs]);
 #pragma unroll
               for (int b = 0; b < NP; ++b) {

@@ -202,3 +202,44 @@ def test_many_short_items_per_cta(cache, nq, nkv):
     p.run()
     torch.cuda.synchronize()
     assert torch.equal(first, p.out)
+
+
+def paged_values(c):
+    """Values that tell slots apart: slot j of a chunk holds 2^chunk in column j, keys 0, so that
+    every column of the output is the sum of what the chunks' slots hold."""
+    S, rows, nq, nkv, d = c["S"], c["rows"], c["nq"], c["nkv"], c["d"]
+    p = Tree(c["lens"], [list(range(-1, rows - 1))] * S, nq, nkv, d, "bf16", "e4m3", page=128, cap=384, chain=True)
+    eye = torch.eye(128, d)
+    p.dev["k"].zero_()
+    p.dev["ve"].fill_(127)
+    for s in range(S):
+        for ch in range(3):
+            p.dev["v"][p.pages[s, ch]] = (eye * 2.0 ** ch).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    for t in (p.kb, p.kb_d, p.vb, p.vb_d):
+        t.zero_()
+    return p
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,rows", [(32, 64), (32, 8)])
+def test_every_chunk_brings_its_own_values(d, nq, rows):
+    """A chunk's values stay until they have been read, however soon the next
+    ones come (again and again, with a cache that lies in L2)."""
+    rng = np.random.default_rng(d + rows)
+    lens = [int(x) for x in rng.choice([0, 1, 128, 129, 256, 257, 300, 384], 33)]
+    p = paged_values(dict(S=33, rows=rows, nq=nq, nkv=8, d=d, lens=lens))
+    want = torch.zeros(33, rows, d, dtype=torch.float64)
+    for s, n in enumerate(lens):
+        for j in range(n):
+            if j % 128 < d:
+                want[s, :, j % 128] += 2.0 ** (j // 128)
+        want[s] /= torch.arange(n + 1, n + rows + 1)[:, None]
+    want = want[:, :, None].expand(33, rows, nq, d)
+    # equal weights: at most 2^-8 of the value in the output's rounding, 2^-16 and the sum's 512 2^-23 before
+    tol = want * (2.0 ** -8 + 2.0 ** -16 + 512 * 2.0 ** -23) * (1 + 2.0 ** -8)
+    want, tol = want.cuda(), tol.cuda()
+    for _ in range(300):
+        p.out.zero_()
+        p.run()
+        assert bool(((p.out.view(33, rows, nq, d).double() - want).abs() <= tol).all())
+    assert p.ws.status() == 0
