@@ -1145,6 +1145,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 const float lo = __uint_as_float(h << 16) + __uint_as_float(l << 16);
                 const float hi = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
                 tt_split_bf16(lo * f, hi * f, v[k], v[8 + k]);
+                if (f == 1.f) v[k] = h, v[8 + k] = l;  // (halfway cases may split the other way round)
               }
               tmem_st16u(ts + 16 * q, v);
             }
@@ -1163,9 +1164,12 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               }
             }
           };
-          // a new reference: the largest of what it has and of n steps' scores
-          auto refer = [&](int i0, int n) {
+          // a new reference, for a row that needs one: the largest of what it has
+          // and of n steps' scores.  (The others keep theirs: a row's result does
+          // not depend on the rows that share its warp, lanes without one included.)
+          auto refer = [&](int i0, int n, bool needs) {
             const float m_new = fmaxf(cols_max(i0, n), m_run);
+            if (!needs) return 1.f;
             const float alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
             m_run = m_new;
             return alpha;
@@ -1180,7 +1184,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
           for (int h = 0; h < np; ++h) {
             uint32_t pk[HC];
             float sum;
-            bool again = false;
+            bool again = false, over;
 #pragma unroll 1
             for (;;) {
               const float m0 = m_run == -INFINITY ? 0.f : -m_run;
@@ -1204,10 +1208,10 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
               tt_unpair(tt_add2(sa, sb), s0, s1);
               sum = s0 + s1;
               // too large for the reference; or a row's first keys, which reference 0 does not suit
-              const bool over = sum > 0x1p30f || (m_run == -INFINITY && sum < 0x1p-30f);
-              if (again || !__any_sync(0xffffffffu, over)) break;
+              over = sum > 0x1p30f || (m_run == -INFINITY && sum < 0x1p-30f);
+              if (again || !__any_sync(0xffffffffu, over && has_row)) break;
               again = true;
-              const float alpha = refer(h * (HC / W), HC / W);
+              const float alpha = refer(h * (HC / W), HC / W, over);
               rescale(alpha);
               l_run *= alpha;
               if (h) {  // the parts before, stored already
@@ -1215,7 +1219,7 @@ __global__ void __launch_bounds__(TtCfg<D, NT, Q8>::THREADS, 1) tree_tc_kernel(c
                 rescale_p(alpha, HC * h);
               }
             }
-            if (!again && m_run == -INFINITY) m_run = 0.f;
+            if (!over && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
             if (NT == 2 && h == min(1, np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
 #pragma unroll

@@ -243,3 +243,30 @@ def test_every_chunk_brings_its_own_values(d, nq, rows):
         p.run()
         assert bool(((p.out.view(33, rows, nq, d).double() - want).abs() <= tol).all())
     assert p.ws.status() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nq,nkv,rows", [(32, 4, 5), (7, 1, 5), (32, 8, 33), (16, 2, 100)])
+def test_same_bits_beside_any_other_rows(cache, nq, nkv, rows):
+    """Tiles that are filled in part: the bits of a row depend neither on what
+    shared memory held nor on what the padding rows beside it hold."""
+    lens = [0, 5, 128, 201, 300, 142] * 4
+    n = max(1, rows - 2)
+    p = Tree(lens, trees(rows, [n] * 24, rows), nq, nkv, 128, "bf16", cache, seed=rows)
+    p.run()
+    check(p)
+    first = p.out.clone()
+    other = Tree(lens, trees(rows, [rows] * 24, rows), nq, nkv, 128, "bf16", cache, seed=rows + 1, q_amp=50.0)
+    pad = torch.zeros(24, rows, dtype=torch.bool)
+    pad[:, n:] = True
+    pad = pad.view(-1).cuda()
+    for fill in (None, 1e30, float("nan"), float("inf"), 1e-30):
+        other.run()  # (leaves other scales and scores behind)
+        if fill is not None:
+            for t in (p.q_d, p.kb_d, p.vb_d):
+                t[pad] = fill
+        p.out.fill_(FILL)
+        p.run()
+        torch.cuda.synchronize()
+        assert torch.equal(first, p.out), (fill, torch.nonzero((first != p.out).any(1)).flatten().tolist())
+    assert p.ws.status() == 0
