@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "abi_common.h"
+#include "abi_prompt.h"
 #include "abi_tree.h"
 #include "common.cuh"
 #include "internal.h"
@@ -1223,6 +1224,10 @@ size_t dflash_workspace_bytes(int32_t op, const void* args) {
     case DFLASH_OP_KV_READ:
     case DFLASH_OP_TREE_BUILD:
       return tree_op_workspace(op, args, who);
+    case DFLASH_OP_QK_NORM_ROPE:
+    case DFLASH_OP_PROMPT_ATTENTION:
+    case DFLASH_OP_TOKEN_LOGPROBS:
+      return prompt_op_workspace(op, args, who);
     default:
       fail(DFLASH_ERR_INVALID_ARG, "dflash_workspace_bytes: unknown op %d", op);
       return 0;

@@ -35,6 +35,9 @@ int fail(int code, const char* fmt, ...);
 
 inline size_t elem_size(int dtype) { return dtype == DFLASH_BF16 ? 2 : 4; }
 
+// Device pointers that the kernels read with 16-byte accesses.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // Carves a workspace into 256-byte aligned pieces; with base == nullptr it
 // only measures.
 struct Bump {

@@ -35,9 +35,6 @@ int check_tree_shape(const dflash_dims& d, int S, int rows, int max_pos, const d
   return DFLASH_OK;
 }
 
-// Device pointers that the kernels read with 16-byte accesses.
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 int check_tree_kv(const dflash_kv& kv, const char* who) {
   DF_CHECK(kv.k && kv.v, "%s: NULL cache pointer", who);
   DF_CHECK(aligned16(kv.k) && aligned16(kv.v), "%s: cache pointers must be 16-byte aligned", who);

@@ -244,6 +244,68 @@ struct TreeBuildDesc {
 };
 cudaError_t launch_tree_build(const TreeBuildDesc& d, cudaStream_t st);
 
+// Head norms and rotation behind the QKV projection (k_qk_norm.cu; see
+// dflash_qk_norm_rope).
+struct QkNormDesc {
+  int dtype, src_dtype;
+  int M, rows, nq, nkv, d;
+  float eps;
+  const int32_t* base_pos;
+  const void* qkv;
+  long long stride;           // elements between rows of qkv
+  const void* q_norm;
+  const void* k_norm;
+  const float* rope_cs;
+  int rope_max_pos;
+  void* q;                    // [M][nq*d]
+  void* k;                    // [M][nkv][d] (cache == 0), or the cache
+  void* v;
+  int cache, cap;
+  const int32_t* pages;
+  int ps, max_pages, pool;
+  uint32_t* status;
+};
+cudaError_t launch_qk_norm(const QkNormDesc& q, cudaStream_t st);
+
+// Causal attention of packed prompts (see dflash_prompt_attention).
+struct PromptAttnDesc {
+  int dtype;
+  int n_seqs, M, nq, nkv, d;
+  const int32_t* row_start;   // [S+1]
+  const int32_t* base_pos;    // [S] or null
+  const void* q;              // [M][nq*d]
+  const void* kb;             // [M][nkv][d]
+  const void* vb;
+  const void* kc;             // cache [S][nkv][cap][d] or page pool [pool][nkv][ps][d]; null without base_pos
+  const void* vc;
+  int cap;
+  const int32_t* pages;
+  int ps, max_pages, pool;
+  int max_pos;                // bound on base_pos (0 without)
+  float scale;                // times log2 e: scores in log2 units
+  void* out;                  // [M][nq*d]
+  void* work;                 // partials
+  uint32_t* status;
+};
+size_t prompt_attn_workspace(const PromptAttnDesc& a, int num_sms);
+cudaError_t launch_prompt_attention(const PromptAttnDesc& a, int num_sms, cudaStream_t st);
+size_t prompt_tc_workspace(const PromptAttnDesc& a, int num_sms);  // bf16 (k_prompt_attn_tc.cu)
+cudaError_t launch_prompt_tc(const PromptAttnDesc& a, int num_sms, cudaStream_t st);
+
+// Log probabilities of given tokens (k_logprobs.cu; see dflash_token_logprobs).
+struct LogprobDesc {
+  int M, V, topk;
+  float invT;
+  const float* logits;
+  const int32_t* tokens;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  uint32_t* status;
+};
+cudaError_t launch_token_logprobs(const LogprobDesc& d, int num_sms, cudaStream_t st);
+
 // Sampling-mode verification (k_sample.cu).
 // Kept set of one logit row under top-k / top-p: the entries up to (key,
 // idx) in the order (logit descending, index ascending); see k_sample.cu.

@@ -1,0 +1,926 @@
+// k_prompt_attn_tc.cu -- causal attention of packed prompts on the tcgen05
+// tensor cores (bf16).
+//
+// Work: an item is (sequence, KV head, two query tiles); a tile holds tok =
+// 128 / group tokens of the group's query heads (row = token * group + head),
+// so that K and V of a chunk serve 2 tok tokens x group heads whatever the
+// group.  An item's chunks are the 128-slot chunks of the cached context, then
+// those of the sequence's own rows up to the item's last token.  The chunks of
+// all items in a row are cut into equal runs, one per CTA (one CTA per SM), so
+// the causal triangle, ragged lengths and few long contexts balance alike.  A
+// CTA walks its run as segments (the part of one item inside the run): a whole
+// item is normalised and written at once, the first and the last segment may
+// leave a partial (O, m, l) that the merge kernel joins in order.
+//
+// Two streams per CTA, one per query tile, each an online softmax with its own
+// score and output accumulators in tensor memory (S 128 + O D columns).  Per
+// chunk and stream (128 query vectors x 128 keys):
+//   S = Q K^T        tcgen05.mma, both operands in shared memory
+//   P = 2^(c S - m)  one thread per query vector, written over S
+//   O += P V         tcgen05.mma, P from tensor memory, V MN-major
+// The streams' softmaxes take turns, so that one stream's products run beside
+// the other's softmax.  The reference m stays while the weights' sum suits
+// bf16 (which has fp32's exponents): it starts at 0 and takes sums of 2^-30 ..
+// 2^30, so the usual chunk needs no maximum and no rescaling of O.  Otherwise
+// the half chunk is done again with its maximum.
+//
+// The softmax is no rounding point: the weights enter their product as two
+// bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products share V's
+// tile and the accumulator.  The sum l uses the unrounded weights.
+//
+// What a row does not see may hold anything.  Scores are hidden by selection;
+// values meet a weight of 0, and 0 * NaN is NaN, so one warp goes over the V
+// tiles that some row of the item sees in part: rows behind the context's or
+// the item's end are cleared, NaN and infinite elements of the others are
+// cleared and noted, and added to the rows that see them when the segment ends.
+//
+// Roles: warp 0 K/V copies; warps 1, 2 the products of stream 0, 1; warp 3
+// query copies and V tiles; warps 4..11 the softmax, a query vector per thread.
+#include <math.h>
+
+#include "attn_tc.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kPtCH = 128;    // keys per chunk
+constexpr int kPtRows = 128;  // query vectors per tile
+constexpr int kPtRing = 8;    // chunks whose bad rows are kept
+constexpr int kPtSetup = 2;   // positions an item has before its chunks', for what it costs besides them
+
+struct PtTma {
+  CUtensorMap kc, vc;  // cache rows [..][D], boxes of 64 dims x 128 rows
+  CUtensorMap kb, vb;  // own rows [M][nkv][D]
+  CUtensorMap q3;      // queries [M][nq][D], box 64 dims x group x tok
+  PromptAttnDesc a;
+  int grp, tok;        // query heads per KV head, tokens per tile
+  uint32_t grp_mul;    // ceil(2^32 / grp) for 2 <= grp, else 0
+};
+
+// r / grp, r < 128.
+__device__ __forceinline__ int pt_div_grp(const PtTma& p, int r) {
+  return p.grp_mul ? (int)__umulhi((uint32_t)r, p.grp_mul) : r;
+}
+
+template <int D>
+struct PtCfg {
+  static constexpr int TILE = kPtCH * D * 2;
+  static constexpr int NS = D == 64 ? 4 : 2;  // K slots, V slots
+  static constexpr int THREADS = 384;
+  static constexpr int K_OFF = 2 * TILE;
+  static constexpr int V_OFF = K_OFF + NS * TILE;
+  static constexpr int X_OFF = V_OFF + NS * TILE;
+  static constexpr int X_BYTES = 2048;
+  static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
+
+struct PtShared {  // after the tiles
+  uint32_t badv[kPtRing][4];  // own rows whose V holds a NaN or infinity, by chunk counter
+  int s0, g0, t0, c0, len;    // the CTA's run: first item, position in it, number of positions
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];
+  uint64_t sfull[2], pdone[2], ofull[2], qfull[2], qfree[2];
+  uint32_t tslot;
+  int abort;
+};
+
+// sum of floor((a i + b) / m) over i < n (Euclid's steps: few for m = 128).
+__device__ __forceinline__ int pt_floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t sum = 0;
+  for (;;) {
+    if (n == 0) return (int)sum;
+    if (a >= m) {
+      sum += (uint32_t)(((uint64_t)n * (n - 1) >> 1) * (a / m));
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const uint32_t y = a * n + b;
+    if (y < m) return (int)sum;
+    n = y / m;
+    b = y % m;
+    const uint32_t x = m;
+    m = a;
+    a = x;
+  }
+}
+
+struct PtSeq {
+  int row0, n, ctx;  // first row, rows, cached positions
+  int cc, T;         // context chunks, items per KV head
+  __device__ __forceinline__ void set(const PromptAttnDesc& a, int tt, int r0, int r1, int c) {
+    row0 = r0;
+    n = r1 - r0;
+    ctx = min(max(c, 0), a.max_pos);
+    cc = (ctx + kPtCH - 1) / kPtCH;
+    T = (n + tt - 1) / tt;
+  }
+  __device__ __forceinline__ int end(int tt, int t) const { return min(n, (t + 1) * tt); }  // behind item t's last token
+  __device__ __forceinline__ int chunks(int tt, int t) const { return cc + (end(tt, t) + kPtCH - 1) / kPtCH; }
+  // Positions of items 0 .. t-1 of a KV head.
+  __device__ __forceinline__ int before(int tt, int t) const {
+    if (t <= 0) return 0;
+    const int u = t == T ? t - 1 : t;  // (whole items)
+    const int x = u * (kPtSetup + cc) + pt_floor_sum(u, kPtCH, tt, tt + kPtCH - 1);
+    return t == T ? x + kPtSetup + chunks(tt, T - 1) : x;
+  }
+};
+
+__device__ __forceinline__ PtSeq pt_seq(const PromptAttnDesc& a, int tt, int s) {
+  PtSeq q;
+  q.set(a, tt, __ldg(a.row_start + s), __ldg(a.row_start + s + 1), a.base_pos ? __ldg(a.base_pos + s) : 0);
+  return q;
+}
+
+// All positions (one warp); none where row_start leaves [0, M] or decreases.
+// status (or null): told of that, and of contexts out of range.
+__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status) {
+  int t = 0;
+  bool bad = false, far = false;
+  for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
+    const PtSeq q = pt_seq(a, tt, s);
+    bad |= q.row0 < 0 || q.row0 > a.M || q.n < 0 || q.n > a.M - q.row0;
+    far |= a.base_pos && __ldg(a.base_pos + s) != q.ctx;
+    if (!bad) t += q.before(tt, q.T) * a.nkv;
+  }
+  if ((bad || far) && status) raise_status(status, ST_RANGE);
+  return __any_sync(0xffffffffu, bad) ? 0 : __reduce_add_sync(0xffffffffu, t);
+}
+
+// The item at position x of the flat order, and the position c in it (one warp).
+struct PtSpot {
+  int s, g, t, c;
+  PtSeq q;
+};
+__device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int x) {
+  const int lane = threadIdx.x & 31;
+  PtSpot p;
+  p.s = a.n_seqs;
+  p.g = p.t = p.c = 0;
+  p.q.set(a, tt, 0, 0, 0);
+  int first = 0;
+  for (int b = 0; b < a.n_seqs; b += 32) {
+    const int s = b + lane;
+    int len = 0;
+    if (s < a.n_seqs) {
+      const PtSeq q = pt_seq(a, tt, s);
+      len = q.before(tt, q.T) * a.nkv;
+    }
+    int inc = len;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, first + inc > x);
+    if (!hit) {
+      first += __shfl_sync(0xffffffffu, inc, 31);
+      continue;
+    }
+    const int w = __ffs(hit) - 1;
+    x -= first + __shfl_sync(0xffffffffu, inc - len, w);
+    p.s = b + w;
+    p.q = pt_seq(a, tt, p.s);
+    const int one = p.q.before(tt, p.q.T);  // positions of a KV head
+    p.g = x / one;
+    x %= one;
+    int lo = 0, hi = p.q.T;  // the item lies in [lo, hi): 32 places at a time
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned le = __ballot_sync(0xffffffffu, at < hi && p.q.before(tt, at) <= x);
+      lo += (__popc(le) - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    p.t = lo;
+    p.c = x - p.q.before(tt, lo);
+    return p;
+  }
+  return p;
+}
+
+// A CTA's run walked segment by segment; every role keeps its own copy.  UNI: a
+// whole warp walks, loaded values go through a reduction, which the compiler
+// knows to be the same in every lane.
+template <bool UNI>
+struct PtSeg {
+  const PromptAttnDesc& a;
+  const int tt;        // tokens per item
+  int left;            // positions of the run not yet walked
+  int s, g, t;         // the item
+  PtSeq q;
+  int end, nch;        // behind the item's last token; its chunks
+  int c0, c1;          // the segment's chunks
+  __device__ __forceinline__ PtSeg(const PromptAttnDesc& a_, int tt_) : a(a_), tt(tt_) {}
+  __device__ __forceinline__ static int same(int x) { return UNI ? __reduce_max_sync(0xffffffffu, x) : x; }
+  __device__ __forceinline__ void load() {
+    q.set(a, tt, same(__ldg(a.row_start + s)), same(__ldg(a.row_start + s + 1)),
+          a.base_pos ? same(__ldg(a.base_pos + s)) : 0);
+  }
+  __device__ __forceinline__ void item() {
+    end = q.end(tt, t);
+    nch = q.chunks(tt, t);
+  }
+  // The part of the current item from position v on, at most `left` positions.
+  __device__ __forceinline__ void take(int v) {
+    const int n = min(nch + kPtSetup - v, left);
+    c0 = max(0, v - kPtSetup);
+    c1 = max(0, v + n - kPtSetup);
+    left -= n;
+  }
+  __device__ __forceinline__ bool begin(const PtShared* sh) {
+    left = same(sh->len);
+    if (left <= 0) return false;
+    s = same(sh->s0);
+    g = same(sh->g0);
+    t = same(sh->t0);
+    load();
+    item();
+    take(same(sh->c0));
+    return c1 > c0 || next();
+  }
+  __device__ __forceinline__ bool next() {
+    do {
+      if (left <= 0) return false;
+      if (++t == q.T) {
+        t = 0;
+        if (++g == a.nkv) {
+          g = 0;
+          do {
+            if (++s >= a.n_seqs) return false;
+            load();
+          } while (q.T == 0);
+        }
+      }
+      item();
+      take(0);
+    } while (c1 <= c0);
+    return true;
+  }
+  __device__ __forceinline__ bool own(int c) const { return c >= q.cc; }
+  __device__ __forceinline__ int key0(int c) const { return (c - q.cc) * kPtCH; }  // an own chunk's first row
+  // Keys of the chunk that some row of the item sees.
+  __device__ __forceinline__ int keys(int c) const { return min(kPtCH, own(c) ? end - key0(c) : q.ctx - c * kPtCH); }
+  // Does some row of the item see the chunk in part?
+  __device__ __forceinline__ bool masked(int c) const {
+    return own(c) ? key0(c) + kPtCH - 1 > t * tt : q.ctx - c * kPtCH < kPtCH;
+  }
+};
+
+// Where a segment's partial lies: slot 0 of CTA b when the item began in an
+// earlier CTA, slot 1 when it ends in a later one.  A slot holds D / 4 column
+// groups of [128 rows] float4 per tile, then maxima and sums.
+template <int D>
+__host__ __device__ constexpr size_t pt_slot_floats() {
+  return (size_t)2 * kPtRows * (D + 2);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const __grid_constant__ PtTma p) {
+  using Cfg = PtCfg<D>;
+  constexpr int TILE = Cfg::TILE, NS = Cfg::NS;
+  extern __shared__ __align__(1024) uint8_t pt_smem[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* Qs = sm;
+  uint8_t* Ks = sm + Cfg::K_OFF;
+  uint8_t* Vs = sm + Cfg::V_OFF;
+  PtShared* sh = reinterpret_cast<PtShared*>(sm + Cfg::X_OFF);
+  static_assert(sizeof(PtShared) <= Cfg::X_BYTES, "exchange area");
+  volatile int* abort = &sh->abort;
+
+  const PromptAttnDesc& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int grp = p.grp, tt = 2 * p.tok;
+  uint32_t* status = a.status;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sh->kfull[i], 1);
+      tc::mbar_init(&sh->kempty[i], 2);  // the two issuers
+      tc::mbar_init(&sh->vfull[i], 1);
+      tc::mbar_init(&sh->vempty[i], 2);
+      tc::mbar_init(&sh->vraw[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh->sfull[i], 1);
+      tc::mbar_init(&sh->pdone[i], 128);
+      // the product's commit, and the issuer's own arrival: what the issuer has
+      // observed (bad rows) is visible to who waits here
+      tc::mbar_init(&sh->ofull[i], 2);
+      tc::mbar_init(&sh->qfull[i], 1);
+      tc::mbar_init(&sh->qfree[i], 1);
+    }
+    sh->abort = 0;
+    tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&p.kb);
+    tc::tma_prefetch_desc(&p.vb);
+    tc::tma_prefetch_desc(&p.q3);
+  }
+  if (warp == 1) tc::tmem_alloc(&sh->tslot, 512);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 0) {
+    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr);
+    const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int x0 = (int)min((long long)blockIdx.x * per, (long long)total), len = min(per, total - x0);
+    PtSpot sp;
+    sp.s = sp.g = sp.t = sp.c = 0;
+    if (len > 0) sp = pt_locate(a, tt, x0);
+    if (lane == 0) {
+      sh->s0 = sp.s;
+      sh->g0 = sp.g;
+      sh->t0 = sp.t;
+      sh->c0 = sp.c;
+      sh->len = sp.s < a.n_seqs ? len : 0;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sh->tslot;
+  const uint64_t lim_ns = wait_limit_ns(status);
+  const bool stall = stall_kv_loads(status);  // test switch: issue no K/V copy
+  const KvMap km{a.pages, a.cap, a.ps, a.max_pages, a.pool, a.nkv};
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t par) {
+    if (ok && !tc::mbar_wait(bar, par & 1u, abort, lim_ns)) {
+      raise_status(status, ST_TIMEOUT);
+      *abort = 1;
+      ok = false;
+    }
+    return ok;
+  };
+  // The same for a whole warp (its lanes go on together: what follows shuffles).
+  auto wait_warp = [&](uint64_t* bar, uint32_t par) {
+    wait(bar, par);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  if (warp == 0) {
+    // ---------------------------------------------------- K/V copies
+    if (lane == 0 && !stall) {
+      PtSeg<false> sg(a, tt);
+      int nk = 0, nv = 0, nraw = 0;  // copies issued; V tiles that warp 3 goes over
+      uint32_t parts = 0u;           // which of the last V tiles those were
+      for (bool on = sg.begin(sh); on && ok; on = sg.next()) {
+        for (int c = sg.c0; c < sg.c1 && ok; ++c) {
+          const bool own = sg.own(c);
+          int row = own ? sg.q.row0 + sg.key0(c) : 0;
+          if (!own) {
+            bool bad = false;
+            row = (int)(km.row0(sg.s, c * kPtCH, &bad) + (uint32_t)sg.g * (uint32_t)km.head_rows());
+            if (bad) raise_status(status, ST_RANGE);  // reads page 0 instead
+          }
+          auto copy = [&](uint8_t* dst, const CUtensorMap* mo, const CUtensorMap* mc, uint64_t* bar) {
+            tc::mbar_arrive_expect_tx(bar, TILE);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              if (own) tc::tma_load_3d(dst + h * (kPtCH * 128), mo, 64 * h, sg.g, row, bar);
+              else tma_load_2d_plain(dst + h * (kPtCH * 128), mc, 64 * h, row, bar);
+            }
+          };
+          if (nk >= NS && !wait(&sh->kempty[nk % NS], (uint32_t)(nk / NS - 1))) break;
+          copy(Ks + (nk % NS) * TILE, &p.kb, &p.kc, &sh->kfull[nk % NS]);
+          ++nk;
+          if (nv >= NS && !wait(&sh->vempty[nv % NS], (uint32_t)(nv / NS - 1))) break;
+          const bool part = sg.masked(c);  // warp 3 goes over it and passes it on
+          parts = parts << 1 | (part ? 1u : 0u);
+          copy(Vs + (nv % NS) * TILE, &p.vb, &p.vc, part ? &sh->vraw[nraw++ & 3] : &sh->vfull[nv % NS]);
+          ++nv;
+        }
+      }
+      // every copy has landed before the CTA's shared memory goes away
+      for (int i = max(0, nk - NS); i < nk; ++i)
+        tc::mbar_wait(&sh->kfull[i % NS], (uint32_t)(i / NS) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nv - NS); i < nv; ++i)
+        if (!(parts >> (nv - 1 - i) & 1u))
+          tc::mbar_wait(&sh->vfull[i % NS], (uint32_t)(i / NS) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nraw - NS); i < nraw; ++i)
+        tc::mbar_wait(&sh->vraw[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, lim_ns);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------------------- MMA issue, stream t
+    // The whole warp walks the stream's jobs, so that descriptors and
+    // addresses stay in uniform registers; one lane issues.
+    const int t = warp - 1;
+    constexpr uint32_t idS = tc::idesc_bf16_f32(kPtRows, kPtCH);
+    constexpr uint32_t idV = tc::idesc_bf16_f32_bmn(kPtRows, D);
+    const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
+    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + ut * TILE), dk = tc::sdesc_sw128(tc::smem_u32(Ks)),
+                   dv = tc::sdesc_sw128_mn(tc::smem_u32(Vs), kPtCH * 128, 1024);
+    const uint32_t tm_s = __reduce_max_sync(0xffffffffu, tmem) + ut * 128u, tm_o = tm_s + 256u;
+    // S of the stream's next job is issued right behind P V of the job
+    // before, whose P lies in the same columns.
+    PtSeg<true> ss(a, tt), sg(a, tt);  // the S side's segment, the P V side's
+    int sc = 0, c = 0;           // its chunk counter and chunk
+    int s_seg = 0, q_seen = -1;  // segment; the last one whose queries have been waited for
+    bool s_on = ss.begin(sh);
+    if (s_on) c = ss.c0;
+    auto wait_s = [&]() {  // the operands of the next S
+      if (q_seen < s_seg) {
+        q_seen = s_seg;
+        if (!wait_warp(&sh->qfull[t], (uint32_t)s_seg)) return;
+      }
+      wait_warp(&sh->kfull[sc % NS], (uint32_t)(sc / NS));
+    };
+    auto issue_s = [&]() {
+      if (!ok) return;
+      const int slot = sc % NS;
+      tc::tc_fence_after();
+      const uint64_t k = dk + (uint64_t)(slot * TILE / 16);
+      const bool q_last = c + 1 == ss.c1;
+      if (tt_elect()) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          constexpr int kBox = kPtCH * 128 / 16;  // descriptor addresses count 16 bytes
+          const uint64_t off = (uint64_t)((j >> 2) * kBox + (j & 3) * 2);
+          tc::mma_bf16(tm_s, dq + off, k + off, idS, j > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&sh->sfull[t]);
+        tc::mma_commit(&sh->kempty[slot]);
+        if (q_last) tc::mma_commit(&sh->qfree[t]);  // the segment's query tile has been read
+      }
+      __syncwarp();
+      ++sc;
+      if (++c == ss.c1) {
+        ++s_seg;
+        s_on = ss.next();
+        c = ss.c0;
+      }
+    };
+    if (s_on) {
+      wait_s();
+      issue_s();
+    }
+    int vc = 0;
+    for (bool on = sg.begin(sh); on && ok; on = sg.next()) {
+      uint32_t acc0 = 0u;  // the segment's first P V starts the accumulator
+      for (int x = sg.c0; x < sg.c1 && ok; ++x, ++vc) {
+        const int slot = vc % NS, nk = sg.keys(x);
+        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vc / NS))) break;
+        // waited for early, so that S follows P V in the tensor pipe without a
+        // gap; not across segments, whose query load may still take a while
+        const bool last = x + 1 == sg.c1;
+        if (!last && s_on) wait_s();
+        if (!wait_warp(&sh->pdone[t], (uint32_t)vc)) break;
+        tc::tc_fence_after();
+        const uint64_t v = dv + (uint64_t)(slot * TILE / 16);
+        if (tt_elect()) {
+#pragma unroll
+          for (int j = 0; j < kPtCH / 16; ++j)  // (16 keys a step; of a short chunk only those that hold some)
+            if (16 * j < nk) {
+              mma_ts(tm_o, tm_s + 16 * j, v + (uint64_t)(j * 128), idV, j > 0 ? 1u : acc0);
+              mma_ts(tm_o, tm_s + 16 * j + 8, v + (uint64_t)(j * 128), idV, 1u);  // what P's first part left
+            }
+          if (last) {  // the segment's output is complete
+            tc::mma_commit(&sh->ofull[t]);
+            tc::mbar_arrive(&sh->ofull[t]);
+          }
+        }
+        __syncwarp();
+        acc0 = 1u;
+        if (s_on) {
+          if (last) wait_s();
+          issue_s();
+        }
+        if (tt_elect()) tc::mma_commit(&sh->vempty[slot]);  // (behind S: the softmax waits for S, nobody yet for V)
+        __syncwarp();
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------- queries, V tiles seen in part
+    PtSeg<false> sg(a, tt);
+    int n = 0, vc = 0, nraw = 0;
+    const uint32_t qbytes = (uint32_t)(D / 64) * (uint32_t)(grp * p.tok) * 128u;
+    for (bool on = sg.begin(sh); on && ok; on = sg.next(), ++n) {
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
+        // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&sh->qfull[t], qbytes);
+          const int tok = sg.q.row0 + sg.t * tt + t * p.tok;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(Qs + t * TILE + h * (kPtRows * 128), &p.q3, 64 * h, sg.g * grp, tok, &sh->qfull[t]);
+        }
+      }
+      for (int c = sg.c0; c < sg.c1 && ok; ++c, ++vc) {
+        if (!sg.masked(c)) continue;
+        const int nk = sg.keys(c), slot = vc % NS;
+        if (!wait_warp(&sh->vraw[nraw & 3], (uint32_t)(nraw >> 2))) break;
+        ++nraw;
+        constexpr int CPR = D / 8;
+        uint8_t* vt = Vs + slot * TILE;
+        auto at = [&](int i) { return reinterpret_cast<uint4*>(vt + tt_off(i / CPR, i % CPR)); };
+        if (sg.own(c)) {
+          uint32_t any = 0u;
+#pragma unroll 8
+          for (int i = lane; i < nk * CPR; i += 32) any |= tt_odd(*at(i));
+          if (lane < 4) sh->badv[vc % kPtRing][lane] = 0u;
+          __syncwarp();
+          if (__any_sync(0xffffffffu, any != 0u)) {
+#pragma unroll 1
+            for (int i = lane; i < nk * CPR; i += 32) {
+              const uint4 x = *at(i);
+              if (tt_odd(x)) {
+                *at(i) = tt_clear_odd(x);
+                atomicOr(&sh->badv[vc % kPtRing][i / CPR >> 5], 1u << (i / CPR & 31));
+              }
+            }
+          }
+        }
+#pragma unroll 4
+        for (int i = nk * CPR + lane; i < ((nk + 15) & ~15) * CPR; i += 32) *at(i) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh->vfull[slot]);
+      }
+      if (!ok) break;
+    }
+    // the query copies have landed before the CTA's shared memory goes away
+    if (lane == 0 && n > 0)
+      for (int t = 0; t < 2; ++t) tc::mbar_wait(&sh->qfull[t], (uint32_t)(n - 1) & 1u, nullptr, lim_ns);
+  } else {
+    // ---------------------------------------------------- softmax, stream t
+    const int t = (warp - 4) >> 2, r = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lane_base + (uint32_t)t * 128u, to = ts + 256u;
+    const int rt = pt_div_grp(p, r), head_in = r - rt * grp;  // the row's token of the tile, and head of the group
+    const bool in_tile = rt < p.tok;
+    PtSeg<false> sg(a, tt);
+    int nj = 0, no = 0;
+    // (after a wait gave up the loops run on without work, to meet the barriers)
+    for (bool on = sg.begin(sh); on; on = sg.next()) {
+      const int token = sg.t * tt + t * p.tok + rt;  // of the sequence
+      const bool has_row = in_tile && token < sg.q.n;
+      const bool warp_on = __any_sync(0xffffffffu, has_row);
+      float m_run = -INFINITY, l_run = 0.f;
+      const int nj0 = nj;
+      // keys of own chunk c that the row sees
+      auto own_seen = [&](int c) { return min(kPtCH, max(0, token + 1 - sg.key0(c))); };
+      for (int c = sg.c0; c < sg.c1; ++c) {
+        const int nk = sg.keys(c);
+        const bool masked = sg.masked(c);
+        const int see = sg.own(c) ? own_seen(c) : nk;
+        wait(&sh->sfull[t], (uint32_t)nj);
+        // the streams' softmaxes take turns
+        if (t == 1) tc::named_bar(7, 256);
+        else if (nj > 0) tc::named_bar(6, 256);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (warp_on) {
+          constexpr int W = 16, HC = 64;  // columns per step, per part
+          auto hide = [&](float (&x)[W], int i) {  // columns W i ..
+            if (masked) {
+              const int n = see - W * i;
+              const uint32_t w = n >= W ? 0xffffu : n > 0 ? (1u << n) - 1u : 0u;
+#pragma unroll
+              for (int k = 0; k < W; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
+            }
+          };
+          const unsigned long long cs2 = tt_pair(a.scale, a.scale);
+          auto cols_max = [&](int i0, int n) {  // the largest score of n steps
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float x[W];
+#pragma unroll 1
+            for (int i = i0; i < i0 + n; ++i) {
+              tmem_ld_async(ts + W * i, x);
+              tmem_wait(x);
+#pragma unroll
+              for (int k = 0; k < W; k += 2) tt_unpair(tt_mul2(tt_pair(x[k], x[k + 1]), cs2), x[k], x[k + 1]);
+              hide(x, i);
+#pragma unroll
+              for (int k = 0; k < W; k += 2) m4[(k >> 1) & 3] = fmaxf(fmaxf(m4[(k >> 1) & 3], x[k]), x[k + 1]);
+            }
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          };
+          unsigned long long sa, sb;
+          // weights 2^(scale x + m0) of a step, as the product takes them (W / 2
+          // columns of their first parts, then what those left), and their sums;
+          // `next` starts the next step's loads once the scores have been taken
+          auto piece = [&](float (&x)[W], uint32_t* pk, float m0, auto next) {
+            const unsigned long long m2 = tt_pair(m0, m0);
+            unsigned long long y[W / 2];
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) y[k] = tt_fma2(tt_pair(x[2 * k], x[2 * k + 1]), cs2, m2);
+            next();
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) {
+              float lo, hi;
+              tt_unpair(y[k], lo, hi);
+              lo = tt_ex2(lo);
+              hi = tt_ex2(hi);
+              if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
+              else sa = tt_add2(sa, tt_pair(lo, hi));
+              tt_split_bf16(lo, hi, pk[k], pk[W / 2 + k]);
+            }
+          };
+          // the weights of the chunk's first n keys
+          auto rescale_p = [&](float f, int n) {
+            if (!__any_sync(0xffffffffu, f != 1.f)) return;
+#pragma unroll 1
+            for (int q = 0; q < n / 16; ++q) {
+              float w[16];
+              uint32_t v[16];
+              tc::tmem_ld16(ts + 16 * q, w);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t h = __float_as_uint(w[k]), l = __float_as_uint(w[8 + k]);
+                const float lo = __uint_as_float(h << 16) + __uint_as_float(l << 16);
+                const float hi = __uint_as_float(h & 0xFFFF0000u) + __uint_as_float(l & 0xFFFF0000u);
+                tt_split_bf16(lo * f, hi * f, v[k], v[8 + k]);
+                if (f == 1.f) v[k] = h, v[8 + k] = l;  // (halfway cases may split the other way round)
+              }
+              tmem_st16u(ts + 16 * q, v);
+            }
+          };
+          auto rescale = [&](float f) {
+            // O holds the stream's chunks before this one: their products
+            // precede this chunk's S in the tensor pipe, so they are complete.
+            if (nj > nj0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                float o[16];
+                tc::tmem_ld16(to + 16 * q, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= f;
+                tc::tmem_st16(to + 16 * q, o);
+              }
+            }
+          };
+          // a new reference, for a row that needs one: the largest of what it has
+          // and of n steps' scores.  (The others keep theirs: a row's result does
+          // not depend on the rows that share its warp, lanes without one included.)
+          auto refer = [&](int i0, int n, bool needs) {
+            const float m_new = fmaxf(cols_max(i0, n), m_run);
+            if (!needs) return 1.f;
+            const float alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
+            m_run = m_new;
+            return alpha;
+          };
+          // A half chunk at a time, whose weights stay in registers until their
+          // sum shows that the reference suits them.
+          const int np = (nk + HC - 1) / HC;  // halves that hold keys
+          float sum0 = 0.f;
+#pragma unroll 1
+          for (int h = 0; h < np; ++h) {
+            uint32_t pk[HC];
+            float sum;
+            bool again = false, over;
+#pragma unroll 1
+            for (;;) {
+              const float m0 = m_run == -INFINITY ? 0.f : -m_run;
+              sa = sb = tt_pair(0.f, 0.f);
+              float x[W];
+              tmem_ld_async(ts + HC * h, x);
+#pragma unroll
+              for (int i = 0; i < HC / W; ++i) {  // the next scores arrive while these are exponentiated
+                tmem_wait(x);
+                hide(x, h * (HC / W) + i);
+                piece(x, pk + i * W, m0, [&]() {
+                  if (i + 1 < HC / W) tmem_ld_async(ts + HC * h + W * (i + 1), x);
+                });
+              }
+              float s0, s1;
+              tt_unpair(tt_add2(sa, sb), s0, s1);
+              sum = s0 + s1;
+              // too large for the reference; or a row's first keys, which reference 0 does not suit
+              over = sum > 0x1p30f || (m_run == -INFINITY && sum < 0x1p-30f);
+              if (again || !__any_sync(0xffffffffu, over && has_row)) break;
+              again = true;
+              const float alpha = refer(h * (HC / W), HC / W, over);
+              rescale(alpha);
+              l_run *= alpha;
+              if (h) {  // the half before, stored already
+                sum0 *= alpha;
+                rescale_p(alpha, HC * h);
+              }
+            }
+            if (!over && m_run == -INFINITY) m_run = 0.f;
+            sum0 += sum;
+            if (h == min(1, np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
+#pragma unroll
+            for (int i = 0; i < HC; i += 32) tmem_st32u(ts + HC * h + i, pk + i);
+          }
+          l_run += sum0;
+        } else {
+          named_arrive(t == 0 ? 7 : 6, 256);
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(&sh->pdone[t]);
+        ++nj;
+      }
+
+      // ---- the segment's end: normalise and write, or leave a partial
+      wait(&sh->ofull[t], (uint32_t)no++);
+      __syncwarp();
+      tc::tc_fence_after();
+      if (warp_on) {
+        const bool whole = sg.c0 == 0 && sg.c1 == sg.nch;
+        const float f = whole ? (l_run > 0.f ? 1.f / l_run : l_run == l_run ? 0.f : l_run) : 1.f;
+        // visible NaN or infinite values of chunks seen in part
+        auto bad_of = [&](int c, int i) {
+          const int n = (has_row ? own_seen(c) : 0) - 32 * i;
+          const uint32_t w = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+          return w & sh->badv[(nj0 + c - sg.c0) % kPtRing][i];
+        };
+        const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
+        uint32_t any_bad = 0u;
+        for (int c = cb; c < sg.c1; ++c)
+          if (sg.masked(c))
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any_bad |= bad_of(c, i);
+        float* part = static_cast<float*>(a.work) +
+                      ((size_t)2 * blockIdx.x + (sg.c0 > 0 ? 0 : 1)) * pt_slot_floats<D>();
+        const int prow = t * kPtRows + r, row = sg.q.row0 + token;
+        const bool write = has_row && DFL_CHECK(row < a.M, status);
+        uint4* out4 = reinterpret_cast<uint4*>(a.out) + ((size_t)row * a.nq + sg.g * grp + head_in) * (D / 8);
+        constexpr int W = 32;  // columns per step
+#pragma unroll 1
+        for (int q = 0; q < D / W; ++q) {
+          const int col = W * q;
+          float o[W];
+          __syncwarp();  // the load below is warp-collective
+          tc::tmem_ld32(to + col, o);
+#pragma unroll
+          for (int k = 0; k < W; ++k) o[k] *= f;
+          if (any_bad)  // added as they are
+            for (int c = cb; c < sg.c1; ++c)
+              if (sg.masked(c))
+                for (int i = 0; i < 4; ++i)
+                  for (uint32_t b = bad_of(c, i); b; b &= b - 1) {
+                    const __nv_bfloat16* v =
+                        static_cast<const __nv_bfloat16*>(a.vb) +
+                        ((size_t)(sg.q.row0 + sg.key0(c) + 32 * i + __ffs(b) - 1) * a.nkv + sg.g) * D + col;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                      const float x = __bfloat162float(v[k]);
+                      if (!(fabsf(x) < INFINITY)) o[k] += x;
+                    }
+                  }
+          __syncwarp();
+          if (whole) {
+            if (write) {
+#pragma unroll
+              for (int k = 0; k < W / 8; ++k)
+                out4[col / 8 + k] = make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
+                                               tt_pack(o[8 * k + 4], o[8 * k + 5]), tt_pack(o[8 * k + 6], o[8 * k + 7]));
+            }
+          } else if (has_row) {
+            float4* p4 = reinterpret_cast<float4*>(part) + (size_t)t * (kPtRows * D / 4);
+#pragma unroll
+            for (int k = 0; k < W / 4; ++k)
+              p4[(size_t)(col / 4 + k) * kPtRows + r] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        if (!whole && has_row) {
+          float* ml = part + (size_t)2 * kPtRows * D;
+          ml[prow] = m_run;
+          ml[2 * kPtRows + prow] = l_run;
+        }
+      }
+    }
+    if (t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of the items that several CTAs shared.  Grid: y = the
+// item's first boundary between runs, so that only shared items' warps do
+// anything; x = (32 rows, CW columns) of the item, one warp each: lanes are
+// rows, so the partials' reads are 512 contiguous bytes; the loads of U
+// partials are in flight at once.
+template <int D, int CW, int U>
+__global__ void __launch_bounds__(128) prompt_tc_merge_kernel(const __grid_constant__ PromptAttnDesc a, int tok, int nb) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, grp = a.nq / a.nkv, tt = 2 * tok;
+  constexpr int CG = D / CW;
+  const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int cg = w % CG, rg = w / CG;
+  // Which item, if any: found beside the attention kernel's last CTAs, for the
+  // lengths it goes by were there before that kernel's own wait ended.
+  PtSpot sp;
+  sp.s = a.n_seqs;
+  int b0 = 0, b1 = 0;
+  const int total = pt_total(a, tt, nullptr), per = (total + nb - 1) / nb;
+  const long long x = (long long)(blockIdx.y + 1) * per;
+  if (x < total) {
+    sp = pt_locate(a, tt, (int)x);
+    const int X = (int)x - sp.c + kPtSetup;  // the item's chunks are [X, X + nch)
+    if (x > X && X / per == (int)blockIdx.y) {  // an item is cut here, for the first time
+      b0 = blockIdx.y;
+      b1 = (X + sp.q.chunks(tt, sp.t) - 1) / per;
+    }
+  }
+  pdl_wait();  // (every CTA: who waits for this kernel waits for the attention too)
+  if (b0 == b1) return;  // none, or written by its CTA
+  const int tile = rg >> 2, prow = (rg & 3) * 32 + lane;
+  const int rt = prow / grp, token = sp.t * tt + tile * tok + rt;
+  const bool has_row = rt < tok && token < sp.q.n;
+  if (!__any_sync(0xffffffffu, has_row)) return;
+  const int mrow = 2 * kPtRows * D + tile * kPtRows + prow;
+  const size_t orow = (size_t)tile * (kPtRows * D) + ((size_t)(cg * (CW / 4)) * kPtRows + prow) * 4;
+  float M = -INFINITY, L = 0.f, o[CW];
+#pragma unroll
+  for (int k = 0; k < CW; ++k) o[k] = 0.f;
+  if (!has_row) return;
+#pragma unroll 1
+  for (int b = b0; b <= b1; b += U) {
+    float4 v[U][CW / 4];
+    float mb[U], lb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int bb = b + u;
+      mb[u] = -INFINITY;
+      lb[u] = 0.f;
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (bb > b1) continue;
+      // slot 0: the item began in an earlier CTA
+      const float* sl = static_cast<const float*>(a.work) + ((size_t)2 * bb + (bb > b0 ? 0 : 1)) * pt_slot_floats<D>();
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) v[u][k] = *reinterpret_cast<const float4*>(sl + orow + (size_t)4 * k * kPtRows);
+      mb[u] = sl[mrow];
+      lb[u] = sl[mrow + 2 * kPtRows];
+    }
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, mb[u]);
+    const float y = M == -INFINITY ? 0.f : tt_ex2(M - Mn);
+    M = Mn;
+    L *= y;
+#pragma unroll
+    for (int k = 0; k < CW; ++k) o[k] *= y;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float e = mb[u] == -INFINITY ? 0.f : tt_ex2(mb[u] - M);
+      L = fmaf(lb[u], e, L);
+#pragma unroll
+      for (int k = 0; k < CW / 4; ++k) {
+        o[4 * k] = fmaf(v[u][k].x, e, o[4 * k]);
+        o[4 * k + 1] = fmaf(v[u][k].y, e, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(v[u][k].z, e, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(v[u][k].w, e, o[4 * k + 3]);
+      }
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)(sp.q.row0 + token) * a.nq +
+                                                                              sp.g * grp + prow - rt * grp) * D + cg * CW);
+#pragma unroll
+  for (int k = 0; k < CW / 8; ++k)
+    out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                        tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                        tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+}
+
+template <int D>
+cudaError_t pt_launch(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
+  using Cfg = PtCfg<D>;
+  PtTma p;
+  p.a = a;
+  p.grp = a.nq / a.nkv;
+  p.tok = kPtRows / p.grp;
+  p.grp_mul = p.grp >= 2 ? (uint32_t)((0x100000000ull + p.grp - 1) / p.grp) : 0u;
+  const uint64_t M = (uint64_t)a.M;
+  bool okm = make_tmap3_bf16(&p.kb, a.kb, D, a.nkv, M, 1, kPtCH) && make_tmap3_bf16(&p.vb, a.vb, D, a.nkv, M, 1, kPtCH) &&
+             make_tmap3_bf16(&p.q3, a.q, D, a.nq, M, p.grp, p.tok);
+  p.kc = p.kb;
+  p.vc = p.vb;
+  if (a.kc) {
+    const uint64_t rows = a.pages ? (uint64_t)a.pool * a.nkv * a.ps : (uint64_t)a.n_seqs * a.nkv * a.cap;
+    okm = okm && make_tmap_bf16(&p.kc, a.kc, D, rows, kPtCH) && make_tmap_bf16(&p.vc, a.vc, D, rows, kPtCH);
+  }
+  if (!okm) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prompt_tc_kernel<D>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
+  if (e != cudaSuccess) return e;
+  constexpr int CW = 32, U = 2, WARPS = 8 * (D / CW);
+  return launch_pdl(prompt_tc_merge_kernel<D, CW, U>, dim3(WARPS / 4, num_sms), dim3(128), 0, st, a, p.tok, num_sms);
+}
+
+}  // namespace
+
+size_t prompt_tc_workspace(const PromptAttnDesc& a, int num_sms) {
+  return (size_t)2 * num_sms * 2 * kPtRows * (a.d + 2) * sizeof(float);
+}
+
+cudaError_t launch_prompt_tc(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
+  return a.d == 128 ? pt_launch<128>(a, num_sms, st) : pt_launch<64>(a, num_sms, st);
+}
+
+}  // namespace dfl

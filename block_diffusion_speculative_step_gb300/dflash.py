@@ -25,11 +25,14 @@ DFLASH_ATTN_BLOCK_BIDIR = 1
 DFLASH_ATTN_TREE = 2
 (DFLASH_OP_EMBED, DFLASH_OP_LAYER, DFLASH_OP_FUSE, DFLASH_OP_DRAFT, DFLASH_OP_VERIFY, DFLASH_OP_PATH,
  DFLASH_OP_SAMPLE_DRAFTS, DFLASH_OP_SAMPLE_ACCEPT, DFLASH_OP_TREE_ATTENTION, DFLASH_OP_TREE_ACCEPT,
- DFLASH_OP_KV_WRITE, DFLASH_OP_KV_READ, DFLASH_OP_TREE_BUILD) = range(13)
+ DFLASH_OP_KV_WRITE, DFLASH_OP_KV_READ, DFLASH_OP_TREE_BUILD, DFLASH_OP_QK_NORM_ROPE,
+ DFLASH_OP_PROMPT_ATTENTION, DFLASH_OP_TOKEN_LOGPROBS) = range(16)
 DFLASH_MAX_LAYERS = 16
 DFLASH_KV_MAX_LAYERS = 64
 DFLASH_MAX_TREE = 128
 DFLASH_TREE_PAD = -2
+DFLASH_NO_TOKEN = -1
+DFLASH_MAX_LOGPROBS = 32
 
 # Every symbol the header exports (checked by the CPU test suite).
 EXPORTS = ("dflash_rope_table", "dflash_embed", "dflash_decoder_layer_forward", "dflash_fuse_context",
@@ -38,7 +41,8 @@ EXPORTS = ("dflash_rope_table", "dflash_embed", "dflash_decoder_layer_forward", 
            "dflash_trace_begin", "dflash_trace_pause", "dflash_trace_read", "dflash_trace_end",
            "dflash_verify_accept_noalloc", "dflash_trace_launches", "dflash_sample_drafts",
            "dflash_sample_accept", "dflash_workspace_control", "dflash_build_flags", "dflash_tree_attention",
-           "dflash_tree_build", "dflash_tree_accept", "dflash_kv_write", "dflash_kv_read")
+           "dflash_tree_build", "dflash_tree_accept", "dflash_kv_write", "dflash_kv_read", "dflash_qk_norm_rope",
+           "dflash_prompt_attention", "dflash_token_logprobs")
 DFLASH_TRACE_FAMILIES = 13
 
 
@@ -159,6 +163,22 @@ class dflash_kv_read_args(C.Structure):
                 ("n_seqs", i32), ("rows", i32), ("base_pos", vp), ("valid", vp)]
 
 
+class dflash_qk_norm_rope_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_seqs", i32), ("rows", i32), ("base_pos", vp), ("qkv", vp),
+                ("qkv_stride", C.c_int64), ("qkv_dtype", i32), ("q_norm", vp), ("k_norm", vp), ("rope_cs", vp),
+                ("rope_max_pos", i32), ("q", vp), ("kb", vp), ("vb", vp), ("kv", dflash_kv)]
+
+
+class dflash_prompt_attention_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_seqs", i32), ("n_rows", i32), ("row_start", vp), ("base_pos", vp), ("q", vp),
+                ("kb", vp), ("vb", vp), ("kv", dflash_kv), ("max_pos", i32), ("scale", f32), ("out", vp)]
+
+
+class dflash_token_logprobs_args(C.Structure):
+    _fields_ = [("dims", dflash_dims), ("n_rows", i32), ("logits", vp), ("temperature", f32), ("tokens", vp),
+                ("logprob", vp), ("entropy", vp), ("topk", i32), ("top_ids", vp), ("top_logprobs", vp)]
+
+
 class dflash_trace_stat(C.Structure):
     _fields_ = [("name", C.c_char * 24), ("launches", i32), ("total_ms", C.c_double), ("bytes", C.c_double)]
 
@@ -178,7 +198,7 @@ def lib(path: str | None = None):
         for name in ("dflash_embed", "dflash_decoder_layer_forward", "dflash_fuse_context", "dflash_draft_block",
                      "dflash_verify_accept", "dflash_path_select", "dflash_sample_drafts", "dflash_sample_accept",
                      "dflash_tree_attention", "dflash_tree_build", "dflash_tree_accept", "dflash_kv_write",
-                     "dflash_kv_read"):
+                     "dflash_kv_read", "dflash_qk_norm_rope", "dflash_prompt_attention", "dflash_token_logprobs"):
             getattr(L, name).argtypes = [vp, vp, C.c_size_t, vp]
             getattr(L, name).restype = C.c_int
         L.dflash_rope_table.argtypes = [f32, i32, i32, vp, vp]
@@ -327,6 +347,18 @@ def dflash_kv_write(args: dflash_kv_write_args, ws_ptr: int, ws_bytes: int, stre
 
 def dflash_kv_read(args: dflash_kv_read_args, ws_ptr: int, ws_bytes: int, stream=None):
     _call("dflash_kv_read", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_qk_norm_rope(args: dflash_qk_norm_rope_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_qk_norm_rope", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_prompt_attention(args: dflash_prompt_attention_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_prompt_attention", args, ws_ptr, ws_bytes, stream)
+
+
+def dflash_token_logprobs(args: dflash_token_logprobs_args, ws_ptr: int, ws_bytes: int, stream=None):
+    _call("dflash_token_logprobs", args, ws_ptr, ws_bytes, stream)
 
 
 def dflash_trace_begin(max_launches: int = 4096):

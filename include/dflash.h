@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define DFLASH_ABI_VERSION 9
+#define DFLASH_ABI_VERSION 10
 #define DFLASH_MAX_LAYERS 16 /* draft layers handled by one fuse / draft call */
 
 typedef struct CUstream_st* dflash_stream_t; /* == cudaStream_t */
@@ -89,7 +89,10 @@ typedef enum {
   DFLASH_OP_TREE_ACCEPT = 9,
   DFLASH_OP_KV_WRITE = 10,
   DFLASH_OP_KV_READ = 11,
-  DFLASH_OP_TREE_BUILD = 12
+  DFLASH_OP_TREE_BUILD = 12,
+  DFLASH_OP_QK_NORM_ROPE = 13,
+  DFLASH_OP_PROMPT_ATTENTION = 14,
+  DFLASH_OP_TOKEN_LOGPROBS = 15
 } dflash_op;
 
 /* Shapes and arithmetic of one decoder stack. */
@@ -661,6 +664,104 @@ typedef struct {
   const int32_t* valid;       /* [n_seqs] or NULL: all rows */
 } dflash_kv_read_args;
 int dflash_kv_read(const dflash_kv_read_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * Prompts.  A prompt pass runs the target over sequences of different lengths
+ * packed one behind the other: M token rows, sequence s's being
+ * [row_start[s], row_start[s+1]), row i of it at position base_pos[s] + i.
+ *
+ * dflash_qk_norm_rope: what stands between the QKV projection and the
+ * attention of a model that normalises every query and key head:
+ *   y = x / sqrt(mean(x^2) + rms_eps) * gain   (per head; no gain: y = x),
+ *   (y_i, y_{i+d/2}) rotated by the position (rotate-half, dflash_rope_table),
+ * in fp32, rounded once to dims.dtype; values are rounded and not turned.
+ * Row m of the M = n_seqs * rows rows belongs to sequence m / rows and sits at
+ * position base_pos[m / rows] + m % rows (packed prompts and trees: n_seqs =
+ * M, rows = 1, base_pos = the rows' positions).  Keys and values go to kb /
+ * vb, token-major, or, where those are NULL, to the cache kv at slot =
+ * position (contiguous or paged, dims.dtype; an 8-bit cache is refused:
+ * dflash_kv_write fills it from kb / vb).
+ * A row outside the RoPE table, or a slot outside the cache or on an unmapped
+ * page, raises DFLASH_ERR_INVALID_ARG in the status word: the row (its keys
+ * and values) is not written.  Outputs must not overlap qkv.
+ */
+typedef struct {
+  dflash_dims dims;        /* n_q_heads, n_kv_heads, head_dim, rms_eps, dtype are used */
+  int32_t n_seqs, rows;
+  const int32_t* base_pos; /* [n_seqs] */
+  const void* qkv;         /* [M][qkv_stride]: query heads, key heads, value heads */
+  int64_t qkv_stride;      /* elements, a multiple of 8; 0: (n_q + 2 n_kv) * head_dim */
+  int32_t qkv_dtype;       /* dflash_dtype of qkv */
+  const void* q_norm;      /* [head_dim] gains of dims.dtype, or NULL: no norm */
+  const void* k_norm;
+  const float* rope_cs;    /* dflash_rope_table output */
+  int32_t rope_max_pos;
+  void* q;                 /* out [M][n_q*d] */
+  void* kb;                /* out [M][n_kv][d], or NULL: the cache */
+  void* vb;
+  dflash_kv kv;            /* kb == NULL: the cache (window 0) */
+} dflash_qk_norm_rope_args;
+int dflash_qk_norm_rope(const dflash_qk_norm_rope_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * dflash_prompt_attention: per query head, for row i of sequence s
+ *   out = softmax_j(scale * q . k_j) v_j  over the cache slots j < base_pos[s]
+ *   and the sequence's own rows j <= i (kb / vb).
+ * Sequences may be empty.  Rows that belong to no sequence (before
+ * row_start[0], behind row_start[n_seqs]) are not read and their outputs are
+ * left as they were.  What a row does not see may hold anything; a NaN or
+ * infinity that it sees makes the outputs that it reaches NaN or infinite.  A
+ * row_start outside [0, n_rows] or below the one before it raises
+ * DFLASH_ERR_INVALID_ARG in the status word and nothing is written; a base_pos
+ * outside [0, max_pos] raises it and is taken as the nearest value in range.
+ * The softmax runs in fp32; with bf16 the weights enter their product with the
+ * values as two bf16 terms (2^-16 relative).  A call is deterministic; the
+ * work is cut into pieces that depend on all the lengths of the launch, so a
+ * sequence's last bits may differ with the batch it runs in.
+ */
+typedef struct {
+  dflash_dims dims;
+  int32_t n_seqs;
+  int32_t n_rows;           /* M, the rows of q, kb, vb and out */
+  const int32_t* row_start; /* [n_seqs + 1] */
+  const int32_t* base_pos;  /* [n_seqs] cached positions of each sequence, or NULL: none (kv is then not read) */
+  const void* q;            /* [M][n_q*d] rotated queries */
+  const void* kb;           /* [M][n_kv][d] rotated keys of the rows */
+  const void* vb;           /* [M][n_kv][d] */
+  dflash_kv kv;             /* the context; contiguous or paged, dims.dtype, window 0 (8 bits are refused) */
+  int32_t max_pos;          /* with base_pos: base_pos[s] <= max_pos <= capacity */
+  float scale;              /* 0: 1 / sqrt(head_dim) */
+  void* out;                /* [M][n_q*d] */
+} dflash_prompt_attention_args;
+int dflash_prompt_attention(const dflash_prompt_attention_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * dflash_token_logprobs: for every row of logits, p = softmax(logits / T):
+ *   logprob[m]  = log p(tokens[m])
+ *   entropy[m]  = - sum_v p(v) log p(v)
+ *   top_ids[m][0..topk-1], top_logprobs[m][..]: the topk most likely tokens
+ *   (descending; the lowest index first on equal logits) and their log p.
+ * Each output is optional.  Logits may be -inf (probability 0, log p -inf).  A
+ * row with a NaN or +inf, or of nothing but -inf, raises DFLASH_ERR_NUMERIC in
+ * the status word: its values are NaN, its top_ids -1.  A token outside [0, V)
+ * has no log probability: its logprob is left as it was, and any but
+ * DFLASH_NO_TOKEN raises DFLASH_ERR_INVALID_ARG in the status word.
+ */
+#define DFLASH_NO_TOKEN (-1)
+#define DFLASH_MAX_LOGPROBS 32
+typedef struct {
+  dflash_dims dims;       /* vocab is used */
+  int32_t n_rows;
+  const float* logits;    /* [n_rows][V] */
+  float temperature;      /* > 0 */
+  const int32_t* tokens;  /* [n_rows], or NULL (logprob is then not written) */
+  float* logprob;         /* out [n_rows], or NULL */
+  float* entropy;         /* out [n_rows], or NULL */
+  int32_t topk;           /* 0 .. DFLASH_MAX_LOGPROBS, at most V */
+  int32_t* top_ids;       /* out [n_rows][topk] */
+  float* top_logprobs;    /* out [n_rows][topk] */
+} dflash_token_logprobs_args;
+int dflash_token_logprobs(const dflash_token_logprobs_args* a, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
 /* Bytes of workspace `op` needs for these arguments (args points to the
  * op's argument struct); 0 on invalid arguments. */
