@@ -83,6 +83,7 @@ GemmDesc gemm_base(int dtype, int M, int K, const void* X, const int32_t* base_p
 // ----------------------------------------------------------- decoder layer
 
 struct LayerScratch {
+  float* qkv;  // the projection's sums, ahead of the head norms
   void *x, *x2, *q, *kb, *vb, *attn, *act;  // x: attention input, x2: MLP input (the same buffer by default)
   float* apart;
   void* gpart;
@@ -106,6 +107,12 @@ struct LayerShape {
   dflash_kv kv;                // DFLASH_ATTN_TREE: the cache
   const int32_t* tree_parent;  // DFLASH_ATTN_TREE (see dflash_layer_args)
   const int32_t* tree_pos;
+  // DFLASH_ATTN_PROMPT: S == 1 and rows is every row
+  int prompts;
+  bool context;                // with cached positions
+  const int32_t* prompt_start;
+  const void *q_norm, *k_norm;
+  bool norm() const { return q_norm || k_norm; }
 };
 
 void layer_gemms(const LayerShape& L, const dflash_layer_weights* w, GemmDesc* g4) {
@@ -137,11 +144,19 @@ void layer_gemms(const LayerShape& L, const dflash_layer_weights* w, GemmDesc* g
   g4[1] = o;
   g4[2] = gu;
   g4[3] = dn;
-  // A tree's rows carry their own positions: every row is a sequence of one
+  // A tree's (and packed prompts') rows carry their own positions: every row is a sequence of one
   // row to the projections (base_pos is then the row's position), and its
   // keys and values land token-major.
-  if (L.mode == DFLASH_ATTN_TREE)
+  if (L.mode == DFLASH_ATTN_TREE || L.mode == DFLASH_ATTN_PROMPT)
     for (int j = 0; j < 4; ++j) g4[j].rows = 1;
+  if (L.norm()) {  // norms and rotation follow the projection
+    g4[0].kind = EPI_STORE;
+    g4[0].ldo = g4[0].seg_rows;
+  }
+}
+
+PromptAttnDesc layer_prompt_desc(const LayerShape& L) {
+  return prompt_attn_desc(L.d, L.prompts, L.rows, L.context, L.max_pos, L.kv, 0.f);
 }
 
 AttnDesc attn_shape(const LayerShape& L) {
@@ -175,7 +190,10 @@ void carve_layer(Bump& b, const LayerShape& L, int sms, LayerScratch& s, int con
   s.apart = static_cast<float*>(b.take(
       L.mode == DFLASH_ATTN_TREE
           ? tree_attn_workspace(tree_attn_desc(d, L.S, L.rows, L.max_pos - L.rows, L.kv, 0.f), sms)
-          : attn_workspace(attn_shape(L))));
+      : L.mode == DFLASH_ATTN_PROMPT ? prompt_attn_workspace(layer_prompt_desc(L), sms)
+                                     : attn_workspace(attn_shape(L))));
+  s.qkv = nullptr;
+  if (L.norm()) s.qkv = static_cast<float*>(b.take(M * (QD + 2 * (size_t)d.n_kv_heads * d.head_dim) * sizeof(float)));
   GemmDesc g4[4];
   layer_gemms(L, nullptr, g4);
   size_t gp = 0;
@@ -219,6 +237,14 @@ static double conv_bytes(const LayerShape& L, const LayerConv& cv) {
 }
 
 int check_layer_shape(const LayerShape& L, const char* who) {
+  if (L.mode == DFLASH_ATTN_PROMPT) {
+    const int rc = check_prompt_shape(L.d, L.prompts, L.rows, L.context, L.max_pos, L.kv, who);
+    if (rc) return rc;
+    DF_CHECK((long)L.rows * (L.d.n_q_heads + 2l * L.d.n_kv_heads) < (1l << 31), "%s: too many heads in all", who);
+    return DFLASH_OK;
+  }
+  if (L.norm() && L.mode == DFLASH_ATTN_BLOCK_BIDIR)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: bidirectional blocks take no head norms", who);
   DF_CHECK(L.S > 0 && L.rows > 0, "%s: n_seqs and rows must be positive", who);
   DF_CHECK(L.mode == DFLASH_ATTN_CAUSAL || L.mode == DFLASH_ATTN_BLOCK_BIDIR || L.mode == DFLASH_ATTN_TREE,
            "%s: bad attn_mode", who);
@@ -277,6 +303,7 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   layer_gemms(L, &w, g4);
   for (auto& g : g4) g.base_pos = base_pos;
   const bool causal = L.mode == DFLASH_ATTN_CAUSAL, tree = L.mode == DFLASH_ATTN_TREE;
+  const bool prompt = L.mode == DFLASH_ATTN_PROMPT;
 
   DF_LAUNCH(st, TF_RMSNORM, 0, launch_rmsnorm(d.dtype, h, w.ln1, M, H, d.rms_eps, s.x, st));
   if (cv) DF_LAUNCH(st, TF_CONV, conv_bytes(L, *cv), layer_conv(L, *cv, 0, s.x, s.xc, 0, s, st));
@@ -290,13 +317,33 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
   qkv.k_dst[0] = direct ? kv.k : s.kb;
   qkv.v_dst[0] = direct ? kv.v : s.vb;
   qkv.kv_cap = direct ? kv.capacity : qkv.rows;
-  if (tree) qkv.base_pos = L.tree_pos;
+  if (tree || prompt) qkv.base_pos = L.tree_pos;
   qkv.kv_window = 0;
   qkv.kv_slot_mode = direct ? 1 : 0;
   qkv.rope_cs = rope_cs;
   qkv.rope_max_pos = rope_max_pos;
+  if (L.norm()) {
+    qkv.out_f32 = s.qkv;
+    qkv.base_pos = nullptr;
+  }
   DF_CUDA(run_gemm(qkv, s.gpart, s.gpart_bytes, c, sms, st));
-  if (causal && kv.pages) {
+  if (L.norm()) {
+    QkNormDesc n = qk_norm_desc(d, M, causal ? L.rows : 1, causal ? &kv : nullptr);
+    n.src_dtype = DFLASH_F32;
+    n.base_pos = causal ? base_pos : L.tree_pos;
+    n.qkv = s.qkv;
+    n.q_norm = L.q_norm;
+    n.k_norm = L.k_norm;
+    n.rope_cs = rope_cs;
+    n.rope_max_pos = rope_max_pos;
+    n.q = s.q;
+    if (!causal) {
+      n.k = s.kb;
+      n.v = s.vb;
+    }
+    n.status = c.status;
+    DF_LAUNCH(st, TF_ROPE, (double)M * qkv.seg_rows * (4 + elem_size(d.dtype)), launch_qk_norm(n, st));
+  } else if (causal && kv.pages) {
     KvScatter ks = kv_scatter_base(L.d, L.S, L.rows, base_pos, nullptr, 0, kv.capacity, rope_max_pos, kv, c);
     ks.kb[0] = s.kb;
     ks.vb[0] = s.vb;
@@ -320,6 +367,20 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
     t.work = s.apart;
     t.status = c.status;
     DF_LAUNCH(st, TF_ATTN, 0, launch_tree_attention(t, sms, st));
+  } else if (prompt) {
+    PromptAttnDesc t = layer_prompt_desc(L);
+    t.row_start = L.prompt_start;
+    t.base_pos = base_pos;
+    t.pos = L.tree_pos;
+    t.pos_end = rope_max_pos;
+    t.zero_pad = 1;  // (as for a tree)
+    t.q = s.q;
+    t.kb = s.kb;
+    t.vb = s.vb;
+    t.out = s.attn;
+    t.work = s.apart;
+    t.status = c.status;
+    DF_LAUNCH(st, TF_ATTN, 0, launch_prompt_attention(t, sms, st));
   } else {
   AttnDesc a = attn_shape(L);
   a.base_pos = base_pos;
@@ -418,6 +479,10 @@ LayerShape draft_layer_shape(const dflash_draft_args* a, int j) {
   L.kv = a->kv_layers[j];
   L.tree_parent = nullptr;
   L.tree_pos = nullptr;
+  L.prompts = 0;
+  L.context = false;
+  L.prompt_start = nullptr;
+  L.q_norm = L.k_norm = nullptr;
   return L;
 }
 
@@ -627,6 +692,16 @@ static LayerShape layer_shape_of(const dflash_layer_args* a) {
   L.kv = a->kv;
   L.tree_parent = a->tree_parent;
   L.tree_pos = a->tree_pos;
+  L.prompts = 0;
+  L.context = false;
+  if (L.mode == DFLASH_ATTN_PROMPT) {
+    L.S = 1;
+    L.prompts = a->n_seqs;
+    L.context = a->base_pos != nullptr;
+  }
+  L.prompt_start = a->prompt_start;
+  L.q_norm = a->q_norm;
+  L.k_norm = a->k_norm;
   return L;
 }
 
@@ -654,16 +729,24 @@ int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws
   if (rc) return rc;
   rc = check_weights(a->w, who);
   if (rc) return rc;
-  DF_CHECK(a->base_pos && a->h && a->kv.k && a->kv.v && a->rope_cs, "%s: NULL pointer", who);
   LayerShape L = layer_shape_of(a);
-  const bool tree = L.mode == DFLASH_ATTN_TREE;
+  const bool tree = L.mode == DFLASH_ATTN_TREE, prompt = L.mode == DFLASH_ATTN_PROMPT;
+  DF_CHECK(a->h && a->rope_cs, "%s: NULL pointer", who);
+  DF_CHECK((prompt && !L.context) || (a->base_pos && a->kv.k && a->kv.v), "%s: NULL pointer", who);
+  DF_CHECK(aligned16(a->q_norm) && aligned16(a->k_norm), "%s: q_norm and k_norm must be 16-byte aligned", who);
+  DF_CHECK(!L.norm() || (aligned16(a->rope_cs) && aligned16(a->kv.k) && aligned16(a->kv.v)),
+           "%s: head norms need a 16-byte aligned RoPE table and cache", who);
+  if (prompt) {
+    DF_CHECK(a->tree_pos && a->prompt_start, "%s: DFLASH_ATTN_PROMPT needs tree_pos and prompt_start", who);
+    DF_CHECK(!L.context || (aligned16(a->kv.k) && aligned16(a->kv.v)), "%s: cache pointers must be 16-byte aligned", who);
+  }
   if (tree) {
     DF_CHECK(a->tree_pos, "%s: DFLASH_ATTN_TREE needs tree_pos", who);
     rc = check_tree_kv(a->kv, who);
     if (rc) return rc;
   }
-  // (a tree's positions are its own: the attention checks them)
-  DF_CHECK(tree ? a->rope_max_pos > 0 : a->max_pos <= a->rope_max_pos, "%s: max_pos %d beyond the RoPE table (%d)", who,
+  // (a tree's and a prompt's positions are their own: the attention checks them)
+  DF_CHECK(tree || prompt ? a->rope_max_pos > 0 : a->max_pos <= a->rope_max_pos, "%s: max_pos %d beyond the RoPE table (%d)", who,
            a->max_pos, a->rope_max_pos);
   {
     const void* st[] = {a->out_x_attn, a->out_q, a->out_kb, a->out_vb, a->out_attn, a->out_x_mlp, a->out_act};

@@ -282,6 +282,9 @@ struct PromptAttnDesc {
   const int32_t* pages;
   int ps, max_pages, pool;
   int max_pos;                // bound on base_pos (0 without)
+  const int32_t* pos;         // [M] or null: the rows' positions, below pos_end
+  int pos_end;
+  int zero_pad;               // write 0 to rows of no sequence, instead of leaving them as they were
   float scale;                // times log2 e: scores in log2 units
   void* out;                  // [M][nq*d]
   void* work;                 // partials

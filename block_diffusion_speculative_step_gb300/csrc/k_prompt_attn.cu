@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "prompt_attn.cuh"
 
 namespace dfl {
 
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
   constexpr int QP = C::QP, VP = C::VP, OC = D / 16;
   extern __shared__ __align__(16) float ps_smem[];
   float *Qs = ps_smem + C::Q_OFF, *Ks = ps_smem + C::K_OFF, *Vs = ps_smem + C::V_OFF, *Ps = ps_smem + C::P_OFF;
-  __shared__ int sh_s, sh_tile;
+  __shared__ int sh_s, sh_tile, sh_good;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, grp = a.nq / a.nkv, g = blockIdx.y;
@@ -102,13 +103,17 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (bad || far) raise_status(a.status, ST_RANGE);
-    if (__any_sync(0xffffffffu, bad)) s = -1;  // row_start leaves [0, M] or decreases: nothing is computed
+    const bool good = !__any_sync(0xffffffffu, bad);
+    if (!good) s = -1;  // row_start leaves [0, M] or decreases: nothing is computed
     if (tid == 0) {
+      sh_good = good;
       sh_s = s;
       sh_tile = t;
     }
   }
   __syncthreads();
+  if ((a.pos || a.zero_pad) && blockIdx.y == 0 && blockIdx.z == 0)
+    prompt_layer_rows<float>(a, sh_good, (long long)blockIdx.x * kPsThreads + tid, (long long)gridDim.x * kPsThreads);
   const int s = sh_s;
   if (s < 0) return;
   bool bad = false, far = false;

@@ -42,6 +42,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "prompt_attn.cuh"
 #include "tc_ptx.cuh"
 #include "tmap.h"
 
@@ -84,6 +85,7 @@ struct PtCfg {
 struct PtShared {  // after the tiles
   uint32_t badv[kPtRing][4];  // own rows whose V holds a NaN or infinity, by chunk counter
   int s0, g0, t0, c0, len;    // the CTA's run: first item, position in it, number of positions
+  int good;                   // row_start is in order
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];
   uint64_t sfull[2], pdone[2], ofull[2], qfull[2], qfree[2];
   uint32_t tslot;
@@ -142,7 +144,7 @@ __device__ __forceinline__ PtSeq pt_seq(const PromptAttnDesc& a, int tt, int s) 
 
 // All positions (one warp); none where row_start leaves [0, M] or decreases.
 // status (or null): told of that, and of contexts out of range.
-__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status) {
+__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status, bool* good) {
   int t = 0;
   bool bad = false, far = false;
   for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
@@ -152,7 +154,8 @@ __device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_
     if (!bad) t += q.before(tt, q.T) * a.nkv;
   }
   if ((bad || far) && status) raise_status(status, ST_RANGE);
-  return __any_sync(0xffffffffu, bad) ? 0 : __reduce_add_sync(0xffffffffu, t);
+  *good = !__any_sync(0xffffffffu, bad);
+  return *good ? __reduce_add_sync(0xffffffffu, t) : 0;
 }
 
 // The item at position x of the flat order, and the position c in it (one warp).
@@ -327,7 +330,8 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
-    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr);
+    bool good;
+    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good);
     const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     const int x0 = (int)min((long long)blockIdx.x * per, (long long)total), len = min(per, total - x0);
     PtSpot sp;
@@ -339,11 +343,14 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
       sh->t0 = sp.t;
       sh->c0 = sp.c;
       sh->len = sp.s < a.n_seqs ? len : 0;
+      sh->good = good;
     }
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (a.pos || a.zero_pad)
+    prompt_layer_rows<__nv_bfloat16>(a, sh->good, blockIdx.x * Cfg::THREADS + tid, (long long)gridDim.x * Cfg::THREADS);
   const uint32_t tmem = sh->tslot;
   const uint64_t lim_ns = wait_limit_ns(status);
   const bool stall = stall_kv_loads(status);  // test switch: issue no K/V copy
@@ -815,7 +822,8 @@ __global__ void __launch_bounds__(128) prompt_tc_merge_kernel(const __grid_const
   PtSpot sp;
   sp.s = a.n_seqs;
   int b0 = 0, b1 = 0;
-  const int total = pt_total(a, tt, nullptr), per = (total + nb - 1) / nb;
+  bool good;
+  const int total = pt_total(a, tt, nullptr, &good), per = (total + nb - 1) / nb;
   const long long x = (long long)(blockIdx.y + 1) * per;
   if (x < total) {
     sp = pt_locate(a, tt, (int)x);

@@ -23,6 +23,7 @@ DFLASH_BF16 = 1
 DFLASH_ATTN_CAUSAL = 0
 DFLASH_ATTN_BLOCK_BIDIR = 1
 DFLASH_ATTN_TREE = 2
+DFLASH_ATTN_PROMPT = 3
 (DFLASH_OP_EMBED, DFLASH_OP_LAYER, DFLASH_OP_FUSE, DFLASH_OP_DRAFT, DFLASH_OP_VERIFY, DFLASH_OP_PATH,
  DFLASH_OP_SAMPLE_DRAFTS, DFLASH_OP_SAMPLE_ACCEPT, DFLASH_OP_TREE_ATTENTION, DFLASH_OP_TREE_ACCEPT,
  DFLASH_OP_KV_WRITE, DFLASH_OP_KV_READ, DFLASH_OP_TREE_BUILD, DFLASH_OP_QK_NORM_ROPE,
@@ -83,7 +84,8 @@ class dflash_layer_args(C.Structure):
                 ("base_pos", vp), ("h", vp), ("kv", dflash_kv), ("attn_mode", i32), ("max_pos", i32),
                 ("rope_cs", vp), ("rope_max_pos", i32), ("tap", vp), ("tap_stride", i32),
                 ("tap_offset", i32), ("out_x_attn", vp), ("out_q", vp), ("out_kb", vp), ("out_vb", vp),
-                ("out_attn", vp), ("out_x_mlp", vp), ("out_act", vp), ("tree_parent", vp), ("tree_pos", vp)]
+                ("out_attn", vp), ("out_x_mlp", vp), ("out_act", vp), ("tree_parent", vp), ("tree_pos", vp),
+                ("prompt_start", vp), ("q_norm", vp), ("k_norm", vp)]
 
 
 class dflash_fuse_args(C.Structure):

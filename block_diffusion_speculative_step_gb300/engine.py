@@ -147,6 +147,8 @@ class Engine:
             a.tap = _ptr(tap)
             a.tap_stride = self.F * t.hidden
             a.tap_offset = tap_offset
+        L = self.m["target"]["layers"][li]
+        a.q_norm, a.k_norm = _ptr(L.get("q_norm")), _ptr(L.get("k_norm"))
         return a
 
     def fuse_args(self, rows: int, feats, base_pos, valid):
@@ -315,17 +317,21 @@ class Engine:
         a.out_kb, a.out_vb = _ptr(self.tkb[li]), _ptr(self.tvb[li])
         return a
 
-    def kv_write_args(self, j0: int, n: int, rows: int, base_pos, valid=None, row_index=None):
-        """Commits rows of the target's layers [j0, j0 + n), n <= DFLASH_KV_MAX_LAYERS."""
+    def kv_write_args(self, j0: int, n: int, rows: int, base_pos, valid=None, row_index=None, source=None, seq=None):
+        """Commits rows of the target's layers [j0, j0 + n), n <= DFLASH_KV_MAX_LAYERS:
+        the last tree forward's, or source (keys, values: a list of layers
+        each); seq: to that sequence's cache alone."""
         a = D.dflash_kv_write_args()
         a.dims = self.tdims
         a.n_layers = n
-        kb = (C.c_void_p * n)(*[_ptr(x) for x in self.tkb[j0:j0 + n]])
-        vb = (C.c_void_p * n)(*[_ptr(x) for x in self.tvb[j0:j0 + n]])
-        kv = (D.dflash_kv * n)(*[self._kv("t", j) for j in range(j0, j0 + n)])
+        keys, values = source or (self.tkb, self.tvb)
+        kb = (C.c_void_p * n)(*[_ptr(x) for x in keys[j0:j0 + n]])
+        vb = (C.c_void_p * n)(*[_ptr(x) for x in values[j0:j0 + n]])
+        kv = (D.dflash_kv * n)(*[self._kv("t", j) if seq is None else self._seq_kv("t", j, seq)
+                                 for j in range(j0, j0 + n)])
         a._keep = (kb, vb, kv)  # host arrays, read during the call
         a.kb, a.vb, a.kv_layers = (C.cast(x, C.c_void_p) for x in a._keep)
-        a.n_seqs, a.rows = self.S, rows
+        a.n_seqs, a.rows = self.S if seq is None else 1, rows
         a.base_pos, a.valid, a.row_index = _ptr(base_pos), _ptr(valid), _ptr(row_index)
         return a
 
@@ -443,7 +449,7 @@ class Engine:
         idx = self.t_path[:, :rows].clamp(min=0).long()[:, :, None].expand(S, rows, f.shape[2])
         self.fuse_with(f.gather(1, idx).view(S * rows, *self.feats.shape[1:]), rows, self.commit_base, self.commit_count)
 
-    def tree_generate(self, prompts: torch.Tensor, n_new: int):
+    def tree_generate(self, prompts, n_new: int):
         """Greedy generation by tree cycles: the tokens and, per cycle, the accepted counts."""
         self.prefill(prompts)
         outs = [[int(a)] for a in self.anchor.cpu()]
@@ -455,6 +461,156 @@ class Engine:
             for s in range(self.S):
                 outs[s].extend(int(t) for t in toks[s, :int(k[s]) + 1])
         return torch.tensor([o[:n_new] for o in outs], dtype=torch.int32), torch.stack(accepts, 1)
+
+    # ---------------------------------------------------------------- prompts
+
+    FUSE_ROWS = 256  # rows of one sequence that a projection takes at once
+
+    def prompt_layer_args(self, li: int, n: int, n_rows: int, h, start, pos, base_pos=None, tap=None, tap_offset=0):
+        """Target layer li over n packed prompts of n_rows rows in all, over
+        the base_pos [n] cached positions of each (None: none)."""
+        a = self.target_layer_args(li, n_rows, h, tap, tap_offset)
+        a.n_seqs, a.attn_mode = n, D.DFLASH_ATTN_PROMPT
+        a.base_pos = _ptr(base_pos)
+        a.prompt_start, a.tree_pos = _ptr(start), _ptr(pos)
+        a.out_kb, a.out_vb = _ptr(self.pkb[li]), _ptr(self.pvb[li])
+        return a
+
+    def _seq_kv(self, kind: str, j: int, s: int):
+        """The dflash_kv of sequence s alone."""
+        kv = self._kv(kind, j)
+        if kind in self.paging:
+            kv.pages += 4 * s * kv.max_pages
+            return kv
+        ks, vs = (self.caches.tk, self.caches.tv) if kind == "t" else (self.caches.dk, self.caches.dv)
+        kv.k, kv.v = _ptr(ks[j][s]), _ptr(vs[j][s])
+        if kv.k_exp:
+            kv.k_exp, kv.v_exp = _ptr(self.caches.tke[j][s]), _ptr(self.caches.tve[j][s])
+        return kv
+
+    def _prompt_buffers(self, n_rows: int, longest: int):
+        """Buffers and workspace of target forwards over n_rows packed rows."""
+        t, w = self.w.target, self.w
+        if getattr(self, "prompt_rows", 0) < n_rows:
+            self.prompt_rows = n_rows
+            new = lambda *shape, dt=None: torch.zeros(shape, dtype=dt or self.dt, device=self.dev)
+            self.ph = new(n_rows, t.hidden, dt=torch.float32)
+            self.pfeats = new(n_rows, self.F, t.hidden)
+            self.pkb = [new(n_rows, t.n_kv, t.head_dim) for _ in range(t.layers)]
+            self.pvb = [new(n_rows, t.n_kv, t.head_dim) for _ in range(t.layers)]
+        # (the pointers that the sizes depend on are set, whatever they point to)
+        layer = self.prompt_layer_args(0, self.S, n_rows, self.ph, self.base_pos, self.base_pos,
+                                       None if self.kv8 else self.base_pos)
+        whole = self.prompt_layer_args(0, self.S, n_rows, self.ph, self.base_pos, self.base_pos)
+        need = max(D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, layer), D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, whole),
+                   D.dflash_workspace_bytes(D.DFLASH_OP_FUSE, self.fuse_args(min(longest, self.FUSE_ROWS), self.pfeats, self.base_pos, None)),
+                   D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.verify_args(1, self.h)))
+        if need > self.ws_bytes:
+            self._new_workspace(int(need))
+
+    def _prompt_forward(self, prompts, done):
+        """One target forward over prompts (one tensor a sequence, maybe
+        empty) behind the done [S] positions that the caches hold of each:
+        residuals in self.ph, keys, values and tap features committed."""
+        S, t = self.S, self.w.target
+        lens = [int(p.numel()) for p in prompts]
+        start = [0]
+        for n in lens:
+            start.append(start[-1] + n)
+        M = start[-1]
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=self.dev)
+        start_d, done_d = i32(start), i32(done)
+        pos = torch.cat([torch.arange(b, b + n, dtype=torch.int32, device=self.dev) for b, n in zip(done, lens)])
+        tokens = torch.cat([p.view(-1) for p in prompts]).int().to(self.dev)
+        self._prompt_buffers(M, max(lens))
+        ws = (self.ws_ptr, self.ws_bytes)
+        e = self.embed_args(self.tdims, 1, self.ph, tokens)
+        e.n_seqs = M
+        D.dflash_embed(e, *ws)
+        for li in range(t.layers):
+            tapped = li in self.w.taps
+            D.dflash_decoder_layer_forward(
+                self.prompt_layer_args(li, S, M, self.ph, start_d, pos, done_d if any(done) else None,
+                                       self.pfeats if tapped else None,
+                                       self.w.taps.index(li) * t.hidden if tapped else 0), *ws)
+        for s, n in enumerate(lens):
+            if n == 0:
+                continue
+            r = slice(start[s], start[s] + n)
+            source = [x[r] for x in self.pkb], [x[r] for x in self.pvb]
+            for j in range(0, t.layers, D.DFLASH_KV_MAX_LAYERS):
+                k = min(D.DFLASH_KV_MAX_LAYERS, t.layers - j)
+                D.dflash_kv_write(self.kv_write_args(j, k, n, done_d[s:], source=source, seq=s), *ws)
+            at = i32(list(range(done[s], done[s] + n, self.FUSE_ROWS)))
+            for i, r0 in enumerate(range(0, n, self.FUSE_ROWS)):
+                f = self.fuse_args(min(self.FUSE_ROWS, n - r0), self.pfeats[start[s] + r0:], at[i:], None)
+                f.n_seqs = 1
+                for j in range(self.w.draft.layers):
+                    f.kv_layers[j] = self._seq_kv("d", j, s)
+                D.dflash_fuse_context(f, *ws)
+        return start
+
+    def prefill_packed(self, prompts, piece: int = 0, each=None):
+        """Prompts of different lengths, one int32 tensor a sequence: as
+        prefill.  piece > 0 takes at most that many tokens of a sequence at a
+        time (a bound on the buffers), the later ones over the cache; an 8-bit
+        cache takes whole prompts only.  each(done, start) follows every
+        forward, whose residual rows are self.ph[start[s]:start[s + 1]]."""
+        S = self.S
+        lens = [int(p.numel()) for p in prompts]
+        assert len(prompts) == S and min(lens) >= 1 and max(lens) + self.B <= self.cap
+        piece = piece or max(lens)
+        assert not self.kv8 or piece >= max(lens), "an 8-bit cache takes whole prompts"
+        last = torch.zeros(S, self.w.target.hidden, dtype=torch.float32, device=self.dev)
+        for c0 in range(0, max(lens), piece):
+            done = [min(n, c0) for n in lens]
+            start = self._prompt_forward([p.view(-1)[c0:c0 + piece] for p in prompts], done)
+            for s, n in enumerate(lens):
+                if c0 < n <= c0 + piece:
+                    last[s] = self.ph[start[s + 1] - 1]
+            if each is not None:
+                each(done, start)
+        self.base_pos.copy_(torch.tensor([n - 1 for n in lens], dtype=torch.int32))
+        self.h[:S].copy_(last)
+        self.verify(1)  # anchor := greedy token after the prompt, base_pos := its length
+
+    def score(self, prompts, topk: int = 0, T: float = 1.0, piece: int = 0):
+        """prefill_packed, and for every prompt of n tokens the target's
+        judgement of it: the log probabilities of its tokens 1 .. n-1 [n-1],
+        and for each of its positions the entropy [n] and the topk most likely
+        next tokens with their log probabilities [n][topk] (the last position
+        speaks of the token behind the prompt)."""
+        S, V = self.S, self.w.vocab
+        lens = [int(p.numel()) for p in prompts]
+        new = lambda n, dt=torch.float32: [torch.zeros(x, n, dtype=dt, device=self.dev) for x in lens]
+        lp, ent, ids, top = new(1), new(1), new(topk, torch.int32), new(topk)
+        step = 256
+        logits = torch.zeros(step, V, dtype=torch.float32, device=self.dev)
+        argmax, count = (torch.zeros(step, dtype=torch.int32, device=self.dev) for _ in range(2))
+
+        def each(done, start):
+            for s in range(S):
+                for r0 in range(start[s], start[s + 1], step):
+                    n, at = min(step, start[s + 1] - r0), done[s] + r0 - start[s]
+                    v = self.verify_args(1, self.ph[r0:], None, logits, update=False)
+                    v.n_seqs, v.argmax, v.margin = n, _ptr(argmax), 0
+                    v.accept_len, v.out_tokens = _ptr(count), _ptr(argmax)
+                    need = D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, v)
+                    if need > self.ws_bytes:
+                        self._new_workspace(int(need))
+                    D.dflash_verify_accept(v, self.ws_ptr, self.ws_bytes)
+                    nxt = prompts[s].view(-1)[at + 1:at + 1 + n].int().to(self.dev)
+                    if nxt.numel() < n:  # (no token is given behind the prompt)
+                        nxt = torch.cat([nxt, torch.full((1,), D.DFLASH_NO_TOKEN, dtype=torch.int32, device=self.dev)])
+                    a = D.dflash_token_logprobs_args()
+                    a.dims = self.tdims
+                    a.n_rows, a.logits, a.temperature, a.topk = n, _ptr(logits), T, topk
+                    a.tokens, a.logprob, a.entropy = _ptr(nxt), _ptr(lp[s][at:]), _ptr(ent[s][at:])
+                    a.top_ids, a.top_logprobs = _ptr(ids[s][at:]), _ptr(top[s][at:])
+                    D.dflash_token_logprobs(a, self.ws_ptr, self.ws_bytes)
+
+        self.prefill_packed(prompts, piece, each)
+        return [(lp[s][:-1, 0], ent[s][:, 0], ids[s], top[s]) for s in range(S)]
 
     def _size_workspace(self, fuse_rows: int):
         need = D.dflash_workspace_bytes(D.DFLASH_OP_DRAFT, self.draft_args())
@@ -517,11 +673,14 @@ class Engine:
         """Inject caller-provided tap features feats [S*rows][F][H]."""
         D.dflash_fuse_context(self.fuse_args(rows, feats, base_pos, valid), self.ws_ptr, self.ws_bytes)
 
-    def prefill(self, prompts: torch.Tensor):
-        """prompts [S][L] int32 on the device.  Runs the target over the
+    def prefill(self, prompts):
+        """prompts [S][L] int32 on the device, or a list of prompts of different
+        lengths (prefill_packed).  Runs the target over the
         prompt (chunks of prefill_chunk rows, then the last token alone),
         injects every prompt position into the draft context, and sets
         anchor = the first greedy token, base_pos = L."""
+        if isinstance(prompts, (list, tuple)):
+            return self.prefill_packed(prompts)
         S, L = prompts.shape
         assert S == self.S and L + self.B <= self.cap
         c0 = 0
@@ -615,7 +774,7 @@ class Engine:
 
     # ---------------------------------------------------------------- loops
 
-    def greedy_generate(self, prompts: torch.Tensor, n_new: int):
+    def greedy_generate(self, prompts, n_new: int):
         self.prefill(prompts)
         out = [self.anchor.clone()]
         while len(out) < n_new:
@@ -623,7 +782,7 @@ class Engine:
             out.append(self.anchor.clone())
         return torch.stack(out, 1).cpu()
 
-    def speculative_generate(self, prompts: torch.Tensor, n_new: int):
+    def speculative_generate(self, prompts, n_new: int):
         self.prefill(prompts)
         outs = [[int(a)] for a in self.anchor.cpu()]
         accepts = []

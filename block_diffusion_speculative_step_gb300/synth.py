@@ -17,6 +17,7 @@ Layouts (row-major, [out][in] for every projection):
   path_u, path_v [R][H]                   path-selector low-rank factors
   draft layer.conv_w1 [4][r][H],          DFlash 2 dynamic depthwise convolution tap
   draft layer.conv_w2 [4][2H][r]          generators (attention in / out, MLP in / out)
+  target layer.q_norm, .k_norm [head_dim] head norms (add_qk_norms)
 """
 from __future__ import annotations
 
@@ -176,6 +177,17 @@ def add_conv_weights(m: dict, w: Workload, rank: int, seed: int = 1, std: float 
     for L in m["draft"]["layers"]:
         L["conv_w1"] = dr.normal((4, rank, H), std, L0.dtype)
         L["conv_w2"] = dr.normal((4, 2 * H, rank), std, L0.dtype)
+
+
+def add_qk_norms(m: dict, w: Workload, seed: int = 2, jitter: float = 0.1) -> None:
+    """Draw query and key head norms (q_norm, k_norm [head_dim], 1 + N(0,
+    jitter)) into every target layer of an existing model dict, from a
+    generator of their own on the model's device."""
+    L0 = m["target"]["layers"][0]["w_o"]
+    dr = _Draw(seed, L0.device)
+    for L in m["target"]["layers"]:
+        L["q_norm"] = dr.gain(w.target.head_dim, jitter, L0.dtype)
+        L["k_norm"] = dr.gain(w.target.head_dim, jitter, L0.dtype)
 
 
 def make_tokens(seed: int, n: int, vocab: int, device="cpu") -> torch.Tensor:

@@ -73,7 +73,8 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 } dflash_dtype;
 typedef enum {
   DFLASH_ATTN_CAUSAL = 0,     /* target verification: row i sees cache slots 0..pos_i */
   DFLASH_ATTN_BLOCK_BIDIR = 1, /* draft block: every row sees the context and the whole block */
-  DFLASH_ATTN_TREE = 2        /* target verification of a tree: a row sees the context, its ancestors and itself */
+  DFLASH_ATTN_TREE = 2,       /* target verification of a tree: a row sees the context, its ancestors and itself */
+  DFLASH_ATTN_PROMPT = 3      /* packed prompts: a row sees its sequence's context and rows up to itself */
 } dflash_attn_mode;
 
 typedef enum {
@@ -208,6 +209,19 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *   outside [0, max_pos - rows] or a node's position outside the table raises
  *   DFLASH_ERR_INVALID_ARG in the status word.  A padding row's attention output
  *   is 0: its residual stays finite and means nothing.
+ * DFLASH_ATTN_PROMPT: the rows are n_seqs prompts of different lengths, packed
+ *   (prompt_start, see dflash_prompt_attention); `rows` is their number in all,
+ *   M.  tree_pos[M] holds the rows' positions.  base_pos[s] is what kv holds of
+ *   sequence s (max_pos bounds it), or NULL: nothing, and kv is not read.  kv
+ *   is not written: the rows' rotated keys and values go to out_kb / out_vb,
+ *   here [M][n_kv][d], from which dflash_kv_write commits them.  A position
+ *   outside the RoPE table raises DFLASH_ERR_INVALID_ARG in the status word.
+ *   The attention output of a row of no sequence is 0: its residual stays
+ *   finite and means nothing.
+ * q_norm, k_norm (optional, [head_dim] gains of dims.dtype): every query and
+ *   key head is normalised before its rotation, from the projection's fp32
+ *   sums (dflash_qk_norm_rope); not with DFLASH_ATTN_BLOCK_BIDIR.  They need
+ *   more workspace: set them before dflash_workspace_bytes is asked.
  * tap (optional): writes the layer's output residual, rounded to dims.dtype,
  *   to tap[row * tap_stride + tap_offset + j] (feature taps for fusion).
  * max_pos: host-side bound with base_pos[s] + rows <= max_pos for every s
@@ -221,7 +235,8 @@ int dflash_embed(const dflash_embed_args* a, void* ws, size_t ws_bytes, dflash_s
  *     q      [M][n_q*d]    rotated queries
  *     kb, vb [n_seqs][n_kv][rows][d]  the block's rotated keys and values
  *                          (DFLASH_ATTN_BLOCK_BIDIR; [M][n_kv][d] with
- *                          DFLASH_ATTN_TREE; causal layers write them into kv)
+ *                          DFLASH_ATTN_TREE and DFLASH_ATTN_PROMPT; causal
+ *                          layers write them into kv)
  *     attn   [M][n_q*d]    attention output, the O projection's input
  *     x_mlp  [M][H]        RMSNorm(h; ln2) after the attention residual
  *     act    [M][I]        SiLU(gate) * up, the down projection's input
@@ -247,7 +262,10 @@ typedef struct {
   void* out_x_mlp;
   void* out_act;
   const int32_t* tree_parent; /* DFLASH_ATTN_TREE: [n_seqs][rows], or NULL for a chain */
-  const int32_t* tree_pos;    /* DFLASH_ATTN_TREE: [M] absolute positions of the rows */
+  const int32_t* tree_pos;    /* DFLASH_ATTN_TREE, DFLASH_ATTN_PROMPT: [M] absolute positions of the rows */
+  const int32_t* prompt_start;/* DFLASH_ATTN_PROMPT: [n_seqs + 1] */
+  const void* q_norm;         /* optional [head_dim] gains */
+  const void* k_norm;
 } dflash_layer_args;
 int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws_bytes,
                                  dflash_stream_t stream);
