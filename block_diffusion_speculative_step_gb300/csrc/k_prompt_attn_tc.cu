@@ -19,7 +19,12 @@
 //   P = 2^(c S - m)  one thread per query vector, written over S
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
 // The streams' softmaxes take turns, so that one stream's products run beside
-// the other's softmax.  The reference m stays while the weights' sum suits
+// the other's softmax.  A turn is what bounds the kernel: one warp per
+// scheduler, about 900 instructions in a row (8k tokens, 32 / 8 heads: 520 us;
+// 444 without any softmax arithmetic, which the tensor core's rate gives; scores
+// in steps of 16 columns instead of 32: 560).  Scores of 64 keys ahead, two
+// buffers a stream and no turns: 584, for a product 64 columns wide takes
+// almost as long as one of 128.  The reference m stays while the weights' sum suits
 // bf16 (which has fp32's exponents): it starts at 0 and takes sums of 2^-30 ..
 // 2^30, so the usual chunk needs no maximum and no rescaling of O.  Otherwise
 // the half chunk is done again with its maximum.
@@ -584,11 +589,11 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         __syncwarp();
         tc::tc_fence_after();
         if (warp_on) {
-          constexpr int W = 16, HC = 64;  // columns per step, per part
+          constexpr int W = 32, HC = 64;  // columns per step, per part
           auto hide = [&](float (&x)[W], int i) {  // columns W i ..
             if (masked) {
               const int n = see - W * i;
-              const uint32_t w = n >= W ? 0xffffu : n > 0 ? (1u << n) - 1u : 0u;
+              const uint32_t w = n >= W ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
 #pragma unroll
               for (int k = 0; k < W; ++k) x[k] = (w >> k) & 1u ? x[k] : -INFINITY;
             }
@@ -610,8 +615,8 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
             return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           };
           unsigned long long sa, sb;
-          // weights 2^(scale x + m0) of a step, as the product takes them (W / 2
-          // columns of their first parts, then what those left), and their sums;
+          // weights 2^(scale x + m0) of a step, as the product takes them (of 16
+          // keys 8 columns of first parts, then what those left), and their sums;
           // `next` starts the next step's loads once the scores have been taken
           auto piece = [&](float (&x)[W], uint32_t* pk, float m0, auto next) {
             const unsigned long long m2 = tt_pair(m0, m0);
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
               hi = tt_ex2(hi);
               if (k & 1) sb = tt_add2(sb, tt_pair(lo, hi));
               else sa = tt_add2(sa, tt_pair(lo, hi));
-              tt_split_bf16(lo, hi, pk[k], pk[W / 2 + k]);
+              tt_split_bf16(lo, hi, pk[(k & ~7) * 2 + (k & 7)], pk[(k & ~7) * 2 + (k & 7) + 8]);
             }
           };
           // the weights of the chunk's first n keys
