@@ -374,6 +374,7 @@ int run_layer(const LayerShape& L, const dflash_layer_weights& w, const dflash_k
     t.pos = L.tree_pos;
     t.pos_end = rope_max_pos;
     t.zero_pad = 1;  // (as for a tree)
+    t.counters = c.counters + kCtrAttn;
     t.q = s.q;
     t.kb = s.kb;
     t.vb = s.vb;

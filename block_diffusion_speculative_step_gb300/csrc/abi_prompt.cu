@@ -186,6 +186,7 @@ int dflash_prompt_attention(const dflash_prompt_attention_args* a, void* ws, siz
   p.vb = a->vb;
   p.out = a->out;
   p.work = static_cast<char*>(ws) + kReservedBytes;
+  p.counters = header(ws).counters + kCtrAttn;
   p.status = header(ws).status;
   DF_LAUNCH((cudaStream_t)stream, TF_ATTN, 0, launch_prompt_attention(p, sms, (cudaStream_t)stream));
   return DFLASH_OK;

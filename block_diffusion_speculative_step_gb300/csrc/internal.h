@@ -288,6 +288,7 @@ struct PromptAttnDesc {
   float scale;                // times log2 e: scores in log2 units
   void* out;                  // [M][nq*d]
   void* work;                 // partials
+  uint32_t* counters;         // arrivals of an item's partials, one per CTA (0 between launches)
   uint32_t* status;
 };
 size_t prompt_attn_workspace(const PromptAttnDesc& a, int num_sms);

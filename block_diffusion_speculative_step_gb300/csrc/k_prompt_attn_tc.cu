@@ -10,7 +10,8 @@
 // the causal triangle, ragged lengths and few long contexts balance alike.  A
 // CTA walks its run as segments (the part of one item inside the run): a whole
 // item is normalised and written at once, the first and the last segment may
-// leave a partial (O, m, l) that the merge kernel joins in order.
+// leave a partial (O, m, l); the CTA that leaves an item's last one joins them,
+// in their order.
 //
 // Two streams per CTA, one per query tile, each an online softmax with its own
 // score and output accumulators in tensor memory (S 128 + O D columns).  Per
@@ -58,6 +59,10 @@ namespace {
 constexpr int kPtCH = 128;    // keys per chunk
 constexpr int kPtRows = 128;  // query vectors per tile
 constexpr int kPtRing = 8;    // chunks whose bad rows are kept
+// Positions of a run at least: shorter ones share an item of few chunks among
+// many CTAs (seven prompts of up to 33 rows over 131 slots: 12.0 us with 1, 10.1
+// with 4, 14.4 with 6).
+constexpr int kPtLeast = 4;
 constexpr int kPtSetup = 2;   // positions an item has before its chunks', for what it costs besides them
 
 struct PtTma {
@@ -85,16 +90,6 @@ struct PtCfg {
   static constexpr int X_BYTES = 2048;
   static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
-};
-
-struct PtShared {  // after the tiles
-  uint32_t badv[kPtRing][4];  // own rows whose V holds a NaN or infinity, by chunk counter
-  int s0, g0, t0, c0, len;    // the CTA's run: first item, position in it, number of positions
-  int good;                   // row_start is in order
-  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];
-  uint64_t sfull[2], pdone[2], ofull[2], qfull[2], qfree[2];
-  uint32_t tslot;
-  int abort;
 };
 
 // sum of floor((a i + b) / m) over i < n (Euclid's steps: few for m = 128).
@@ -141,21 +136,38 @@ struct PtSeq {
   }
 };
 
-__device__ __forceinline__ PtSeq pt_seq(const PromptAttnDesc& a, int tt, int s) {
+struct PtShared {  // after the tiles
+  uint32_t badv[kPtRing][4];  // own rows whose V holds a NaN or infinity, by chunk counter
+  int s0, g0, t0, c0, len;    // the CTA's run: first item, position in it, number of positions
+  PtSeq q;                    // the first item's sequence
+  int x0, per;                // its first position, positions of a run
+  int last;                   // this CTA's partial was its item's last one
+  int good;                   // row_start is in order
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];
+  uint64_t sfull[2], pdone[2], ofull[2], qfull[2], qfree[2];
+  uint32_t tslot;
+  int abort;
+};
+
+__device__ __forceinline__ PtSeq pt_seq(const PromptAttnDesc& a, int tt, int s, bool* far) {
+  const int c = a.base_pos ? __ldg(a.base_pos + s) : 0;
   PtSeq q;
-  q.set(a, tt, __ldg(a.row_start + s), __ldg(a.row_start + s + 1), a.base_pos ? __ldg(a.base_pos + s) : 0);
+  q.set(a, tt, __ldg(a.row_start + s), __ldg(a.row_start + s + 1), c);
+  *far |= q.ctx != c;
   return q;
 }
 
 // All positions (one warp); none where row_start leaves [0, M] or decreases.
-// status (or null): told of that, and of contexts out of range.
-__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status, bool* good) {
+// status (or null): told of that, and of contexts out of range.  mine: the
+// sequence of this lane, of the first 32.
+__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status, bool* good, PtSeq* mine) {
   int t = 0;
   bool bad = false, far = false;
+  mine->set(a, tt, 0, 0, 0);
   for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
-    const PtSeq q = pt_seq(a, tt, s);
+    const PtSeq q = pt_seq(a, tt, s, &far);
+    if (s < 32) *mine = q;
     bad |= q.row0 < 0 || q.row0 > a.M || q.n < 0 || q.n > a.M - q.row0;
-    far |= a.base_pos && __ldg(a.base_pos + s) != q.ctx;
     if (!bad) t += q.before(tt, q.T) * a.nkv;
   }
   if ((bad || far) && status) raise_status(status, ST_RANGE);
@@ -163,12 +175,13 @@ __device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_
   return *good ? __reduce_add_sync(0xffffffffu, t) : 0;
 }
 
-// The item at position x of the flat order, and the position c in it (one warp).
+// The item at position x of the flat order, and the position c in it (one
+// warp; x below pt_total's result, mine from there).
 struct PtSpot {
   int s, g, t, c;
   PtSeq q;
 };
-__device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int x) {
+__device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int x, const PtSeq& mine) {
   const int lane = threadIdx.x & 31;
   PtSpot p;
   p.s = a.n_seqs;
@@ -176,12 +189,13 @@ __device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int
   p.q.set(a, tt, 0, 0, 0);
   int first = 0;
   for (int b = 0; b < a.n_seqs; b += 32) {
-    const int s = b + lane;
-    int len = 0;
-    if (s < a.n_seqs) {
-      const PtSeq q = pt_seq(a, tt, s);
-      len = q.before(tt, q.T) * a.nkv;
+    PtSeq q = mine;
+    if (b > 0) {
+      bool far = false;
+      q.set(a, tt, 0, 0, 0);
+      if (b + lane < a.n_seqs) q = pt_seq(a, tt, b + lane, &far);
     }
+    const int len = q.before(tt, q.T) * a.nkv;
     int inc = len;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,8 +210,12 @@ __device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int
     const int w = __ffs(hit) - 1;
     x -= first + __shfl_sync(0xffffffffu, inc - len, w);
     p.s = b + w;
-    p.q = pt_seq(a, tt, p.s);
-    const int one = p.q.before(tt, p.q.T);  // positions of a KV head
+    p.q.row0 = __shfl_sync(0xffffffffu, q.row0, w);
+    p.q.n = __shfl_sync(0xffffffffu, q.n, w);
+    p.q.ctx = __shfl_sync(0xffffffffu, q.ctx, w);
+    p.q.cc = __shfl_sync(0xffffffffu, q.cc, w);
+    p.q.T = __shfl_sync(0xffffffffu, q.T, w);
+    const int one = __shfl_sync(0xffffffffu, len, w) / a.nkv;  // positions of a KV head
     p.g = x / one;
     x %= one;
     int lo = 0, hi = p.q.T;  // the item lies in [lo, hi): 32 places at a time
@@ -249,7 +267,11 @@ struct PtSeg {
     s = same(sh->s0);
     g = same(sh->g0);
     t = same(sh->t0);
-    load();
+    q.row0 = same(sh->q.row0);
+    q.n = same(sh->q.n);
+    q.ctx = same(sh->q.ctx);
+    q.cc = same(sh->q.cc);
+    q.T = same(sh->q.T);
     item();
     take(same(sh->c0));
     return c1 > c0 || next();
@@ -288,6 +310,79 @@ struct PtSeg {
 template <int D>
 __host__ __device__ constexpr size_t pt_slot_floats() {
   return (size_t)2 * kPtRows * (D + 2);
+}
+
+// Joins the partials that CTAs b0 .. b1 left of an item, in their order, by
+// eight warps: a warp takes 32 rows and CW columns at a time, lanes are rows,
+// so its reads are 512 contiguous bytes; the loads of U partials are in flight
+// at once.
+template <int D>
+__device__ __forceinline__ void pt_join(const PtTma& p, const PtSeq& q, int g, int t, int b0, int b1, int warp) {
+  constexpr int CW = 16, U = 4, CG = D / CW;
+  const PromptAttnDesc& a = p.a;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int w = warp; w < 8 * CG; w += 8) {
+    const int rg = w / CG, cg = w % CG, tile = rg >> 2, r = (rg & 3) * 32 + lane;
+    const int rt = pt_div_grp(p, r), token = t * 2 * p.tok + tile * p.tok + rt;
+    const bool has_row = rt < p.tok && token < q.n;
+    if (!__any_sync(0xffffffffu, has_row)) continue;
+    if (!has_row) continue;
+    const int mrow = 2 * kPtRows * D + tile * kPtRows + r;
+    const size_t orow = (size_t)tile * (kPtRows * D) + ((size_t)(cg * (CW / 4)) * kPtRows + r) * 4;
+    float M = -INFINITY, L = 0.f, o[CW];
+#pragma unroll
+    for (int k = 0; k < CW; ++k) o[k] = 0.f;
+#pragma unroll 1
+    for (int b = b0; b <= b1; b += U) {
+      float4 v[U][CW / 4];
+      float mb[U], lb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        mb[u] = -INFINITY;
+        lb[u] = 0.f;
+#pragma unroll
+        for (int k = 0; k < CW / 4; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b + u > b1) continue;
+        // slot 0: the item began in an earlier CTA
+        const float* sl =
+            static_cast<const float*>(a.work) + ((size_t)2 * (b + u) + (b + u > b0 ? 0 : 1)) * pt_slot_floats<D>();
+#pragma unroll
+        for (int k = 0; k < CW / 4; ++k)
+          v[u][k] = __ldcg(reinterpret_cast<const float4*>(sl + orow + (size_t)4 * k * kPtRows));
+        mb[u] = __ldcg(sl + mrow);
+        lb[u] = __ldcg(sl + mrow + 2 * kPtRows);
+      }
+      float Mn = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, mb[u]);
+      const float y = M == -INFINITY ? 0.f : tt_ex2(M - Mn);
+      M = Mn;
+      L *= y;
+#pragma unroll
+      for (int k = 0; k < CW; ++k) o[k] *= y;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float e = mb[u] == -INFINITY ? 0.f : tt_ex2(mb[u] - M);
+        L = fmaf(lb[u], e, L);
+#pragma unroll
+        for (int k = 0; k < CW / 4; ++k) {
+          o[4 * k] = fmaf(v[u][k].x, e, o[4 * k]);
+          o[4 * k + 1] = fmaf(v[u][k].y, e, o[4 * k + 1]);
+          o[4 * k + 2] = fmaf(v[u][k].z, e, o[4 * k + 2]);
+          o[4 * k + 3] = fmaf(v[u][k].w, e, o[4 * k + 3]);
+        }
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                          ((size_t)(q.row0 + token) * a.nq + g * p.grp + r - rt * p.grp) * D + cg * CW);
+#pragma unroll
+    for (int k = 0; k < CW / 8; ++k)
+      out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                          tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                          tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+  }
 }
 
 template <int D>
@@ -336,18 +431,23 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
   pdl_launch_dependents();
   if (warp == 0) {
     bool good;
-    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good);
-    const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    PtSeq mine;
+    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good, &mine);
+    const int per = max(kPtLeast, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     const int x0 = (int)min((long long)blockIdx.x * per, (long long)total), len = min(per, total - x0);
     PtSpot sp;
     sp.s = sp.g = sp.t = sp.c = 0;
-    if (len > 0) sp = pt_locate(a, tt, x0);
+    sp.q = mine;
+    if (len > 0) sp = pt_locate(a, tt, x0, mine);
     if (lane == 0) {
       sh->s0 = sp.s;
       sh->g0 = sp.g;
       sh->t0 = sp.t;
       sh->c0 = sp.c;
       sh->len = sp.s < a.n_seqs ? len : 0;
+      sh->q = sp.q;
+      sh->x0 = x0;
+      sh->per = per;
       sh->good = good;
     }
   }
@@ -799,6 +899,22 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
           ml[2 * kPtRows + prow] = l_run;
         }
       }
+      if (sg.c0 > 0 || sg.c1 < sg.nch) {  // the item is shared: who leaves its last partial joins them
+        const int first = sg.c0 > 0 ? sh->x0 - sh->c0 : sh->x0 + sh->len - sg.c1 - kPtSetup;  // the item's first position
+        const int b0 = (first + kPtSetup) / sh->per, b1 = (first + kPtSetup + sg.nch - 1) / sh->per;
+        __threadfence();
+        tc::named_bar(1, 256);
+        if (tid == 128) {
+          uint32_t* ctr = a.counters + b0;
+          const uint32_t before = atomicAdd(ctr, 1u);
+          sh->last = before == (uint32_t)(b1 - b0);
+          if (sh->last) *ctr = 0u;  // (ready for the next launch)
+          __threadfence();
+        }
+        tc::named_bar(1, 256);
+        if (sh->last) pt_join<D>(p, sg.q, sg.g, sg.t, b0, b1, warp - 4);
+        tc::named_bar(1, 256);  // (sh->last has been read)
+      }
     }
     if (t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
   }
@@ -808,96 +924,6 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
-}
-
-// Joins the partials of the items that several CTAs shared.  Grid: y = the
-// item's first boundary between runs, so that only shared items' warps do
-// anything; x = (32 rows, CW columns) of the item, one warp each: lanes are
-// rows, so the partials' reads are 512 contiguous bytes; the loads of U
-// partials are in flight at once.
-template <int D, int CW, int U>
-__global__ void __launch_bounds__(128) prompt_tc_merge_kernel(const __grid_constant__ PromptAttnDesc a, int tok, int nb) {
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, grp = a.nq / a.nkv, tt = 2 * tok;
-  constexpr int CG = D / CW;
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int cg = w % CG, rg = w / CG;
-  // Which item, if any: found beside the attention kernel's last CTAs, for the
-  // lengths it goes by were there before that kernel's own wait ended.
-  PtSpot sp;
-  sp.s = a.n_seqs;
-  int b0 = 0, b1 = 0;
-  bool good;
-  const int total = pt_total(a, tt, nullptr, &good), per = (total + nb - 1) / nb;
-  const long long x = (long long)(blockIdx.y + 1) * per;
-  if (x < total) {
-    sp = pt_locate(a, tt, (int)x);
-    const int X = (int)x - sp.c + kPtSetup;  // the item's chunks are [X, X + nch)
-    if (x > X && X / per == (int)blockIdx.y) {  // an item is cut here, for the first time
-      b0 = blockIdx.y;
-      b1 = (X + sp.q.chunks(tt, sp.t) - 1) / per;
-    }
-  }
-  pdl_wait();  // (every CTA: who waits for this kernel waits for the attention too)
-  if (b0 == b1) return;  // none, or written by its CTA
-  const int tile = rg >> 2, prow = (rg & 3) * 32 + lane;
-  const int rt = prow / grp, token = sp.t * tt + tile * tok + rt;
-  const bool has_row = rt < tok && token < sp.q.n;
-  if (!__any_sync(0xffffffffu, has_row)) return;
-  const int mrow = 2 * kPtRows * D + tile * kPtRows + prow;
-  const size_t orow = (size_t)tile * (kPtRows * D) + ((size_t)(cg * (CW / 4)) * kPtRows + prow) * 4;
-  float M = -INFINITY, L = 0.f, o[CW];
-#pragma unroll
-  for (int k = 0; k < CW; ++k) o[k] = 0.f;
-  if (!has_row) return;
-#pragma unroll 1
-  for (int b = b0; b <= b1; b += U) {
-    float4 v[U][CW / 4];
-    float mb[U], lb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int bb = b + u;
-      mb[u] = -INFINITY;
-      lb[u] = 0.f;
-#pragma unroll
-      for (int k = 0; k < CW / 4; ++k) v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (bb > b1) continue;
-      // slot 0: the item began in an earlier CTA
-      const float* sl = static_cast<const float*>(a.work) + ((size_t)2 * bb + (bb > b0 ? 0 : 1)) * pt_slot_floats<D>();
-#pragma unroll
-      for (int k = 0; k < CW / 4; ++k) v[u][k] = *reinterpret_cast<const float4*>(sl + orow + (size_t)4 * k * kPtRows);
-      mb[u] = sl[mrow];
-      lb[u] = sl[mrow + 2 * kPtRows];
-    }
-    float Mn = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, mb[u]);
-    const float y = M == -INFINITY ? 0.f : tt_ex2(M - Mn);
-    M = Mn;
-    L *= y;
-#pragma unroll
-    for (int k = 0; k < CW; ++k) o[k] *= y;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float e = mb[u] == -INFINITY ? 0.f : tt_ex2(mb[u] - M);
-      L = fmaf(lb[u], e, L);
-#pragma unroll
-      for (int k = 0; k < CW / 4; ++k) {
-        o[4 * k] = fmaf(v[u][k].x, e, o[4 * k]);
-        o[4 * k + 1] = fmaf(v[u][k].y, e, o[4 * k + 1]);
-        o[4 * k + 2] = fmaf(v[u][k].z, e, o[4 * k + 2]);
-        o[4 * k + 3] = fmaf(v[u][k].w, e, o[4 * k + 3]);
-      }
-    }
-  }
-  const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)(sp.q.row0 + token) * a.nq +
-                                                                              sp.g * grp + prow - rt * grp) * D + cg * CW);
-#pragma unroll
-  for (int k = 0; k < CW / 8; ++k)
-    out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                        tt_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                        tt_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
 }
 
 template <int D>
@@ -920,10 +946,7 @@ cudaError_t pt_launch(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
   if (!okm) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prompt_tc_kernel<D>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
-  if (e != cudaSuccess) return e;
-  constexpr int CW = 32, U = 2, WARPS = 8 * (D / CW);
-  return launch_pdl(prompt_tc_merge_kernel<D, CW, U>, dim3(WARPS / 4, num_sms), dim3(128), 0, st, a, p.tok, num_sms);
+  return launch_pdl(prompt_tc_kernel<D>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
 }
 
 }  // namespace
