@@ -1,13 +1,13 @@
 // k_prompt_attn.cu -- causal attention of packed prompts in fp32, and the choice
 // between it and the tensor-core kernel (k_prompt_attn_tc.cu, bf16).
 //
-// A CTA has a tile of 64 query vectors of one (sequence, KV head), the group's
+// A CTA has a tile of 64 (or 16) query vectors of one (sequence, KV head), the group's
 // query heads side by side (vector = token * group + head), and walks the keys
 // that the tile sees in chunks of 64: cached slots, then the sequence's own
 // rows up to the tile's last token.  Scores and outputs are register tiles
-// (4 x 4 and 4 x d/16 per thread), the softmax runs along with a running
-// maximum and sum.  Full precision has no tensor-core form, so the fp32 units
-// bound it.  Where few tiles would leave SMs idle, the chunks of a tile are cut
+// (4 x 4 and 4 x d/16 per thread, 64 multiply-adds for eight 16-byte reads of
+// shared memory), the softmax runs along with a running maximum and sum.  Full
+// precision has no tensor-core form, so the fp32 units bound it.  Where few tiles would leave SMs idle, the chunks of a tile are cut
 // into `split` parts of equal number that a second kernel joins.
 #include <math.h>
 
@@ -22,34 +22,40 @@ namespace dfl {
 
 namespace {
 
-constexpr int kPsQ = 64;        // query vectors of a tile
 constexpr int kPsK = 64;        // keys of a chunk
 constexpr int kPsThreads = 256;
 
-template <int D>
+// R: query vectors per thread; a tile holds 16 R.
+template <int D, int R>
 struct PsCfg {
-  static constexpr int QP = kPsQ + 4;  // pitches, in floats (transposed tiles: rows of 64 vectors)
-  static constexpr int VP = D + 4;
-  static constexpr int Q_OFF = 0;                // [D][QP]
-  static constexpr int K_OFF = Q_OFF + D * QP;   // [D][QP]
-  static constexpr int V_OFF = K_OFF + D * QP;   // [64][VP]
-  static constexpr int P_OFF = V_OFF + kPsK * VP;  // [64 keys][QP]
-  static constexpr int FLOATS = P_OFF + kPsK * QP;
+  static constexpr int Q = 16 * R;
+  static constexpr int RP = D + 4;  // pitches, in floats: 16-byte reads of eight rows meet all banks
+  static constexpr int PP = kPsK + 4;
+  static constexpr int Q_OFF = 0;                  // [Q][RP]
+  static constexpr int K_OFF = Q_OFF + Q * RP;      // [64][RP]
+  static constexpr int V_OFF = K_OFF + kPsK * RP;  // [64][RP]
+  static constexpr int P_OFF = V_OFF + kPsK * RP;  // [Q][PP]
+  static constexpr int FLOATS = P_OFF + Q * PP;
   static constexpr size_t SMEM = FLOATS * sizeof(float);
 };
 
-// Query tiles of a sequence of n rows, and the launch's bound on their number.
-__host__ __device__ __forceinline__ int ps_tiles(int n, int grp) {
-  return (int)(((long long)n * grp + kPsQ - 1) / kPsQ);
+// Query tiles (of `size` vectors) of a sequence of n rows, and the launch's
+// bound on their number.
+__host__ __device__ __forceinline__ int ps_tiles(int n, int grp, int size) {
+  return (int)(((long long)n * grp + size - 1) / size);
 }
-long long ps_max_tiles(const PromptAttnDesc& a) {
-  return (long long)a.M * (a.nq / a.nkv) / kPsQ + std::min(a.n_seqs, a.M);
+long long ps_max_tiles(const PromptAttnDesc& a, int size) {
+  return (long long)a.M * (a.nq / a.nkv) / size + std::min(a.n_seqs, a.M);
 }
+
+// Tiles of 64 vectors, or of 16 where those leave SMs idle (three prompts of 64
+// rows, 4 heads: 6.4 us, 10.4 with 64).
+int ps_rows(const PromptAttnDesc& a, int num_sms) { return ps_max_tiles(a, 64) * a.nkv < num_sms ? 1 : 4; }
 
 // Parts of a tile's chunks: enough tiles x parts for two CTAs an SM, each part
 // at least 4 chunks of the longest tile.
 int ps_split(const PromptAttnDesc& a, int num_sms) {
-  const long long ctas = ps_max_tiles(a) * a.nkv, chunks = a.max_pos / kPsK + a.M / kPsK + 2;
+  const long long ctas = ps_max_tiles(a, 16 * ps_rows(a, num_sms)) * a.nkv, chunks = a.max_pos / kPsK + a.M / kPsK + 2;
   return (int)std::max(1ll, std::min(std::min(2ll * num_sms / std::max(ctas, 1ll), chunks / 4), 64ll));
 }
 
@@ -67,10 +73,10 @@ __device__ __forceinline__ PsSeq ps_seq(const PromptAttnDesc& a, int s, bool* ba
   return q;
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_constant__ PromptAttnDesc a, int split) {
-  using C = PsCfg<D>;
-  constexpr int QP = C::QP, VP = C::VP, OC = D / 16;
+  using C = PsCfg<D, R>;
+  constexpr int RP = C::RP, PP = C::PP, OV = D / 64;  // OV: float4s of an output row per thread
   extern __shared__ __align__(16) float ps_smem[];
   float *Qs = ps_smem + C::Q_OFF, *Ks = ps_smem + C::K_OFF, *Vs = ps_smem + C::V_OFF, *Ps = ps_smem + C::P_OFF;
   __shared__ int sh_s, sh_tile, sh_good;
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
       int k = 0;
       if (b + tid < a.n_seqs) {
         const PsSeq q = ps_seq(a, b + tid, &bad, &far);
-        k = bad ? 0 : ps_tiles(q.n, grp);
+        k = bad ? 0 : ps_tiles(q.n, grp, C::Q);
       }
       int inc = k;
 #pragma unroll
@@ -118,34 +124,33 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
   if (s < 0) return;
   bool bad = false, far = false;
   const PsSeq sq = ps_seq(a, s, &bad, &far);
-  const int qv0 = sh_tile * kPsQ, nqv = min(kPsQ, sq.n * grp - qv0);
+  const int qv0 = sh_tile * C::Q, nqv = min(C::Q, sq.n * grp - qv0);
   const int last = (qv0 + nqv - 1) / grp;                        // the tile's last token
   const int cctx = (sq.ctx + kPsK - 1) / kPsK, nch = cctx + last / kPsK + 1;
   const int z = blockIdx.z, c_lo = (int)((long long)nch * z / split), c_hi = (int)((long long)nch * (z + 1) / split);
   const float* q = static_cast<const float*>(a.q);
   const size_t QD = (size_t)a.nq * D, KD = (size_t)a.nkv * D;
 
-  for (int i = tid; i < kPsQ * (D / 4); i += kPsThreads) {
+  for (int i = tid; i < C::Q * (D / 4); i += kPsThreads) {
     const int r = i / (D / 4), e = i % (D / 4) * 4, qv = qv0 + r;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nqv)
       x = __ldg(reinterpret_cast<const float4*>(q + (sq.row0 + qv / grp) * QD + (size_t)(g * grp + qv % grp) * D + e));
-    Qs[e * QP + r] = x.x;
-    Qs[(e + 1) * QP + r] = x.y;
-    Qs[(e + 2) * QP + r] = x.z;
-    Qs[(e + 3) * QP + r] = x.w;
+    *reinterpret_cast<float4*>(Qs + r * RP + e) = x;
   }
-  const int ty = tid >> 4, tx = tid & 15;  // rows 4 ty .., score columns 4 tx .., output columns tx OC ..
-  int tok[4];
+  // a thread's rows are ty + 16 i, its score columns tx + 16 k, its output columns 64 v + 4 tx ..
+  const int ty = tid >> 4, tx = tid & 15;
+  int tok[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tok[i] = (qv0 + 4 * ty + i) / grp;
-  float m[4], l[4], o[4][OC];
+  for (int i = 0; i < R; ++i) tok[i] = (qv0 + ty + 16 * i) / grp;
+  float m[R], l[R];
+  float4 o[R][OV];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < OC; ++k) o[i][k] = 0.f;
+    for (int v = 0; v < OV; ++v) o[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const KvMap km{a.pages, a.cap, a.ps, a.max_pages, a.pool, a.nkv};
 
@@ -169,6 +174,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
       pitch = KD;
     }
     __syncthreads();  // the chunk before has been used
+    bool odd = false;  // a value is NaN or infinite
     for (int i = tid; i < kPsK * (D / 4); i += kPsThreads) {
       const int r = i / (D / 4), e = i % (D / 4) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -176,35 +182,39 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
         x = __ldg(reinterpret_cast<const float4*>(kp + r * pitch + e));
         y = __ldg(reinterpret_cast<const float4*>(vp + r * pitch + e));
       }
-      Ks[e * QP + r] = x.x;
-      Ks[(e + 1) * QP + r] = x.y;
-      Ks[(e + 2) * QP + r] = x.z;
-      Ks[(e + 3) * QP + r] = x.w;
-      *reinterpret_cast<float4*>(Vs + r * VP + e) = y;
+      *reinterpret_cast<float4*>(Ks + r * RP + e) = x;
+      *reinterpret_cast<float4*>(Vs + r * RP + e) = y;
+      odd |= !(fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY);
     }
-    __syncthreads();
-    float sc[4][4] = {};
-#pragma unroll 8
-    for (int e = 0; e < D; ++e) {
-      const float4 x = *reinterpret_cast<const float4*>(Qs + e * QP + 4 * ty);
-      const float4 y = *reinterpret_cast<const float4*>(Ks + e * QP + 4 * tx);
-      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    odd = __syncthreads_or(odd) != 0;
+    float sc[R][4] = {};
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+      float4 x[R], y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * RP + e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sc[i][k] = fmaf(xs[i], ys[k], sc[i][k]);
+      for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * k) * RP + e);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sc[i][k] = fmaf(x[i].x, y[k].x, sc[i][k]);
+          sc[i][k] = fmaf(x[i].y, y[k].y, sc[i][k]);
+          sc[i][k] = fmaf(x[i].z, y[k].z, sc[i][k]);
+          sc[i][k] = fmaf(x[i].w, y[k].w, sc[i][k]);
+        }
     }
     // keys of the chunk that row i sees
-    int see[4];
+    int see[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) see[i] = ctx ? nk : min(nk, tok[i] + 1 - j0);
-    float p[4][4];
+    for (int i = 0; i < R; ++i) see[i] = ctx ? nk : min(nk, tok[i] + 1 - j0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        sc[i][k] = 4 * tx + k < see[i] ? sc[i][k] * a.scale : -INFINITY;
+        sc[i][k] = tx + 16 * k < see[i] ? sc[i][k] * a.scale : -INFINITY;
         mx = fmaxf(mx, sc[i][k]);
       }
 #pragma unroll
@@ -215,64 +225,76 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        p[i][k] = exp2f(sc[i][k] - ref);
-        sum += p[i][k];
+        const float p = exp2f(sc[i][k] - ref);
+        Ps[(ty + 16 * i) * PP + tx + 16 * k] = p;
+        sum += p;
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       l[i] = l[i] * alpha + sum;
 #pragma unroll
-      for (int k = 0; k < OC; ++k) o[i][k] *= alpha;
+      for (int v = 0; v < OV; ++v)
+        o[i][v] = make_float4(o[i][v].x * alpha, o[i][v].y * alpha, o[i][v].z * alpha, o[i][v].w * alpha);
     }
+    __syncwarp();  // (a row's weights come from the half warp that uses them)
+    // All keys, four at a time: what is hidden has weight 0 (behind the last key
+    // values are 0 too).  But 0 times a NaN or infinite value is NaN: where
+    // there are such, keys that every row of this thread sees, then the rest
+    // one row at a time.
+    int all = (nk + 3) & ~3;
+    if (odd) {
+      all = nk;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<float4*>(Ps + (4 * tx + k) * QP + 4 * ty) = make_float4(p[0][k], p[1][k], p[2][k], p[3][k]);
-    __syncthreads();
-    // keys that every row of this thread sees, then the rest one row at a time:
-    // a hidden value may be NaN or infinite, and 0 times it is NaN
-    const int all = max(0, min(min(see[0], see[1]), min(see[2], see[3])));
-    auto product = [&](int j, bool some) {
-      const float4 w = *reinterpret_cast<const float4*>(Ps + j * QP + 4 * ty);
-      const float ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < OC; k += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(Vs + j * VP + tx * OC + k);
-        const float vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!some || j < see[i])
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][k + e] = fmaf(ws[i], vs[e], o[i][k + e]);
-      }
+      for (int i = 0; i < R; ++i) all = min(all, see[i]);
+      all = max(all, 0) & ~3;
+    }
+    auto axpy = [](float w, const float4& v, float4& y) {
+      y.x = fmaf(w, v.x, y.x);
+      y.y = fmaf(w, v.y, y.y);
+      y.z = fmaf(w, v.z, y.z);
+      y.w = fmaf(w, v.w, y.w);
     };
-#pragma unroll 4
-    for (int j = 0; j < all; ++j) product(j, false);
+#pragma unroll 2
+    for (int j = 0; j < all; j += 4) {
+      float4 w[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) w[i] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * PP + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int v = 0; v < OV; ++v) {
+          const float4 x = *reinterpret_cast<const float4*>(Vs + (j + e) * RP + 64 * v + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < R; ++i) axpy(e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w, x, o[i][v]);
+        }
+    }
 #pragma unroll 1
-    for (int j = all; j < nk; ++j) product(j, true);
+    for (int j = all; j < nk; ++j)
+#pragma unroll
+      for (int v = 0; v < OV; ++v) {
+        const float4 x = *reinterpret_cast<const float4*>(Vs + j * RP + 64 * v + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (j < see[i]) axpy(Ps[(ty + 16 * i) * PP + j], x, o[i][v]);
+      }
   }
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < R; ++i) {
+    const int r = ty + 16 * i;
     if (r >= nqv) continue;
     const int qv = qv0 + r, head = g * grp + qv % grp;
     const size_t row = (size_t)(sq.row0 + qv / grp);
-    if (split == 1) {
-      const float inv = 1.f / l[i];  // (every row sees itself: l > 0, or NaN)
-      float* out = static_cast<float*>(a.out) + row * QD + (size_t)head * D + tx * OC;
+    const float f = split == 1 ? 1.f / l[i] : 1.f;  // (every row sees itself: l > 0, or NaN)
+    float* part = static_cast<float*>(a.work) + ((size_t)z * a.M * a.nq + row * a.nq + head) * (D + 4);
+    float* out = split == 1 ? static_cast<float*>(a.out) + row * QD + (size_t)head * D : part;
 #pragma unroll
-      for (int k = 0; k < OC; k += 4)
-        *reinterpret_cast<float4*>(out + k) =
-            make_float4(o[i][k] * inv, o[i][k + 1] * inv, o[i][k + 2] * inv, o[i][k + 3] * inv);
-    } else {
-      float* part = static_cast<float*>(a.work) + ((size_t)z * a.M * a.nq + row * a.nq + head) * (D + 4);
-#pragma unroll
-      for (int k = 0; k < OC; k += 4)
-        *reinterpret_cast<float4*>(part + tx * OC + k) = make_float4(o[i][k], o[i][k + 1], o[i][k + 2], o[i][k + 3]);
-      if (tx == 0) {
-        part[D] = m[i];
-        part[D + 1] = l[i];
-      }
+    for (int v = 0; v < OV; ++v)
+      *reinterpret_cast<float4*>(out + 64 * v + 4 * tx) =
+          make_float4(o[i][v].x * f, o[i][v].y * f, o[i][v].z * f, o[i][v].w * f);
+    if (split > 1 && tx == 0) {
+      part[D] = m[i];
+      part[D + 1] = l[i];
     }
   }
 }
@@ -307,14 +329,15 @@ __global__ void __launch_bounds__(128) prompt_simt_merge_kernel(const __grid_con
   for (int k = 0; k < D / 32; ++k) out[lane + 32 * k] = o[k] / L;
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t ps_launch(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
+  using C = PsCfg<D, R>;
   const int split = ps_split(a, num_sms);
   cudaError_t e =
-      cudaFuncSetAttribute(prompt_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PsCfg<D>::SMEM);
+      cudaFuncSetAttribute(prompt_simt_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prompt_simt_kernel<D>, dim3((unsigned)ps_max_tiles(a), a.nkv, split), dim3(kPsThreads),
-                 PsCfg<D>::SMEM, st, a, split);
+  e = launch_pdl(prompt_simt_kernel<D, R>, dim3((unsigned)ps_max_tiles(a, C::Q), a.nkv, split), dim3(kPsThreads),
+                 C::SMEM, st, a, split);
   if (e != cudaSuccess || split == 1) return e;
   return launch_pdl(prompt_simt_merge_kernel<D>, dim3((unsigned)(((long long)a.M * a.nq + 3) / 4)), dim3(128), 0, st, a,
                     split);
@@ -330,7 +353,8 @@ size_t prompt_attn_workspace(const PromptAttnDesc& a, int num_sms) {
 
 cudaError_t launch_prompt_attention(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
   if (a.dtype == DFLASH_BF16) return launch_prompt_tc(a, num_sms, st);
-  return a.d == 128 ? ps_launch<128>(a, num_sms, st) : ps_launch<64>(a, num_sms, st);
+  if (ps_rows(a, num_sms) == 1) return a.d == 128 ? ps_launch<128, 1>(a, num_sms, st) : ps_launch<64, 1>(a, num_sms, st);
+  return a.d == 128 ? ps_launch<128, 4>(a, num_sms, st) : ps_launch<64, 4>(a, num_sms, st);
 }
 
 }  // namespace dfl
