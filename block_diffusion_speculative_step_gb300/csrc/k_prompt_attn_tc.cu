@@ -86,7 +86,8 @@ struct PtCfg {
   static constexpr int THREADS = 384;
   static constexpr int K_OFF = 2 * TILE;
   static constexpr int V_OFF = K_OFF + NS * TILE;
-  static constexpr int X_OFF = V_OFF + NS * TILE;
+  static constexpr int O_OFF = V_OFF + NS * TILE;  // 2 KB a softmax warp, where it turns its output rows
+  static constexpr int X_OFF = O_OFF + 8 * 2048;
   static constexpr int X_BYTES = 2048;
   static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -138,6 +139,7 @@ struct PtSeq {
 
 struct PtShared {  // after the tiles
   uint32_t badv[kPtRing][4];  // own rows whose V holds a NaN or infinity, by chunk counter
+  int odd[kPtRing];           // are there such rows?
   int s0, g0, t0, c0, len;    // the CTA's run: first item, position in it, number of positions
   PtSeq q;                    // the first item's sequence
   int x0, per;                // its first position, positions of a run
@@ -633,14 +635,17 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         uint8_t* vt = Vs + slot * TILE;
         auto at = [&](int i) { return reinterpret_cast<uint4*>(vt + tt_off(i / CPR, i % CPR)); };
         if (sg.own(c)) {
+          const int first = max(0, sg.t * tt + 1 - sg.key0(c)) * CPR;  // (rows before it are seen by every row of the item)
           uint32_t any = 0u;
 #pragma unroll 8
-          for (int i = lane; i < nk * CPR; i += 32) any |= tt_odd(*at(i));
-          if (lane < 4) sh->badv[vc % kPtRing][lane] = 0u;
-          __syncwarp();
-          if (__any_sync(0xffffffffu, any != 0u)) {
+          for (int i = first + lane; i < nk * CPR; i += 32) any |= tt_odd(*at(i));
+          const bool odd = __any_sync(0xffffffffu, any != 0u);
+          if (lane == 0) sh->odd[vc % kPtRing] = odd;
+          if (odd) {
+            if (lane < 4) sh->badv[vc % kPtRing][lane] = 0u;
+            __syncwarp();
 #pragma unroll 1
-            for (int i = lane; i < nk * CPR; i += 32) {
+            for (int i = first + lane; i < nk * CPR; i += 32) {
               const uint4 x = *at(i);
               if (tt_odd(x)) {
                 *at(i) = tt_clear_odd(x);
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     const int t = (warp - 4) >> 2, r = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lane_base + (uint32_t)t * 128u, to = ts + 256u;
-    const int rt = pt_div_grp(p, r), head_in = r - rt * grp;  // the row's token of the tile, and head of the group
+    const int rt = pt_div_grp(p, r);  // the row's token of the tile
     const bool in_tile = rt < p.tok;
     PtSeg<false> sg(a, tt);
     int nj = 0, no = 0;
@@ -680,8 +685,8 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
       auto own_seen = [&](int c) { return min(kPtCH, max(0, token + 1 - sg.key0(c))); };
       for (int c = sg.c0; c < sg.c1; ++c) {
         const int nk = sg.keys(c);
-        const bool masked = sg.masked(c);
         const int see = sg.own(c) ? own_seen(c) : nk;
+        const int all = sg.own(c) ? sg.t * tt + t * p.tok + 1 - sg.key0(c) : nk;  // keys that every row of the tile sees
         wait(&sh->sfull[t], (uint32_t)nj);
         // the streams' softmaxes take turns
         if (t == 1) tc::named_bar(7, 256);
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         if (warp_on) {
           constexpr int W = 32, HC = 64;  // columns per step, per part
           auto hide = [&](float (&x)[W], int i) {  // columns W i ..
-            if (masked) {
+            if (all < W * (i + 1)) {
               const int n = see - W * i;
               const uint32_t w = n >= W ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
 #pragma unroll
@@ -831,12 +836,25 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         ++nj;
       }
 
-      // ---- the segment's end: normalise and write, or leave a partial
+      // ---- the segment's end: normalise and write, or leave a partial.  What
+      // does not depend on the last product comes before the wait for it.
+      const bool whole = sg.c0 == 0 && sg.c1 == sg.nch;
+      // A whole item's rows are turned in shared memory, so that four lanes
+      // store 64 bytes of a row: lane i has piece i % 4 of rows i / 4 + 8 k.
+      uint4* stage = reinterpret_cast<uint4*>(sm + Cfg::O_OFF + (warp - 4) * 2048);
+      uint32_t piece_at[4];  // in 16-byte pieces of `out` (the host checks that they fit)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = (warp & 3) * 32 + 8 * k + (lane >> 2), tk = pt_div_grp(p, rr), at = sg.t * tt + t * p.tok + tk;
+        const bool write = tk < p.tok && at < sg.q.n && DFL_CHECK(sg.q.row0 + at < a.M, status);
+        piece_at[k] = write ? ((uint32_t)(sg.q.row0 + at) * a.nq + sg.g * grp + rr - tk * grp) * (D / 8) + (lane & 3)
+                            : 0xffffffffu;
+      }
+      const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
       wait(&sh->ofull[t], (uint32_t)no++);
       __syncwarp();
       tc::tc_fence_after();
       if (warp_on) {
-        const bool whole = sg.c0 == 0 && sg.c1 == sg.nch;
         const float f = whole ? (l_run > 0.f ? 1.f / l_run : l_run == l_run ? 0.f : l_run) : 1.f;
         // visible NaN or infinite values of chunks seen in part
         auto bad_of = [&](int c, int i) {
@@ -844,17 +862,11 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
           const uint32_t w = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
           return w & sh->badv[(nj0 + c - sg.c0) % kPtRing][i];
         };
-        const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
-        uint32_t any_bad = 0u;
-        for (int c = cb; c < sg.c1; ++c)
-          if (sg.masked(c))
-#pragma unroll
-            for (int i = 0; i < 4; ++i) any_bad |= bad_of(c, i);
+        bool any_bad = false;
+        for (int c = cb; c < sg.c1; ++c) any_bad |= sg.masked(c) && sh->odd[(nj0 + c - sg.c0) % kPtRing] != 0;
         float* part = static_cast<float*>(a.work) +
                       ((size_t)2 * blockIdx.x + (sg.c0 > 0 ? 0 : 1)) * pt_slot_floats<D>();
-        const int prow = t * kPtRows + r, row = sg.q.row0 + token;
-        const bool write = has_row && DFL_CHECK(row < a.M, status);
-        uint4* out4 = reinterpret_cast<uint4*>(a.out) + ((size_t)row * a.nq + sg.g * grp + head_in) * (D / 8);
+        const int prow = t * kPtRows + r;
         constexpr int W = 32;  // columns per step
 #pragma unroll 1
         for (int q = 0; q < D / W; ++q) {
@@ -866,7 +878,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
           for (int k = 0; k < W; ++k) o[k] *= f;
           if (any_bad)  // added as they are
             for (int c = cb; c < sg.c1; ++c)
-              if (sg.masked(c))
+              if (sg.masked(c) && sh->odd[(nj0 + c - sg.c0) % kPtRing])
                 for (int i = 0; i < 4; ++i)
                   for (uint32_t b = bad_of(c, i); b; b &= b - 1) {
                     const __nv_bfloat16* v =
@@ -880,12 +892,21 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
                   }
           __syncwarp();
           if (whole) {
-            if (write) {
 #pragma unroll
-              for (int k = 0; k < W / 8; ++k)
-                out4[col / 8 + k] = make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
-                                               tt_pack(o[8 * k + 4], o[8 * k + 5]), tt_pack(o[8 * k + 6], o[8 * k + 7]));
+            for (int k = 0; k < 4; ++k)
+              stage[lane * 4 + (k ^ ((lane >> 1) & 3))] =
+                  make_uint4(tt_pack(o[8 * k], o[8 * k + 1]), tt_pack(o[8 * k + 2], o[8 * k + 3]),
+                             tt_pack(o[8 * k + 4], o[8 * k + 5]), tt_pack(o[8 * k + 6], o[8 * k + 7]));
+            __syncwarp();
+            uint4 y[4];  // (all read before the first is stored: the stores may alias)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rr = 8 * k + (lane >> 2);
+              y[k] = stage[rr * 4 + ((lane & 3) ^ ((rr >> 1) & 3))];
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (piece_at[k] != 0xffffffffu) reinterpret_cast<uint4*>(a.out)[piece_at[k] + col / 8] = y[k];
           } else if (has_row) {
             float4* p4 = reinterpret_cast<float4*>(part) + (size_t)t * (kPtRows * D / 4);
 #pragma unroll
