@@ -40,7 +40,7 @@ int check_prompt_shape(const dflash_dims& d, int S, int M, bool context, int max
   DF_CHECK((long long)M * d.n_q_heads < (1ll << 31) / 16, "%s: too many query vectors", who);
   // pieces (128 query vectors x KV head x 128 keys) of one sequence of all rows, and what every sequence adds
   const double tiles = (double)M * grp / 64 + S, mean = max_pos * (context ? 1.0 / 64 : 0.0) + M / 128.0 + 8;
-  if (tiles * d.n_kv_heads * mean >= (double)(1u << 31) || S > (1 << 20))
+  if (tiles * d.n_kv_heads * mean >= (double)(1u << 31) || S > (1 << 16))
     return fail(DFLASH_ERR_UNSUPPORTED, "%s: too many (query tile, KV head, 128-key chunk) pieces", who);
   return DFLASH_OK;
 }

@@ -611,14 +611,15 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
   } else if (warp == 3) {
     // ---------------------------------------------------- queries, V tiles seen in part
     PtSeg<false> sg(a, tt);
-    int n = 0, vc = 0, nraw = 0;
+    int n = 0, vc = 0, nraw = 0, copied[2] = {0, 0};
     const uint32_t qbytes = (uint32_t)(D / 64) * (uint32_t)(grp * p.tok) * 128u;
     for (bool on = sg.begin(sh); on && ok; on = sg.next(), ++n) {
-#pragma unroll 1
+#pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
         // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
         if (lane == 0) {
+          ++copied[t];
           tc::mbar_arrive_expect_tx(&sh->qfull[t], qbytes);
           const int tok = sg.q.row0 + sg.t * tt + t * p.tok;
 #pragma unroll
@@ -663,8 +664,8 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
       if (!ok) break;
     }
     // the query copies have landed before the CTA's shared memory goes away
-    if (lane == 0 && n > 0)
-      for (int t = 0; t < 2; ++t) tc::mbar_wait(&sh->qfull[t], (uint32_t)(n - 1) & 1u, nullptr, lim_ns);
+    for (int t = 0; t < 2; ++t)
+      if (copied[t] > 0) tc::mbar_wait(&sh->qfull[t], (uint32_t)(copied[t] - 1) & 1u, nullptr, lim_ns);
   } else {
     // ---------------------------------------------------- softmax, stream t
     const int t = (warp - 4) >> 2, r = tid & 127;

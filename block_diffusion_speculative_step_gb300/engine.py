@@ -541,9 +541,10 @@ class Engine:
             for j in range(0, t.layers, D.DFLASH_KV_MAX_LAYERS):
                 k = min(D.DFLASH_KV_MAX_LAYERS, t.layers - j)
                 D.dflash_kv_write(self.kv_write_args(j, k, n, done_d[s:], source=source, seq=s), *ws)
-            at = i32(list(range(done[s], done[s] + n, self.FUSE_ROWS)))
-            for i, r0 in enumerate(range(0, n, self.FUSE_ROWS)):
-                f = self.fuse_args(min(self.FUSE_ROWS, n - r0), self.pfeats[start[s] + r0:], at[i:], None)
+            step = min(self.FUSE_ROWS, self.w.window or self.FUSE_ROWS)  # (a ring takes no two rows of a slot at once)
+            at = i32(list(range(done[s], done[s] + n, step)))
+            for i, r0 in enumerate(range(0, n, step)):
+                f = self.fuse_args(min(step, n - r0), self.pfeats[start[s] + r0:], at[i:], None)
                 f.n_seqs = 1
                 for j in range(self.w.draft.layers):
                     f.kv_layers[j] = self._seq_kv("d", j, s)

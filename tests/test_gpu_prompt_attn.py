@@ -255,3 +255,40 @@ def test_two_streams(dtype):
             p.run(st)
     for p in ps:
         p.check()
+
+
+def test_expired_waits_are_reported():
+    """With its K/V copies switched off the call gives up within its limit,
+    reports it, and the next one on the same workspace is exact."""
+    p = Prompt([300, 70, 1], 8, 2, 128, "bf16", ctx=[100, 0, 513], seed=21)
+    D.dflash_workspace_control(p.ws.ptr, p.ws.bytes, wait_limit_ns=2_000_000, stall_kv_loads=True)
+    p.run()
+    torch.cuda.synchronize()
+    assert p.ws.status() == D.DFLASH_ERR_TIMEOUT
+    D.dflash_workspace_control(p.ws.ptr, p.ws.bytes)
+    p.out.fill_(FILL)
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_problems_that_share_a_workspace(dtype):
+    """Two captured calls of different lengths in turn on one workspace."""
+    ps = [Prompt([400, 3], 8, 2, 64, dtype, seed=22), Prompt([5, 129, 700, 0, 64], 8, 2, 64, dtype, ctx=[0, 7, 300, 9, 128],
+                                                             seed=23)]
+    big = max(ps, key=lambda p: p.ws.bytes)
+    graphs = []
+    for p in ps:
+        p.ws = big.ws
+        p.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.run()
+        graphs.append(g)
+    for p in ps:
+        p.out.fill_(FILL)
+    for g in graphs * 3:
+        g.replay()
+    for p in ps:
+        p.check()

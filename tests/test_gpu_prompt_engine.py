@@ -105,6 +105,19 @@ def test_generation_from_packed_prompts(norms, kind):
     assert torch.equal(out, torch.stack(alone))
 
 
+def test_window_rings():
+    """Prompts longer than the draft's window: its ring holds the last positions."""
+    w = small("f32", window=32)
+    prompts = prompts_of(w, [200, 200])
+    a, b = engine(w, 11, 2), engine(w, 11, 2)
+    a.chunk = 32  # (rows at a time that a ring of 32 takes)
+    a.prefill(torch.stack(prompts))
+    b.prefill(prompts)
+    assert a.status() == D.DFLASH_OK and b.status() == D.DFLASH_OK
+    for x, y in zip(a.caches.dk + a.caches.dv, b.caches.dk + b.caches.dv):
+        assert float((x - y).abs().max()) < 1e-5 * max(1.0, float(x.abs().max()))
+
+
 @pytest.mark.parametrize("piece", [0, 7, 32])
 @pytest.mark.parametrize("page", [0, 128])
 def test_prompts_in_pieces(piece, page):
@@ -167,6 +180,26 @@ def test_scores_in_pieces_and_generation_after():
         b.cycle()
     assert torch.equal(a.out_tokens, b.out_tokens) and torch.equal(a.base_pos, b.base_pos)
     assert a.status() == D.DFLASH_OK and b.status() == D.DFLASH_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_generation_from_packed_prompts_over_an_8_bit_cache(dtype):
+    """A sequence goes on as it does alone: the rows of its prompt see each
+    other unquantised either way.  (bf16: up to a near-tie, so only the caches.)"""
+    w = small(dtype)
+    lens, n = [40, 9, 130], 12
+    prompts = prompts_of(w, lens)
+    eng = engine(w, 12, 3, norms=True, kv8=True)
+    out = eng.greedy_generate(prompts, n)
+    assert eng.status() == D.DFLASH_OK
+    for s, p in enumerate(prompts):
+        one = engine(w, 12, 1, norms=True, kv8=True)
+        alone = one.greedy_generate([p], n)[0]
+        if dtype == "f32":
+            assert torch.equal(out[s], alone)
+            for x, y in zip(eng.caches.tk + eng.caches.tv, one.caches.tk + one.caches.tv):
+                differ = (x[s, :, :lens[s]] != y[0, :, :lens[s]]).float().mean()
+                assert float(differ) < 1e-3  # (codes on a rounding border)
 
 
 @pytest.mark.parametrize("page", [0, 128])
