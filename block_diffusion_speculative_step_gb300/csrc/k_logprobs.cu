@@ -400,7 +400,13 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
       if (nc > 1 && tid < cand) sh.list[tid] = key;
       __syncthreads();
       const float mr = sh.out[0], lnz = sh.out[1];
-      if (key) {
+      const size_t o = (size_t)m_row * d.topk;
+      if (lnz != lnz) {  // no distribution
+        if (tid < d.topk) {
+          d.top_ids[o + tid] = -1;
+          d.top_logprobs[o + tid] = NAN;
+        }
+      } else if (key) {
         int r = tid;
         if (nc > 1) {
           r = 0;
@@ -408,10 +414,8 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
           for (int j = 0; j < cand; ++j) r += sh.list[j] > key;
         }
         if (r < d.topk) {
-          const size_t o = (size_t)m_row * d.topk + r;
-          const bool bad = lnz != lnz;
-          d.top_ids[o] = bad ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
-          d.top_logprobs[o] = bad ? NAN : (lp_value((uint32_t)(key >> 32)) - mr) * d.invT - lnz;
+          d.top_ids[o + r] = (int)(0xFFFFFFFFu - (uint32_t)key);
+          d.top_logprobs[o + r] = (lp_value((uint32_t)(key >> 32)) - mr) * d.invT - lnz;
         }
       }
     }

@@ -627,6 +627,9 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
             tc::tma_load_3d(Qs + t * TILE + h * (kPtRows * 128), &p.q3, 64 * h, sg.g * grp, tok, &sh->qfull[t]);
         }
       }
+      PtSeg<false> nx(sg);
+      if (nx.next() && lane < 2 * (D / 64))  // the next segment's queries into L2
+        tma_prefetch_3d(&p.q3, 64 * (lane >> 1), nx.g * grp, nx.q.row0 + nx.t * tt + (lane & 1) * p.tok);
       for (int c = sg.c0; c < sg.c1 && ok; ++c, ++vc) {
         if (!sg.masked(c)) continue;
         const int nk = sg.keys(c), slot = vc % NS;
@@ -852,11 +855,11 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
                             : 0xffffffffu;
       }
       const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
+      const float f = whole ? (l_run > 0.f ? 1.f / l_run : l_run == l_run ? 0.f : l_run) : 1.f;
       wait(&sh->ofull[t], (uint32_t)no++);
       __syncwarp();
       tc::tc_fence_after();
       if (warp_on) {
-        const float f = whole ? (l_run > 0.f ? 1.f / l_run : l_run == l_run ? 0.f : l_run) : 1.f;
         // visible NaN or infinite values of chunks seen in part
         auto bad_of = [&](int c, int i) {
           const int n = (has_row ? own_seen(c) : 0) - 32 * i;

@@ -158,6 +158,19 @@ def test_rows_that_are_no_distribution(V):
     p.check(status=D.DFLASH_ERR_NUMERIC)
 
 
+@pytest.mark.parametrize("V", [5, 33, 40000])
+def test_rows_of_nan_of_either_sign(V):
+    """All of a row NaN, or all but one element: every alternative says so."""
+    x = rand(4, V, 7)
+    x[0] = -NAN
+    x[1] = NAN
+    x[2] = torch.copysign(torch.full((V,), NAN), torch.tensor(-1.0))
+    x[2, 1] = 1.0
+    p = Scores(x, 5)
+    p.run()
+    p.check(status=D.DFLASH_ERR_NUMERIC)
+
+
 def test_tokens():
     p = Scores(rand(5, 1000), 3, tokens=[0, 999, -1, 5, -1])
     p.run()
