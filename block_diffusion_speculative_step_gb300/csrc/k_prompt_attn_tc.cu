@@ -20,12 +20,19 @@
 //   P = 2^(c S - m)  one thread per query vector, written over S
 //   O += P V         tcgen05.mma, P from tensor memory, V MN-major
 // The streams' softmaxes take turns, so that one stream's products run beside
-// the other's softmax.  A turn is what bounds the kernel: one warp per
-// scheduler, about 900 instructions in a row (8k tokens, 32 / 8 heads: 520 us;
-// 444 without any softmax arithmetic, which the tensor core's rate gives; scores
-// in steps of 16 columns instead of 32: 560).  Scores of 64 keys ahead, two
-// buffers a stream and no turns: 584, for a product 64 columns wide takes
-// almost as long as one of 128.  The reference m stays while the weights' sum suits
+// the other's softmax.  Bound: the chain of a stream.  A chunk of both streams
+// takes 4.1k cycles (8k tokens, 32 / 8 heads), its products 3.0k (61 a product,
+// the tensor core's rate); the chain is softmax 1750, store and hand-over 290,
+// P V 980, the next S 520, commits and wake-ups 500.  8k tokens: 512 us, 1.0
+// PFLOP/s of the formula's, 1.6 of those executed (540 in loops of seconds, at
+// the power limit); without any softmax arithmetic 444; scores in steps of 16
+// columns instead of 32: 560.  Slower too: scores of 64 keys ahead in two
+// buffers a stream without turns (584 where this then took 558: a product 64
+// columns wide takes almost as long as one of 128); P V of a chunk's first half
+// beside the softmax of its second (563, 548); two threads a row (619, 548);
+// the output by four warps of its own (553, 509: with 512 threads 128 registers
+// are left to each).
+// The reference m stays while the weights' sum suits
 // bf16 (which has fp32's exponents): it starts at 0 and takes sums of 2^-30 ..
 // 2^30, so the usual chunk needs no maximum and no rescaling of O.  Otherwise
 // the half chunk is done again with its maximum.
@@ -63,7 +70,9 @@ constexpr int kPtRing = 8;    // chunks whose bad rows are kept
 // many CTAs (seven prompts of up to 33 rows over 131 slots: 12.0 us with 1, 10.1
 // with 4, 14.4 with 6).
 constexpr int kPtLeast = 4;
-constexpr int kPtSetup = 2;   // positions an item has before its chunks', for what it costs besides them
+// Positions an item has before its chunks', for what it costs besides them (16
+// prompts of 229 to 3401 tokens: 681 / 660 / 680 / 698 us with 1 / 2 / 3 / 4).
+constexpr int kPtSetup = 2;
 
 struct PtTma {
   CUtensorMap kc, vc;  // cache rows [..][D], boxes of 64 dims x 128 rows
