@@ -23,7 +23,7 @@
 // the other's softmax.  Bound: the chain of a stream.  A chunk of both streams
 // takes 4.1k cycles (8k tokens, 32 / 8 heads), its products 3.0k (61 a product,
 // the tensor core's rate); the chain is softmax 1750, store and hand-over 290,
-// P V 980, the next S 520, commits and wake-ups 500.  8k tokens: 512 us, 1.0
+// P V 980, the next S 520, commits and wake-ups 500.  8k tokens: 512 us, 1.07
 // PFLOP/s of the formula's, 1.6 of those executed (540 in loops of seconds, at
 // the power limit); without any softmax arithmetic 444; scores in steps of 16
 // columns instead of 32: 560.  Slower too: scores of 64 keys ahead in two
@@ -170,16 +170,21 @@ __device__ __forceinline__ PtSeq pt_seq(const PromptAttnDesc& a, int tt, int s, 
 
 // All positions (one warp); none where row_start leaves [0, M] or decreases.
 // status (or null): told of that, and of contexts out of range.  mine: the
-// sequence of this lane, of the first 32.
-__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status, bool* good, PtSeq* mine) {
+// sequence of this lane, of the first 32, and len its positions.
+__device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_t* status, bool* good, PtSeq* mine,
+                                        int* len) {
   int t = 0;
+  *len = 0;
   bool bad = false, far = false;
   mine->set(a, tt, 0, 0, 0);
   for (int s = threadIdx.x & 31; s < a.n_seqs; s += 32) {
     const PtSeq q = pt_seq(a, tt, s, &far);
-    if (s < 32) *mine = q;
     bad |= q.row0 < 0 || q.row0 > a.M || q.n < 0 || q.n > a.M - q.row0;
     if (!bad) t += q.before(tt, q.T) * a.nkv;
+    if (s < 32) {
+      *mine = q;
+      *len = t;
+    }
   }
   if ((bad || far) && status) raise_status(status, ST_RANGE);
   *good = !__any_sync(0xffffffffu, bad);
@@ -187,12 +192,12 @@ __device__ __forceinline__ int pt_total(const PromptAttnDesc& a, int tt, uint32_
 }
 
 // The item at position x of the flat order, and the position c in it (one
-// warp; x below pt_total's result, mine from there).
+// warp; x below pt_total's result, mine and its length from there).
 struct PtSpot {
   int s, g, t, c;
   PtSeq q;
 };
-__device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int x, const PtSeq& mine) {
+__device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int x, const PtSeq& mine, int mine_len) {
   const int lane = threadIdx.x & 31;
   PtSpot p;
   p.s = a.n_seqs;
@@ -201,12 +206,13 @@ __device__ __forceinline__ PtSpot pt_locate(const PromptAttnDesc& a, int tt, int
   int first = 0;
   for (int b = 0; b < a.n_seqs; b += 32) {
     PtSeq q = mine;
+    int len = mine_len;
     if (b > 0) {
       bool far = false;
       q.set(a, tt, 0, 0, 0);
       if (b + lane < a.n_seqs) q = pt_seq(a, tt, b + lane, &far);
+      len = q.before(tt, q.T) * a.nkv;
     }
-    const int len = q.before(tt, q.T) * a.nkv;
     int inc = len;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -435,6 +441,8 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&p.kb);
     tc::tma_prefetch_desc(&p.vb);
+    tc::tma_prefetch_desc(&p.kc);
+    tc::tma_prefetch_desc(&p.vc);
     tc::tma_prefetch_desc(&p.q3);
   }
   if (warp == 1) tc::tmem_alloc(&sh->tslot, 512);
@@ -443,13 +451,14 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
   if (warp == 0) {
     bool good;
     PtSeq mine;
-    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good, &mine);
+    int mine_len;
+    const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good, &mine, &mine_len);
     const int per = max(kPtLeast, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     const int x0 = (int)min((long long)blockIdx.x * per, (long long)total), len = min(per, total - x0);
     PtSpot sp;
     sp.s = sp.g = sp.t = sp.c = 0;
     sp.q = mine;
-    if (len > 0) sp = pt_locate(a, tt, x0, mine);
+    if (len > 0) sp = pt_locate(a, tt, x0, mine, mine_len);
     if (lane == 0) {
       sh->s0 = sp.s;
       sh->g0 = sp.g;
