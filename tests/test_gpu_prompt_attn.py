@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from block_diffusion_speculative_step_gb300 import dflash as D
-from tests.prompt_ref import FILL, Prompt
+from tests.prompt_ref import FILL, Prompt, attend, half_step, weight_error
 
 pytestmark = pytest.mark.gpu
 
@@ -292,3 +292,24 @@ def test_problems_that_share_a_workspace(dtype):
         g.replay()
     for p in ps:
         p.check()
+
+
+def test_rows_past_2_to_31_elements():
+    """More than 2^31 elements of queries and outputs."""
+    p = Prompt([140] * 999 + [300], 128, 8, 128, "bf16", seed=24)
+    assert p.q.numel() > 2 ** 31
+    p.run()
+    p.check(seqs=[0, 1, 500, 998, 999])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_very_long_prompt(d):
+    """70000 rows: the last ones against the reference."""
+    n, few = 70001, 40
+    p = Prompt([n], 4, 1, d, "bf16", seed=25)
+    p.run()
+    torch.cuda.synchronize()
+    assert p.ws.status() == D.DFLASH_OK
+    out, mag, big = attend(p.q[-few:].double(), p.kb.double(), p.vb.double(), n - few, d ** -0.5)
+    tol = half_step(p.dt) * out.abs() + weight_error(d, n, big, p.dt)[..., None] * mag
+    assert bool(((p.out[-few:].double() - out).abs() <= tol * (1 + half_step(p.dt))).all())

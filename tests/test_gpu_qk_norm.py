@@ -220,3 +220,23 @@ def test_replays():
         x.fill_(FILL)
     g.replay()
     p.check()
+
+
+def test_rows_past_2_to_31_elements():
+    """A projection of more than 2^31 elements: its last rows as they are alone."""
+    M, n = 150000, 3
+    big = Heads([0] * n, 1, 96, 8, 128, src="bf16")
+    qkv = torch.zeros(M, big.width, dtype=torch.bfloat16, device="cuda")
+    assert qkv.numel() > 2 ** 31
+    qkv[-n:] = big.qkv
+    base = torch.zeros(M, dtype=torch.int32, device="cuda")
+    q = torch.full((M, 96, 128), FILL, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.full((M, 8, 128), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    big.run()
+    a = big.a
+    a.n_seqs, a.qkv, a.base_pos, a.q, a.kb, a.vb = M, ptr(qkv), ptr(base), ptr(q), ptr(k), ptr(v)
+    big.run()
+    torch.cuda.synchronize()
+    assert big.ws.status() == D.DFLASH_OK
+    for got, want in ((q, big.q), (k, big.k), (v, big.v)):
+        assert torch.equal(got[-n:], want) and not bool(got[:-n].any())
