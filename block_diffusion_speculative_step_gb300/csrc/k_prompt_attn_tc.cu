@@ -391,7 +391,7 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtSeq& q, int g, i
         }
       }
     }
-    const float inv = L > 0.f ? 1.f / L : L == L ? 0.f : L;
+    const float inv = 1.f / L;  // (every row sees itself: 0 is a row whose scores are all -inf, NaN as 0 / 0)
     uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                           ((size_t)(q.row0 + token) * a.nq + g * p.grp + r - rt * p.grp) * D + cg * CW);
 #pragma unroll
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
                             : 0xffffffffu;
       }
       const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
-      const float f = whole ? (l_run > 0.f ? 1.f / l_run : l_run == l_run ? 0.f : l_run) : 1.f;
+      const float f = whole ? 1.f / l_run : 1.f;  // (as in pt_join)
       wait(&sh->ofull[t], (uint32_t)no++);
       __syncwarp();
       tc::tc_fence_after();

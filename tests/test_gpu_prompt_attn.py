@@ -313,3 +313,23 @@ def test_a_very_long_prompt(d):
     out, mag, big = attend(p.q[-few:].double(), p.kb.double(), p.vb.double(), n - few, d ** -0.5)
     tol = half_step(p.dt) * out.abs() + weight_error(d, n, big, p.dt)[..., None] * mag
     assert bool(((p.out[-few:].double() - out).abs() <= tol * (1 + half_step(p.dt))).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ctx", [0, 300, 5000])
+def test_rows_whose_scores_are_all_minus_infinity(dtype, ctx):
+    """The softmax of nothing but -inf is NaN, in whole items and joined ones;
+    the other rows are as they are without."""
+    p, clean = (Prompt([90], 4, 2, 64, dtype, ctx=[ctx], seed=26) for _ in range(2))
+    for x in (p, clean):
+        x.kb[:, 0, 5] = 1.0
+        x.kc[0, 0, :, 5] = 1.0
+        x.run()
+    assert p.out.isfinite().all()
+    p.q[60:70, 1, 5] = -INF
+    p.run()
+    torch.cuda.synchronize()
+    assert p.ws.status() == D.DFLASH_OK
+    spoiled = torch.zeros(90, 4, dtype=torch.bool, device="cuda")
+    spoiled[60:70, 1] = True
+    assert bool(p.out[spoiled].isnan().all()) and torch.equal(p.out[~spoiled], clean.out[~spoiled])
