@@ -113,6 +113,7 @@ class Engine:
         self.feats = z(S * max(B, prefill_chunk), self.F, H)
         self.ones = torch.ones(S, dtype=torch.int32, device=self.dev)
         self.ws = None
+        self.old_ws = []  # (tensor, address) of the workspaces that this one replaced
         self.paging = {}  # "t" / "d" -> (page table, page size, max pages, pool pages) once paged
         # DFlash 2 draft convolutions: on when the workload has them (the
         # weights sit in the draft layers as conv_w1 / conv_w2)
@@ -502,11 +503,15 @@ class Engine:
         layer = self.prompt_layer_args(0, self.S, n_rows, self.ph, self.base_pos, self.base_pos,
                                        None if self.kv8 else self.base_pos)
         whole = self.prompt_layer_args(0, self.S, n_rows, self.ph, self.base_pos, self.base_pos)
-        need = max(D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, layer), D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, whole),
-                   D.dflash_workspace_bytes(D.DFLASH_OP_FUSE, self.fuse_args(min(longest, self.FUSE_ROWS), self.pfeats, self.base_pos, None)),
-                   D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.verify_args(1, self.h)))
-        if need > self.ws_bytes:
-            self._new_workspace(int(need))
+        self._prompt_workspace(
+            D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, layer), D.dflash_workspace_bytes(D.DFLASH_OP_LAYER, whole),
+            D.dflash_workspace_bytes(D.DFLASH_OP_FUSE, self.fuse_args(min(longest, self.FUSE_ROWS), self.pfeats, self.base_pos, None)),
+            D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.verify_args(1, self.h)))
+
+    def _prompt_workspace(self, *needs):
+        """The workspace grows with the prompts, at least twofold (the smaller ones are kept)."""
+        if max(needs) > self.ws_bytes:
+            self._new_workspace(max(*needs, 2 * self.ws_bytes))
 
     def _prompt_forward(self, prompts, done):
         """One target forward over prompts (one tensor a sequence, maybe
@@ -521,7 +526,7 @@ class Engine:
         i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=self.dev)
         start_d, done_d = i32(start), i32(done)
         pos = torch.cat([torch.arange(b, b + n, dtype=torch.int32, device=self.dev) for b, n in zip(done, lens)])
-        tokens = torch.cat([p.view(-1) for p in prompts]).int().to(self.dev)
+        tokens = torch.cat([p.reshape(-1).to(self.dev).int() for p in prompts])
         self._prompt_buffers(M, max(lens))
         ws = (self.ws_ptr, self.ws_bytes)
         e = self.embed_args(self.tdims, 1, self.ph, tokens)
@@ -560,12 +565,13 @@ class Engine:
         S = self.S
         lens = [int(p.numel()) for p in prompts]
         assert len(prompts) == S and min(lens) >= 1 and max(lens) + self.B <= self.cap
+        assert piece >= 0, "piece is a number of tokens"
         piece = piece or max(lens)
         assert not self.kv8 or piece >= max(lens), "an 8-bit cache takes whole prompts"
         last = torch.zeros(S, self.w.target.hidden, dtype=torch.float32, device=self.dev)
         for c0 in range(0, max(lens), piece):
             done = [min(n, c0) for n in lens]
-            start = self._prompt_forward([p.view(-1)[c0:c0 + piece] for p in prompts], done)
+            start = self._prompt_forward([p.reshape(-1)[c0:c0 + piece] for p in prompts], done)
             for s, n in enumerate(lens):
                 if c0 < n <= c0 + piece:
                     last[s] = self.ph[start[s + 1] - 1]
@@ -596,11 +602,9 @@ class Engine:
                     v = self.verify_args(1, self.ph[r0:], None, logits, update=False)
                     v.n_seqs, v.argmax, v.margin = n, _ptr(argmax), 0
                     v.accept_len, v.out_tokens = _ptr(count), _ptr(argmax)
-                    need = D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, v)
-                    if need > self.ws_bytes:
-                        self._new_workspace(int(need))
+                    self._prompt_workspace(D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, v))
                     D.dflash_verify_accept(v, self.ws_ptr, self.ws_bytes)
-                    nxt = prompts[s].view(-1)[at + 1:at + 1 + n].int().to(self.dev)
+                    nxt = prompts[s].reshape(-1)[at + 1:at + 1 + n].int().to(self.dev)
                     if nxt.numel() < n:  # (no token is given behind the prompt)
                         nxt = torch.cat([nxt, torch.full((1,), D.DFLASH_NO_TOKEN, dtype=torch.int32, device=self.dev)])
                     a = D.dflash_token_logprobs_args()
@@ -630,7 +634,9 @@ class Engine:
         self._new_workspace(int(need))
 
     def _new_workspace(self, n: int):
-        self.ws_bytes = n
+        if self.ws is not None:  # graphs captured of earlier steps use it, and its status has not been read
+            self.old_ws.append((self.ws, self.ws_ptr))
+        self.ws_bytes = int(n)
         self.ws = torch.zeros(self.ws_bytes + 256, dtype=torch.uint8, device=self.dev)
         self.ws_ptr = (self.ws.data_ptr() + 255) & ~255
         D.dflash_workspace_init(self.ws_ptr, self.ws_bytes)
@@ -638,7 +644,8 @@ class Engine:
     # -------------------------------------------------------------- the steps
 
     def status(self) -> int:
-        return D.dflash_read_status(self.ws_ptr)
+        st = [D.dflash_read_status(p) for p in (self.ws_ptr, *(p for _, p in self.old_ws))]
+        return next((x for x in st if x != D.DFLASH_OK), D.DFLASH_OK)
 
     def target_forward(self, rows: int, first, rest=None, taps=True, base_pos=None):
         """Embed the rows and run every target layer causally; keeps tap

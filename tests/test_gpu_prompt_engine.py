@@ -312,3 +312,58 @@ def test_a_captured_prompt_layer():
         torch.cuda.synchronize()
         assert torch.equal(h, want)
     assert eng.status() == D.DFLASH_OK
+
+
+def test_captured_cycles_outlive_a_growing_workspace():
+    """A cycle captured into a graph, then prompts that need a larger
+    workspace: the graph's cycles are the eager ones."""
+    w = small("bf16")
+    short, long = prompts_of(w, [9, 4]), prompts_of(w, [700, 300])
+    eng, ref = engine(w, 11, 2, 1024), engine(w, 11, 2, 1024)
+    eng.prefill(short)
+    eng.cycle()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        eng.cycle()
+    before = eng.ws_ptr
+    for e in (eng, ref):
+        e.score(long, topk=2)
+    assert eng.ws_ptr != before  # (or the case is none)
+    junk = [torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(64)]  # whatever was freed
+    for _ in range(4):
+        g.replay()
+        ref.cycle()
+        assert torch.equal(eng.out_tokens, ref.out_tokens) and torch.equal(eng.base_pos, ref.base_pos)
+    del junk
+    assert eng.status() == D.DFLASH_OK and ref.status() == D.DFLASH_OK
+
+
+def test_a_growing_workspace_keeps_the_status():
+    w = small("f32")
+    eng = engine(w, 12, 1, 1024)
+    a = D.dflash_token_logprobs_args()
+    x, t, o = torch.zeros(1, 8, device="cuda"), torch.tensor([8], dtype=torch.int32, device="cuda"), torch.zeros(1, device="cuda")
+    a.dims.vocab, a.n_rows, a.temperature = 8, 1, 1.0
+    a.logits, a.tokens, a.logprob = x.data_ptr(), t.data_ptr(), o.data_ptr()
+    D.dflash_token_logprobs(a, eng.ws_ptr, eng.ws_bytes)  # a token outside the vocabulary
+    before = eng.ws_ptr
+    eng.prefill(prompts_of(w, [900]))
+    eng._prompt_workspace(eng.ws_bytes + 1)
+    assert eng.ws_ptr != before
+    assert eng.status() == D.DFLASH_ERR_INVALID_ARG and eng.status() == D.DFLASH_OK
+
+
+def test_prompts_as_they_come():
+    """64-bit tokens, strided ones, tokens on the host; and a piece of no tokens."""
+    w = small("f32")
+    plain = prompts_of(w, [40, 7])
+    wide = torch.zeros(40, 3, dtype=torch.int64, device="cuda")
+    wide[:, 1] = plain[0]
+    a, b = engine(w, 13, 2), engine(w, 13, 2)
+    x, y = a.score(plain, topk=2), b.score([wide[:, 1], plain[1].long().cpu()], topk=2)
+    for u, v in zip(x, y):
+        assert all(torch.equal(i, j) for i, j in zip(u, v))
+    assert torch.equal(a.anchor, b.anchor) and a.status() == b.status() == D.DFLASH_OK
+    with pytest.raises(AssertionError):
+        b.prefill_packed(plain, piece=-4)
