@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
   }
 }
 
-// Joins the parts of each query vector, one warp each.
+// Joins the parts (at most 64) of each query vector, one warp each.
 template <int D>
 __global__ void __launch_bounds__(128) prompt_simt_merge_kernel(const __grid_constant__ PromptAttnDesc a, int split) {
   pdl_wait();
@@ -316,13 +316,34 @@ __global__ void __launch_bounds__(128) prompt_simt_merge_kernel(const __grid_con
   if (!__any_sync(0xffffffffu, in) || __any_sync(0xffffffffu, bad)) return;
   const float* part = static_cast<const float*>(a.work) + (size_t)w * (D + 4);
   const size_t step = (size_t)a.M * a.nq * (D + 4);
-  float M = -INFINITY, L = 0.f, o[D / 32] = {};
-  for (int z = 0; z < split; ++z) M = fmaxf(M, part[z * step + D]);
-  for (int z = 0; z < split; ++z) {
-    const float f = exp2f(part[z * step + D] - (M == -INFINITY ? 0.f : M));
-    L = fmaf(part[z * step + D + 1], f, L);
+  float m[2], l[2];  // of parts lane, lane + 32
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = fmaf(part[z * step + lane + 32 * k], f, o[k]);
+  for (int k = 0; k < 2; ++k) {
+    const int z = lane + 32 * k;
+    m[k] = z < split ? part[z * step + D] : -INFINITY;
+    l[k] = z < split ? part[z * step + D + 1] : 0.f;
+  }
+  const float M = warp_max(fmaxf(m[0], m[1])), ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[D / 32] = {};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    m[k] = exp2f(m[k] - ref);
+    L = fmaf(l[k], m[k], L);
+  }
+  L = warp_sum(L);
+#pragma unroll 1
+  for (int b = 0; b < split; b += 8) {  // eight parts' loads in flight
+    float x[8][D / 32];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) x[u][k] = b + u < split ? part[(b + u) * step + lane + 32 * k] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float f = __shfl_sync(0xffffffffu, b < 32 ? m[0] : m[1], (b + u) & 31);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[k] = fmaf(x[u][k], f, o[k]);
+    }
   }
   float* out = static_cast<float*>(a.out) + (size_t)w * D;
 #pragma unroll
