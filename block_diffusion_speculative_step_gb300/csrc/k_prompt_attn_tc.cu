@@ -11,7 +11,14 @@
 // CTA walks its run as segments (the part of one item inside the run): a whole
 // item is normalised and written at once, the first and the last segment may
 // leave a partial (O, m, l); the CTA that leaves an item's last one joins them,
-// in their order.
+// in their order, or a second kernel does (pt_apart).
+//
+// Where sequences have at most a tile of rows (single tokens, short prompts over
+// long contexts) an item is one tile, whose chunks the streams take in turn:
+// two chunks are under way at once, and the streams' outputs are joined from
+// tensor memory at the segment's end.  An empty second tile would cost its
+// products all the same: 64 single tokens over 4096 slots 175 us instead of 314
+// (92% of the copy rate), one over 131072 95 instead of 162.
 //
 // Two streams per CTA, one per query tile, each an online softmax with its own
 // score and output accumulators in tensor memory (S 128 + O D columns).  Per
@@ -51,6 +58,8 @@
 // query copies and V tiles; warps 4..11 the softmax, a query vector per thread.
 #include <math.h>
 
+#include <algorithm>
+
 #include "attn_tc.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -70,6 +79,7 @@ constexpr int kPtRing = 8;    // chunks whose bad rows are kept
 // many CTAs (seven prompts of up to 33 rows over 131 slots: 12.0 us with 1, 10.1
 // with 4, 14.4 with 6).
 constexpr int kPtLeast = 4;
+constexpr int kPtLeastOne = 2;  // of items of one tile (16 rows over 2048 slots: 19.5 / 16.2 / 16.8 / 18.8 us with 1 / 2 / 4 / 6)
 // Positions an item has before its chunks', for what it costs besides them (16
 // prompts of 229 to 3401 tokens: 681 / 660 / 680 / 698 us with 1 / 2 / 3 / 4).
 constexpr int kPtSetup = 2;
@@ -81,6 +91,13 @@ struct PtTma {
   PromptAttnDesc a;
   int grp, tok;        // query heads per KV head, tokens per tile
   uint32_t grp_mul;    // ceil(2^32 / grp) for 2 <= grp, else 0
+  int apart;           // shared items are joined by a kernel of their own
+};
+
+// The shared item that begins in a CTA, for that kernel.
+struct PtItem {
+  int row0, n;  // the item's first row, its tokens (0: none)
+  int g, b1;    // KV head; the CTA with its last part
 };
 
 // r / grp, r < 128.
@@ -88,15 +105,19 @@ __device__ __forceinline__ int pt_div_grp(const PtTma& p, int r) {
   return p.grp_mul ? (int)__umulhi((uint32_t)r, p.grp_mul) : r;
 }
 
-template <int D>
+// TWO: an item has two query tiles, one a stream; otherwise one, whose chunks
+// the streams take in turn.
+template <int D, bool TWO>
 struct PtCfg {
   static constexpr int TILE = kPtCH * D * 2;
-  static constexpr int NS = D == 64 ? 4 : 2;  // K slots, V slots
+  static constexpr int NK = D == 64 ? 4 : 2;              // K slots
+  static constexpr int NV = D == 64 ? 4 : TWO ? 2 : 3;    // V slots
   static constexpr int THREADS = 384;
-  static constexpr int K_OFF = 2 * TILE;
-  static constexpr int V_OFF = K_OFF + NS * TILE;
-  static constexpr int O_OFF = V_OFF + NS * TILE;  // 2 KB a softmax warp, where it turns its output rows
-  static constexpr int X_OFF = O_OFF + 8 * 2048;
+  static constexpr int K_OFF = (TWO ? 2 : 1) * TILE;
+  static constexpr int V_OFF = K_OFF + NK * TILE;
+  static constexpr int O_OFF = V_OFF + NV * TILE;  // 2 KB a softmax warp, where it turns its output rows
+  static constexpr int M_OFF = O_OFF + 8 * 2048;   // the streams' maxima and sums, [2][2][128] (one tile)
+  static constexpr int X_OFF = M_OFF + (TWO ? 0 : 2048);
   static constexpr int X_BYTES = 2048;
   static constexpr size_t SMEM = X_OFF + X_BYTES + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -154,7 +175,7 @@ struct PtShared {  // after the tiles
   int x0, per;                // its first position, positions of a run
   int last;                   // this CTA's partial was its item's last one
   int good;                   // row_start is in order
-  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4], vraw[4];  // (vraw: a ring of its own)
   uint64_t sfull[2], pdone[2], ofull[2], qfull[2], qfree[2];
   uint32_t tslot;
   int abort;
@@ -329,20 +350,27 @@ __host__ __device__ constexpr size_t pt_slot_floats() {
   return (size_t)2 * kPtRows * (D + 2);
 }
 
-// Joins the partials that CTAs b0 .. b1 left of an item, in their order, by
-// eight warps: a warp takes 32 rows and CW columns at a time, lanes are rows,
-// so its reads are 512 contiguous bytes; the loads of U partials are in flight
-// at once.
+// The CTAs' items, behind the slots.
 template <int D>
-__device__ __forceinline__ void pt_join(const PtTma& p, const PtSeq& q, int g, int t, int b0, int b1, int warp) {
-  constexpr int CW = 16, U = 4, CG = D / CW;
+__host__ __device__ __forceinline__ PtItem* pt_items(void* work, int ctas) {
+  return reinterpret_cast<PtItem*>(static_cast<float*>(work) + (size_t)2 * ctas * pt_slot_floats<D>());
+}
+
+// Joins the partials that CTAs b0 .. b1 left of an item, in their order, by
+// warp `warp` of `warps`: a warp takes 32 rows and CW columns at a time, lanes
+// are rows, so its reads are 512 contiguous bytes; the loads of U partials are
+// in flight at once.
+template <int D, bool TWO, int CW, int U>
+__device__ __forceinline__ void pt_join(const PtTma& p, const PtItem& it, int b0, int warp, int warps) {
+  constexpr int CG = D / CW;
+  const int b1 = it.b1;
   const PromptAttnDesc& a = p.a;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int w = warp; w < 8 * CG; w += 8) {
-    const int rg = w / CG, cg = w % CG, tile = rg >> 2, r = (rg & 3) * 32 + lane;
-    const int rt = pt_div_grp(p, r), token = t * 2 * p.tok + tile * p.tok + rt;
-    const bool has_row = rt < p.tok && token < q.n;
+  for (int w = warp; w < (TWO ? 8 : 4) * CG; w += warps) {
+    const int rg = w / CG, cg = w % CG, tile = TWO ? rg >> 2 : 0, r = (rg & 3) * 32 + lane;
+    const int rt = pt_div_grp(p, r), token = tile * p.tok + rt;
+    const bool has_row = rt < p.tok && token < it.n;
     if (!__any_sync(0xffffffffu, has_row)) continue;
     if (!has_row) continue;
     const int mrow = 2 * kPtRows * D + tile * kPtRows + r;
@@ -393,7 +421,7 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtSeq& q, int g, i
     }
     const float inv = 1.f / L;  // (every row sees itself: 0 is a row whose scores are all -inf, NaN as 0 / 0)
     uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                          ((size_t)(q.row0 + token) * a.nq + g * p.grp + r - rt * p.grp) * D + cg * CW);
+                                          ((size_t)(it.row0 + token) * a.nq + it.g * p.grp + r - rt * p.grp) * D + cg * CW);
 #pragma unroll
     for (int k = 0; k < CW / 8; ++k)
       out[k] = make_uint4(tt_pack(o[8 * k] * inv, o[8 * k + 1] * inv), tt_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
@@ -402,10 +430,11 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtSeq& q, int g, i
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const __grid_constant__ PtTma p) {
-  using Cfg = PtCfg<D>;
-  constexpr int TILE = Cfg::TILE, NS = Cfg::NS;
+template <int D, bool TWO>
+__global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(const __grid_constant__ PtTma p) {
+  using Cfg = PtCfg<D, TWO>;
+  constexpr int TILE = Cfg::TILE, NK = Cfg::NK, NV = Cfg::NV;
+  constexpr int STEP = TWO ? 1 : 2;  // a stream's next chunk
   extern __shared__ __align__(1024) uint8_t pt_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_smem) + 1023) & ~uintptr_t(1023));
   uint8_t* Qs = sm;
@@ -417,15 +446,15 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
 
   const PromptAttnDesc& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int grp = p.grp, tt = 2 * p.tok;
+  const int grp = p.grp, tt = (TWO ? 2 : 1) * p.tok;
   uint32_t* status = a.status;
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sh->kfull[i], 1);
-      tc::mbar_init(&sh->kempty[i], 2);  // the two issuers
+      tc::mbar_init(&sh->kempty[i], TWO ? 2 : 1);  // the issuers that use it
       tc::mbar_init(&sh->vfull[i], 1);
-      tc::mbar_init(&sh->vempty[i], 2);
+      tc::mbar_init(&sh->vempty[i], TWO ? 2 : 1);
       tc::mbar_init(&sh->vraw[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -435,7 +464,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
       // observed (bad rows) is visible to who waits here
       tc::mbar_init(&sh->ofull[i], 2);
       tc::mbar_init(&sh->qfull[i], 1);
-      tc::mbar_init(&sh->qfree[i], 1);
+      tc::mbar_init(&sh->qfree[i], TWO ? 1 : 2);
     }
     sh->abort = 0;
     tc::fence_mbar_init();
@@ -453,7 +482,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     PtSeq mine;
     int mine_len;
     const int total = pt_total(a, tt, blockIdx.x == 0 ? status : nullptr, &good, &mine, &mine_len);
-    const int per = max(kPtLeast, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const int per = max(TWO ? kPtLeast : kPtLeastOne, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     const int x0 = (int)min((long long)blockIdx.x * per, (long long)total), len = min(per, total - x0);
     PtSpot sp;
     sp.s = sp.g = sp.t = sp.c = 0;
@@ -518,34 +547,34 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
               else tma_load_2d_plain(dst + h * (kPtCH * 128), mc, 64 * h, row, bar);
             }
           };
-          if (nk >= NS && !wait(&sh->kempty[nk % NS], (uint32_t)(nk / NS - 1))) break;
-          copy(Ks + (nk % NS) * TILE, &p.kb, &p.kc, &sh->kfull[nk % NS]);
+          if (nk >= NK && !wait(&sh->kempty[nk % NK], (uint32_t)(nk / NK - 1))) break;
+          copy(Ks + (nk % NK) * TILE, &p.kb, &p.kc, &sh->kfull[nk % NK]);
           ++nk;
-          if (nv >= NS && !wait(&sh->vempty[nv % NS], (uint32_t)(nv / NS - 1))) break;
+          if (nv >= NV && !wait(&sh->vempty[nv % NV], (uint32_t)(nv / NV - 1))) break;
           const bool part = sg.masked(c);  // warp 3 goes over it and passes it on
           parts = parts << 1 | (part ? 1u : 0u);
-          copy(Vs + (nv % NS) * TILE, &p.vb, &p.vc, part ? &sh->vraw[nraw++ & 3] : &sh->vfull[nv % NS]);
+          copy(Vs + (nv % NV) * TILE, &p.vb, &p.vc, part ? &sh->vraw[nraw++ & 3] : &sh->vfull[nv % NV]);
           ++nv;
         }
       }
       // every copy has landed before the CTA's shared memory goes away
-      for (int i = max(0, nk - NS); i < nk; ++i)
-        tc::mbar_wait(&sh->kfull[i % NS], (uint32_t)(i / NS) & 1u, nullptr, lim_ns);
-      for (int i = max(0, nv - NS); i < nv; ++i)
+      for (int i = max(0, nk - NK); i < nk; ++i)
+        tc::mbar_wait(&sh->kfull[i % NK], (uint32_t)(i / NK) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nv - NV); i < nv; ++i)
         if (!(parts >> (nv - 1 - i) & 1u))
-          tc::mbar_wait(&sh->vfull[i % NS], (uint32_t)(i / NS) & 1u, nullptr, lim_ns);
-      for (int i = max(0, nraw - NS); i < nraw; ++i)
+          tc::mbar_wait(&sh->vfull[i % NV], (uint32_t)(i / NV) & 1u, nullptr, lim_ns);
+      for (int i = max(0, nraw - NV); i < nraw; ++i)
         tc::mbar_wait(&sh->vraw[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, lim_ns);
     }
   } else if (warp == 1 || warp == 2) {
     // ---------------------------------------------------- MMA issue, stream t
     // The whole warp walks the stream's jobs, so that descriptors and
     // addresses stay in uniform registers; one lane issues.
-    const int t = warp - 1;
+    const int t = warp - 1, qt = TWO ? t : 0;  // stream, query tile
     constexpr uint32_t idS = tc::idesc_bf16_f32(kPtRows, kPtCH);
     constexpr uint32_t idV = tc::idesc_bf16_f32_bmn(kPtRows, D);
     const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
-    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + ut * TILE), dk = tc::sdesc_sw128(tc::smem_u32(Ks)),
+    const uint64_t dq = tc::sdesc_sw128(tc::smem_u32(Qs) + (TWO ? ut * TILE : 0u)), dk = tc::sdesc_sw128(tc::smem_u32(Ks)),
                    dv = tc::sdesc_sw128_mn(tc::smem_u32(Vs), kPtCH * 128, 1024);
     const uint32_t tm_s = __reduce_max_sync(0xffffffffu, tmem) + ut * 128u, tm_o = tm_s + 256u;
     // S of the stream's next job is issued right behind P V of the job
@@ -554,20 +583,37 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     int sc = 0, c = 0;           // its chunk counter and chunk
     int s_seg = 0, q_seen = -1;  // segment; the last one whose queries have been waited for
     bool s_on = ss.begin(sh);
-    if (s_on) c = ss.c0;
+    if (s_on) c = ss.c0 + (TWO ? 0 : t);
+    if (!TWO) sc = t;
+    auto next_seg = [&]() {
+      if (!TWO) sc -= c - ss.c1;  // the next segment's first chunk
+      ++s_seg;
+      s_on = ss.next();
+      c = ss.c0 + (TWO ? 0 : t);
+      if (!TWO) sc += t;
+    };
     auto wait_s = [&]() {  // the operands of the next S
+      if constexpr (!TWO) {
+        while (s_on && c >= ss.c1) {  // the segment's one chunk is the other stream's
+          q_seen = s_seg;
+          if (!wait_warp(&sh->qfull[qt], (uint32_t)s_seg)) return;
+          if (lane == 0) tc::mbar_arrive(&sh->qfree[qt]);
+          next_seg();
+        }
+        if (!s_on) return;
+      }
       if (q_seen < s_seg) {
         q_seen = s_seg;
-        if (!wait_warp(&sh->qfull[t], (uint32_t)s_seg)) return;
+        if (!wait_warp(&sh->qfull[qt], (uint32_t)s_seg)) return;
       }
-      wait_warp(&sh->kfull[sc % NS], (uint32_t)(sc / NS));
+      wait_warp(&sh->kfull[sc % NK], (uint32_t)(sc / NK));
     };
     auto issue_s = [&]() {
-      if (!ok) return;
-      const int slot = sc % NS;
+      if (!ok || (!TWO && !s_on)) return;
+      const int slot = sc % NK;
       tc::tc_fence_after();
       const uint64_t k = dk + (uint64_t)(slot * TILE / 16);
-      const bool q_last = c + 1 == ss.c1;
+      const bool q_last = c + STEP >= ss.c1;
       if (tt_elect()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -577,29 +623,27 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         }
         tc::mma_commit(&sh->sfull[t]);
         tc::mma_commit(&sh->kempty[slot]);
-        if (q_last) tc::mma_commit(&sh->qfree[t]);  // the segment's query tile has been read
+        if (q_last) tc::mma_commit(&sh->qfree[qt]);  // the segment's query tile has been read
       }
       __syncwarp();
-      ++sc;
-      if (++c == ss.c1) {
-        ++s_seg;
-        s_on = ss.next();
-        c = ss.c0;
-      }
+      sc += STEP;
+      c += STEP;
+      if (q_last) next_seg();
     };
     if (s_on) {
       wait_s();
       issue_s();
     }
-    int vc = 0;
+    int vc = 0, v_end = 0;  // the stream's chunks; of one tile: all chunks up to the segment's end
     for (bool on = sg.begin(sh); on && ok; on = sg.next()) {
       uint32_t acc0 = 0u;  // the segment's first P V starts the accumulator
-      for (int x = sg.c0; x < sg.c1 && ok; ++x, ++vc) {
-        const int slot = vc % NS, nk = sg.keys(x);
-        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vc / NS))) break;
+      if (!TWO) v_end += sg.c1 - sg.c0;
+      for (int x = sg.c0 + (TWO ? 0 : t); x < sg.c1 && ok; x += STEP, ++vc) {
+        const int vi = TWO ? vc : v_end - (sg.c1 - x), slot = vi % NV, nk = sg.keys(x);
+        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vi / NV))) break;
         // waited for early, so that S follows P V in the tensor pipe without a
         // gap; not across segments, whose query load may still take a while
-        const bool last = x + 1 == sg.c1;
+        const bool last = x + STEP >= sg.c1;
         if (!last && s_on) wait_s();
         if (!wait_warp(&sh->pdone[t], (uint32_t)vc)) break;
         tc::tc_fence_after();
@@ -618,11 +662,14 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         }
         __syncwarp();
         acc0 = 1u;
+        // V's slot is given back behind S, for which the softmax waits; but ahead
+        // of a wait that may pass over segments, whose V comes into the slot
+        if (!TWO && tt_elect()) tc::mma_commit(&sh->vempty[slot]);
         if (s_on) {
           if (last) wait_s();
           issue_s();
         }
-        if (tt_elect()) tc::mma_commit(&sh->vempty[slot]);  // (behind S: the softmax waits for S, nobody yet for V)
+        if (TWO && tt_elect()) tc::mma_commit(&sh->vempty[slot]);
         __syncwarp();
       }
     }
@@ -633,7 +680,7 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     const uint32_t qbytes = (uint32_t)(D / 64) * (uint32_t)(grp * p.tok) * 128u;
     for (bool on = sg.begin(sh); on && ok; on = sg.next(), ++n) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < (TWO ? 2 : 1); ++t) {
         if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
         // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
         if (lane == 0) {
@@ -646,11 +693,12 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
         }
       }
       PtSeg<false> nx(sg);
-      if (nx.next() && lane < 2 * (D / 64))  // the next segment's queries into L2
-        tma_prefetch_3d(&p.q3, 64 * (lane >> 1), nx.g * grp, nx.q.row0 + nx.t * tt + (lane & 1) * p.tok);
+      if (nx.next() && lane < (TWO ? 2 : 1) * (D / 64))  // the next segment's queries into L2
+        tma_prefetch_3d(&p.q3, 64 * (TWO ? lane >> 1 : lane), nx.g * grp,
+                        nx.q.row0 + nx.t * tt + (TWO ? lane & 1 : 0) * p.tok);
       for (int c = sg.c0; c < sg.c1 && ok; ++c, ++vc) {
         if (!sg.masked(c)) continue;
-        const int nk = sg.keys(c), slot = vc % NS;
+        const int nk = sg.keys(c), slot = vc % NV;
         if (!wait_warp(&sh->vraw[nraw & 3], (uint32_t)(nraw >> 2))) break;
         ++nraw;
         constexpr int CPR = D / 8;
@@ -695,24 +743,28 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
     const int rt = pt_div_grp(p, r);  // the row's token of the tile
     const bool in_tile = rt < p.tok;
     PtSeg<false> sg(a, tt);
-    int nj = 0, no = 0;
+    int nj = 0, no = 0;                    // the stream's chunks; segments (of one tile: of stream 0)
+    int nch = 0, no1 = 0;                  // one tile: all chunks; stream 1's segments
+    if (p.apart && tid == 128) pt_items<D>(a.work, gridDim.x)[blockIdx.x].n = 0;  // (no shared item begins here)
     // (after a wait gave up the loops run on without work, to meet the barriers)
     for (bool on = sg.begin(sh); on; on = sg.next()) {
-      const int token = sg.t * tt + t * p.tok + rt;  // of the sequence
+      const int token = sg.t * tt + (TWO ? t * p.tok : 0) + rt;  // of the sequence
       const bool has_row = in_tile && token < sg.q.n;
       const bool warp_on = __any_sync(0xffffffffu, has_row);
       float m_run = -INFINITY, l_run = 0.f;
       const int nj0 = nj;
       // keys of own chunk c that the row sees
       auto own_seen = [&](int c) { return min(kPtCH, max(0, token + 1 - sg.key0(c))); };
-      for (int c = sg.c0; c < sg.c1; ++c) {
+      for (int c = sg.c0 + (TWO ? 0 : t); c < sg.c1; c += STEP) {
         const int nk = sg.keys(c);
         const int see = sg.own(c) ? own_seen(c) : nk;
-        const int all = sg.own(c) ? sg.t * tt + t * p.tok + 1 - sg.key0(c) : nk;  // keys that every row of the tile sees
+        const int all = sg.own(c) ? sg.t * tt + (TWO ? t * p.tok : 0) + 1 - sg.key0(c) : nk;  // keys that every row of the tile sees
         wait(&sh->sfull[t], (uint32_t)nj);
         // the streams' softmaxes take turns
-        if (t == 1) tc::named_bar(7, 256);
-        else if (nj > 0) tc::named_bar(6, 256);
+        if (TWO) {
+          if (t == 1) tc::named_bar(7, 256);
+          else if (nj > 0) tc::named_bar(6, 256);
+        }
         __syncwarp();
         tc::tc_fence_after();
         if (warp_on) {
@@ -845,12 +897,12 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
             }
             if (!over && m_run == -INFINITY) m_run = 0.f;
             sum0 += sum;
-            if (h == min(1, np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
+            if (TWO && h == min(1, np - 1)) named_arrive(t == 0 ? 7 : 6, 256);
 #pragma unroll
             for (int i = 0; i < HC; i += 32) tmem_st32u(ts + HC * h + i, pk + i);
           }
           l_run += sum0;
-        } else {
+        } else if (TWO) {
           named_arrive(t == 0 ? 7 : 6, 256);
         }
         tc::tc_fence_before();
@@ -867,40 +919,72 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
       uint32_t piece_at[4];  // in 16-byte pieces of `out` (the host checks that they fit)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int rr = (warp & 3) * 32 + 8 * k + (lane >> 2), tk = pt_div_grp(p, rr), at = sg.t * tt + t * p.tok + tk;
+        const int rr = (warp & 3) * 32 + 8 * k + (lane >> 2), tk = pt_div_grp(p, rr), at = sg.t * tt + (TWO ? t * p.tok : 0) + tk;
         const bool write = tk < p.tok && at < sg.q.n && DFL_CHECK(sg.q.row0 + at < a.M, status);
         piece_at[k] = write ? ((uint32_t)(sg.q.row0 + at) * a.nq + sg.g * grp + rr - tk * grp) * (D / 8) + (lane & 3)
                             : 0xffffffffu;
       }
       const int cb = max(sg.c0, max(sg.q.cc, sg.c1 - 3));  // (an item's tokens reach into three chunks at most)
-      const float f = whole ? 1.f / l_run : 1.f;  // (as in pt_join)
-      wait(&sh->ofull[t], (uint32_t)no++);
+      float f = 1.f, f1 = 0.f;  // factors of the stream's output; of one tile: of stream 0's and stream 1's
+      if constexpr (TWO) {
+        if (whole) f = 1.f / l_run;  // (as in pt_join)
+        wait(&sh->ofull[t], (uint32_t)no++);
+      } else {
+        float* ml = reinterpret_cast<float*>(sm + Cfg::M_OFF);
+        ml[t * 256 + r] = m_run;
+        ml[t * 256 + 128 + r] = l_run;
+        wait(&sh->ofull[0], (uint32_t)no++);
+        if (sg.c1 - sg.c0 > 1) wait(&sh->ofull[1], (uint32_t)no1++);
+        tc::named_bar(1, 256);
+        const float m0 = ml[r], m1 = ml[256 + r];
+        m_run = fmaxf(m0, m1);
+        f = m0 == -INFINITY ? 0.f : tt_ex2(m0 - m_run);
+        f1 = m1 == -INFINITY ? 0.f : tt_ex2(m1 - m_run);
+        l_run = fmaf(ml[128 + r], f, ml[384 + r] * f1);
+        if (whole) {
+          f /= l_run;
+          f1 /= l_run;
+        }
+      }
       __syncwarp();
       tc::tc_fence_after();
       if (warp_on) {
         // visible NaN or infinite values of chunks seen in part
+        const int cj0 = (TWO ? nj0 : nch) - sg.c0;
         auto bad_of = [&](int c, int i) {
           const int n = (has_row ? own_seen(c) : 0) - 32 * i;
           const uint32_t w = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
-          return w & sh->badv[(nj0 + c - sg.c0) % kPtRing][i];
+          return w & sh->badv[(cj0 + c) % kPtRing][i];
         };
         bool any_bad = false;
-        for (int c = cb; c < sg.c1; ++c) any_bad |= sg.masked(c) && sh->odd[(nj0 + c - sg.c0) % kPtRing] != 0;
+        for (int c = cb; c < sg.c1; ++c) any_bad |= sg.masked(c) && sh->odd[(cj0 + c) % kPtRing] != 0;
         float* part = static_cast<float*>(a.work) +
                       ((size_t)2 * blockIdx.x + (sg.c0 > 0 ? 0 : 1)) * pt_slot_floats<D>();
-        const int prow = t * kPtRows + r;
+        const int prow = (TWO ? t * kPtRows : 0) + r;
         constexpr int W = 32;  // columns per step
 #pragma unroll 1
-        for (int q = 0; q < D / W; ++q) {
-          const int col = W * q;
+        for (int q = 0; q < D / W / STEP; ++q) {  // (of one tile each stream takes half of the columns)
+          const int col = W * q + (TWO ? 0 : t * (D / 2));
           float o[W];
           __syncwarp();  // the load below is warp-collective
-          tc::tmem_ld32(to + col, o);
+          if constexpr (TWO) {
+            tc::tmem_ld32(to + col, o);
 #pragma unroll
-          for (int k = 0; k < W; ++k) o[k] *= f;
+            for (int k = 0; k < W; ++k) o[k] *= f;
+          } else {
+            tc::tmem_ld32(lane_base + 256u + col, o);
+#pragma unroll
+            for (int k = 0; k < W; ++k) o[k] *= f;
+            if (sg.c1 - sg.c0 > 1) {
+              float y[W];
+              tc::tmem_ld32(lane_base + 384u + col, y);
+#pragma unroll
+              for (int k = 0; k < W; ++k) o[k] = fmaf(y[k], f1, o[k]);
+            }
+          }
           if (any_bad)  // added as they are
             for (int c = cb; c < sg.c1; ++c)
-              if (sg.masked(c) && sh->odd[(nj0 + c - sg.c0) % kPtRing])
+              if (sg.masked(c) && sh->odd[(cj0 + c) % kPtRing])
                 for (int i = 0; i < 4; ++i)
                   for (uint32_t b = bad_of(c, i); b; b &= b - 1) {
                     const __nv_bfloat16* v =
@@ -930,36 +1014,44 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
             for (int k = 0; k < 4; ++k)
               if (piece_at[k] != 0xffffffffu) reinterpret_cast<uint4*>(a.out)[piece_at[k] + col / 8] = y[k];
           } else if (has_row) {
-            float4* p4 = reinterpret_cast<float4*>(part) + (size_t)t * (kPtRows * D / 4);
+            float4* p4 = reinterpret_cast<float4*>(part) + (TWO ? (size_t)t * (kPtRows * D / 4) : 0);
 #pragma unroll
             for (int k = 0; k < W / 4; ++k)
               p4[(size_t)(col / 4 + k) * kPtRows + r] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
-        if (!whole && has_row) {
+        if (!whole && has_row && (TWO || t == 0)) {
           float* ml = part + (size_t)2 * kPtRows * D;
           ml[prow] = m_run;
           ml[2 * kPtRows + prow] = l_run;
         }
       }
-      if (sg.c0 > 0 || sg.c1 < sg.nch) {  // the item is shared: who leaves its last partial joins them
+      if (!TWO) tc::tc_fence_before();
+      if (sg.c0 > 0 || sg.c1 < sg.nch) {  // the item is shared
         const int first = sg.c0 > 0 ? sh->x0 - sh->c0 : sh->x0 + sh->len - sg.c1 - kPtSetup;  // the item's first position
         const int b0 = (first + kPtSetup) / sh->per, b1 = (first + kPtSetup + sg.nch - 1) / sh->per;
-        __threadfence();
-        tc::named_bar(1, 256);
-        if (tid == 128) {
-          uint32_t* ctr = a.counters + b0;
-          const uint32_t before = atomicAdd(ctr, 1u);
-          sh->last = before == (uint32_t)(b1 - b0);
-          if (sh->last) *ctr = 0u;  // (ready for the next launch)
+        const PtItem it{sg.q.row0 + sg.t * tt, sg.end - sg.t * tt, sg.g, b1};
+        if (p.apart) {
+          if (sg.c0 == 0 && tid == 128) pt_items<D>(a.work, gridDim.x)[blockIdx.x] = it;
+        } else {  // who leaves the last partial joins them
           __threadfence();
+          tc::named_bar(1, 256);
+          if (tid == 128) {
+            uint32_t* ctr = a.counters + b0;
+            const uint32_t before = atomicAdd(ctr, 1u);
+            sh->last = before == (uint32_t)(b1 - b0);
+            if (sh->last) *ctr = 0u;  // (ready for the next launch)
+            __threadfence();
+          }
+          tc::named_bar(1, 256);
+          if (sh->last) pt_join<D, TWO, 16, 4>(p, it, b0, warp - 4, 8);
         }
-        tc::named_bar(1, 256);
-        if (sh->last) pt_join<D>(p, sg.q, sg.g, sg.t, b0, b1, warp - 4);
-        tc::named_bar(1, 256);  // (sh->last has been read)
       }
+      // (sh->last has been read; of one tile, the streams' outputs, maxima and sums)
+      if (!TWO || !p.apart) tc::named_bar(1, 256);
+      nch += sg.c1 - sg.c0;
     }
-    if (t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
+    if (TWO && t == 0 && nj > 0) tc::named_bar(6, 256);  // meets stream 1's last arrival
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -969,9 +1061,34 @@ __global__ void __launch_bounds__(PtCfg<D>::THREADS, 1) prompt_tc_kernel(const _
   }
 }
 
-template <int D>
+// Joins every shared item: CTA (b, y) takes every gridDim.y-th share of the one
+// that begins in CTA b of the kernel before.
+template <int D, bool TWO>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PtTma p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(pt_items<D>(p.a.work, gridDim.x)) + blockIdx.x);
+  const PtItem it{x.x, x.y, x.z, x.w};
+  if (it.n > 0) pt_join<D, TWO, 8, 8>(p, it, blockIdx.x, blockIdx.y * 8 + (threadIdx.x >> 5), gridDim.y * 8);
+}
+
+// Are shared items joined by a kernel of their own?  Within the kernel one CTA
+// reads an item's partials (65 GB/s), while the second launch costs 3 us but
+// spreads them over all SMs: from 256 KB an item on, or 16 partials, by what is
+// known here of the lengths.  In the kernel / apart: 64 rows over 8000 slots 51
+// / 26 us, 32 over 4000 28 / 17.5, 1 over 8000 18.3 / 17.2; 5 rows over nothing
+// 7.1 / 10.8, 200 sequences of 5 rows over 300 53 / 57.
+bool pt_apart(const PromptAttnDesc& a, int num_sms, int tt) {
+  const double rows = (double)a.M / a.n_seqs, grp = a.nq / a.nkv;
+  const double items = (double)a.nkv * std::max((double)a.n_seqs, (double)a.M / tt);
+  const double chunks = ((double)a.max_pos + rows) / kPtCH + 1;
+  const double parts = std::min(num_sms / items, chunks / kPtLeastOne);
+  return parts >= 16 || parts * std::min(rows, (double)tt) * grp * a.d * 4 >= 256 * 1024;
+}
+
+template <int D, bool TWO>
 cudaError_t pt_launch(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
-  using Cfg = PtCfg<D>;
+  using Cfg = PtCfg<D, TWO>;
   PtTma p;
   p.a = a;
   p.grp = a.nq / a.nkv;
@@ -987,19 +1104,28 @@ cudaError_t pt_launch(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
     okm = okm && make_tmap_bf16(&p.kc, a.kc, D, rows, kPtCH) && make_tmap_bf16(&p.vc, a.vc, D, rows, kPtCH);
   }
   if (!okm) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_tc_kernel<D>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
+  p.apart = pt_apart(a, num_sms, p.tok * (TWO ? 2 : 1)) ? 1 : 0;
+  e = launch_pdl(prompt_tc_kernel<D, TWO>, dim3(num_sms), dim3(Cfg::THREADS), Cfg::SMEM, st, p);
+  if (e != cudaSuccess || !p.apart) return e;
+  return launch_pdl(prompt_join_kernel<D, TWO>, dim3(num_sms, TWO ? D / 8 : D / 16), dim3(256), 0, st, p);
 }
 
 }  // namespace
 
 size_t prompt_tc_workspace(const PromptAttnDesc& a, int num_sms) {
-  return (size_t)2 * num_sms * 2 * kPtRows * (a.d + 2) * sizeof(float);
+  return (size_t)num_sms * (2 * 2 * kPtRows * (a.d + 2) * sizeof(float) + sizeof(PtItem));
 }
 
 cudaError_t launch_prompt_tc(const PromptAttnDesc& a, int num_sms, cudaStream_t st) {
-  return a.d == 128 ? pt_launch<128>(a, num_sms, st) : pt_launch<64>(a, num_sms, st);
+  // Items of two tiles where sequences have more rows than a tile on average (one
+  // / two tiles, 32 rows a tile: 8 sequences of 16 rows over 4000 slots 37 / 54
+  // us, of 32 40 / 57, of 33 57 / 48, of 64 59 / 53; 16 of 1 to 64 over 1000 34 /
+  // 38; a prompt of 2000 73 / 58).
+  const bool two = (long long)a.M > (long long)a.n_seqs * (kPtRows / (a.nq / a.nkv));
+  if (two) return a.d == 128 ? pt_launch<128, true>(a, num_sms, st) : pt_launch<64, true>(a, num_sms, st);
+  return a.d == 128 ? pt_launch<128, false>(a, num_sms, st) : pt_launch<64, false>(a, num_sms, st);
 }
 
 }  // namespace dfl

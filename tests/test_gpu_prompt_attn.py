@@ -333,3 +333,84 @@ def test_rows_whose_scores_are_all_minus_infinity(dtype, ctx):
     spoiled = torch.zeros(90, 4, dtype=torch.bool, device="cuda")
     spoiled[60:70, 1] = True
     assert bool(p.out[spoiled].isnan().all()) and torch.equal(p.out[~spoiled], clean.out[~spoiled])
+
+
+FEW = [  # at most a tile's tokens per sequence on average: lens, contexts
+    ([1], [0]),
+    ([1], [1]),
+    ([1] * 40, [37 * i for i in range(40)]),
+    ([1, 0, 2, 0, 0, 5, 1], [128, 9, 0, 640, 1, 127, 4000]),
+    ([3] * 9 + [90], [1000, 0, 0, 129, 1, 256, 2, 0, 77, 300]),
+    ([16, 1, 1, 1, 1, 1, 1, 1], [0, 5000, 0, 0, 0, 700, 0, 0]),
+    ([7], [9000]),
+]
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(32, 8, 128), (8, 1, 64), (4, 4, 128), (14, 2, 64)])
+@pytest.mark.parametrize("page", [0, 128])
+@pytest.mark.parametrize("lens,ctx", FEW)
+def test_few_rows_a_sequence(lens, ctx, page, nq, nkv, d):
+    """Items of a single tile, whose chunks the streams share out."""
+    p = Prompt(lens, nq, nkv, d, "bf16", ctx=ctx, page=page, seed=27)
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_few_rows_with_values_that_later_rows_hold(bad, d):
+    p = Prompt([16, 1, 9, 2, 100, 3, 1, 1, 1, 1], 4, 1, d, "bf16", ctx=[0, 300, 128, 0, 250, 7, 0, 900, 2, 0], seed=28)
+    for row, e in ((9, 3), (15, 0), (20, 17), (28 + 60, 5), (28 + 99, 1), (130, 40)):
+        p.vb[row, 0, e] = bad
+    p.vc[4, 0, 249, 9] = bad
+    p.vc[7, 0, 3, 9] = bad
+    p.run()
+    p.check()
+
+
+def test_few_rows_captured_and_replayed():
+    """The same bits from every replay."""
+    p = Prompt([1] * 30 + [20], 8, 2, 128, "bf16", ctx=[200 * i for i in range(31)], seed=29)
+    p.run()
+    torch.cuda.synchronize()
+    first = p.out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run()
+    for _ in range(5):
+        p.out.fill_(FILL)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p.out, first)
+    assert p.ws.status() == D.DFLASH_OK
+
+
+def test_few_rows_expired_waits_are_reported():
+    p = Prompt([1, 1, 20], 8, 2, 128, "bf16", ctx=[100, 0, 1513], seed=30)
+    D.dflash_workspace_control(p.ws.ptr, p.ws.bytes, wait_limit_ns=2_000_000, stall_kv_loads=True)
+    p.run()
+    torch.cuda.synchronize()
+    assert p.ws.status() == D.DFLASH_ERR_TIMEOUT
+    D.dflash_workspace_control(p.ws.ptr, p.ws.bytes)
+    p.out.fill_(FILL)
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("nq,nkv,d", [(32, 8, 128), (8, 1, 64), (14, 2, 128)])
+@pytest.mark.parametrize("lens,ctx", [([200], [9000]), ([100, 0, 70], [5000, 77, 12000])])
+def test_items_that_many_ctas_share(lens, ctx, nq, nkv, d):
+    """Two tiles an item, joined by a kernel of their own; rows of no sequence stay."""
+    p = Prompt(lens, nq, nkv, d, "bf16", ctx=ctx, lead=3, tail=50, seed=31)
+    p.vb[3 + 60, 0, 5] = NAN
+    p.run()
+    p.check()
+    first = p.out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run()
+    for _ in range(3):
+        p.out.fill_(FILL)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first.isnan(), p.out.isnan()) and torch.equal(first.nan_to_num(), p.out.nan_to_num())
