@@ -17,8 +17,8 @@
 // long contexts) an item is one tile, whose chunks the streams take in turn:
 // two chunks are under way at once, and the streams' outputs are joined from
 // tensor memory at the segment's end.  An empty second tile would cost its
-// products all the same: 64 single tokens over 4096 slots 175 us instead of 314
-// (92% of the copy rate), one over 131072 95 instead of 162.
+// products all the same: 64 single tokens over 4096 slots 171 us instead of 314
+// (94% of the copy rate), one over 131072 92 instead of 162.
 //
 // Two streams per CTA, one per query tile, each an online softmax with its own
 // score and output accumulators in tensor memory (S 128 + O D columns).  Per
@@ -110,12 +110,14 @@ __device__ __forceinline__ int pt_div_grp(const PtTma& p, int r) {
 template <int D, bool TWO>
 struct PtCfg {
   static constexpr int TILE = kPtCH * D * 2;
-  static constexpr int NK = D == 64 ? 4 : 2;              // K slots
-  static constexpr int NV = D == 64 ? 4 : TWO ? 2 : 3;    // V slots
+  static constexpr int NS = D == 64 ? 4 : 2;  // K slots, V slots
+  // Slots of a ring.  With one tile each stream has a ring of its own: who waits
+  // on a slot's barrier by parity must have seen its phase before.
+  static constexpr int R = TWO ? NS : NS / 2;
   static constexpr int THREADS = 384;
-  static constexpr int K_OFF = (TWO ? 2 : 1) * TILE;
-  static constexpr int V_OFF = K_OFF + NK * TILE;
-  static constexpr int O_OFF = V_OFF + NV * TILE;  // 2 KB a softmax warp, where it turns its output rows
+  static constexpr int K_OFF = 2 * TILE;  // behind the streams' query tiles; of one tile: this item's and the next one's
+  static constexpr int V_OFF = K_OFF + NS * TILE;
+  static constexpr int O_OFF = V_OFF + NS * TILE;  // 2 KB a softmax warp, where it turns its output rows
   static constexpr int M_OFF = O_OFF + 8 * 2048;   // the streams' maxima and sums, [2][2][128] (one tile)
   static constexpr int X_OFF = M_OFF + (TWO ? 0 : 2048);
   static constexpr int X_BYTES = 2048;
@@ -433,7 +435,7 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtItem& it, int b0
 template <int D, bool TWO>
 __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(const __grid_constant__ PtTma p) {
   using Cfg = PtCfg<D, TWO>;
-  constexpr int TILE = Cfg::TILE, NK = Cfg::NK, NV = Cfg::NV;
+  constexpr int TILE = Cfg::TILE, R = Cfg::R;
   constexpr int STEP = TWO ? 1 : 2;  // a stream's next chunk
   extern __shared__ __align__(1024) uint8_t pt_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pt_smem) + 1023) & ~uintptr_t(1023));
@@ -527,50 +529,86 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
   if (warp == 0) {
     // ---------------------------------------------------- K/V copies
     if (lane == 0 && !stall) {
-      PtSeg<false> sg(a, tt);
-      int nk = 0, nv = 0, nraw = 0;  // copies issued; V tiles that warp 3 goes over
-      uint32_t parts = 0u;           // which of the last V tiles those were
-      for (bool on = sg.begin(sh); on && ok; on = sg.next()) {
-        for (int c = sg.c0; c < sg.c1 && ok; ++c) {
-          const bool own = sg.own(c);
-          int row = own ? sg.q.row0 + sg.key0(c) : 0;
-          if (!own) {
-            bool bad = false;
-            row = (int)(km.row0(sg.s, c * kPtCH, &bad) + (uint32_t)sg.g * (uint32_t)km.head_rows());
-            if (bad) raise_status(status, ST_RANGE);  // reads page 0 instead
-          }
-          auto copy = [&](uint8_t* dst, const CUtensorMap* mo, const CUtensorMap* mc, uint64_t* bar) {
-            tc::mbar_arrive_expect_tx(bar, TILE);
+      int nk[2] = {0, 0}, nv[2] = {0, 0}, nraw = 0;  // copies issued, by ring; V tiles that warp 3 goes over
+      uint32_t parts[2] = {0u, 0u};                  // which of the last V tiles those were
+      auto copy = [&](const PtSeg<false>& sg, int c, uint8_t* dst, const CUtensorMap* mo, const CUtensorMap* mc,
+                      uint64_t* bar) {
+        const bool own = sg.own(c);
+        int row = own ? sg.q.row0 + sg.key0(c) : 0;
+        if (!own) {
+          bool bad = false;
+          row = (int)(km.row0(sg.s, c * kPtCH, &bad) + (uint32_t)sg.g * (uint32_t)km.head_rows());
+          if (bad) raise_status(status, ST_RANGE);  // reads page 0 instead
+        }
+        tc::mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-              if (own) tc::tma_load_3d(dst + h * (kPtCH * 128), mo, 64 * h, sg.g, row, bar);
-              else tma_load_2d_plain(dst + h * (kPtCH * 128), mc, 64 * h, row, bar);
-            }
-          };
-          if (nk >= NK && !wait(&sh->kempty[nk % NK], (uint32_t)(nk / NK - 1))) break;
-          copy(Ks + (nk % NK) * TILE, &p.kb, &p.kc, &sh->kfull[nk % NK]);
-          ++nk;
-          if (nv >= NV && !wait(&sh->vempty[nv % NV], (uint32_t)(nv / NV - 1))) break;
-          const bool part = sg.masked(c);  // warp 3 goes over it and passes it on
-          parts = parts << 1 | (part ? 1u : 0u);
-          copy(Vs + (nv % NV) * TILE, &p.vb, &p.vc, part ? &sh->vraw[nraw++ & 3] : &sh->vfull[nv % NV]);
-          ++nv;
+        for (int h = 0; h < D / 64; ++h) {
+          if (own) tc::tma_load_3d(dst + h * (kPtCH * 128), mo, 64 * h, sg.g, row, bar);
+          else tma_load_2d_plain(dst + h * (kPtCH * 128), mc, 64 * h, row, bar);
+        }
+      };
+      auto ring = [&](const PtSeg<false>& sg, int c) { return TWO ? 0 : (c - sg.c0) & 1; };
+      auto copy_k = [&](const PtSeg<false>& sg, int c) {
+        const int x = ring(sg, c), slot = x * R + nk[x] % R;
+        if (nk[x] >= R && !wait(&sh->kempty[slot], (uint32_t)(nk[x] / R - 1))) return false;
+        copy(sg, c, Ks + slot * TILE, &p.kb, &p.kc, &sh->kfull[slot]);
+        ++nk[x];
+        return true;
+      };
+      auto copy_v = [&](const PtSeg<false>& sg, int c) {
+        const int x = ring(sg, c), slot = x * R + nv[x] % R;
+        if (nv[x] >= R && !wait(&sh->vempty[slot], (uint32_t)(nv[x] / R - 1))) return false;
+        const bool part = sg.masked(c);  // warp 3 goes over it and passes it on
+        parts[x] = parts[x] << 1 | (part ? 1u : 0u);
+        copy(sg, c, Vs + slot * TILE, &p.vb, &p.vc, part ? &sh->vraw[nraw++ & 3] : &sh->vfull[slot]);
+        ++nv[x];
+        return true;
+      };
+      PtSeg<false> sg(a, tt);
+      bool on = sg.begin(sh);
+      if constexpr (TWO) {
+        for (; on && ok; on = sg.next())
+          for (int c = sg.c0; c < sg.c1 && ok; ++c)
+            if (!copy_k(sg, c) || !copy_v(sg, c)) break;
+      } else {
+        // K(c + 1) before V(c), the order in which their slots come free: after
+        // the scores of chunk c - 1, after the other stream's output of c - 2
+        PtSeg<false> kg(sg);
+        bool k_on = on;
+        int c = sg.c0, k = sg.c0;
+        auto step = [](PtSeg<false>& g, int& i, bool& go) {
+          if (++i == g.c1) {
+            go = g.next();
+            i = g.c0;
+          }
+        };
+        if (k_on && copy_k(kg, k)) step(kg, k, k_on);
+        while (on && ok) {
+          if (k_on) {
+            if (!copy_k(kg, k)) break;
+            step(kg, k, k_on);
+          }
+          if (!copy_v(sg, c)) break;
+          step(sg, c, on);
         }
       }
       // every copy has landed before the CTA's shared memory goes away
-      for (int i = max(0, nk - NK); i < nk; ++i)
-        tc::mbar_wait(&sh->kfull[i % NK], (uint32_t)(i / NK) & 1u, nullptr, lim_ns);
-      for (int i = max(0, nv - NV); i < nv; ++i)
-        if (!(parts >> (nv - 1 - i) & 1u))
-          tc::mbar_wait(&sh->vfull[i % NV], (uint32_t)(i / NV) & 1u, nullptr, lim_ns);
-      for (int i = max(0, nraw - NV); i < nraw; ++i)
+#pragma unroll
+      for (int x = 0; x < (TWO ? 1 : 2); ++x) {
+        for (int i = max(0, nk[x] - R); i < nk[x]; ++i)
+          tc::mbar_wait(&sh->kfull[x * R + i % R], (uint32_t)(i / R) & 1u, nullptr, lim_ns);
+        for (int i = max(0, nv[x] - R); i < nv[x]; ++i)
+          if (!(parts[x] >> (nv[x] - 1 - i) & 1u))
+            tc::mbar_wait(&sh->vfull[x * R + i % R], (uint32_t)(i / R) & 1u, nullptr, lim_ns);
+      }
+      for (int i = max(0, nraw - Cfg::NS); i < nraw; ++i)
         tc::mbar_wait(&sh->vraw[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, lim_ns);
     }
   } else if (warp == 1 || warp == 2) {
     // ---------------------------------------------------- MMA issue, stream t
     // The whole warp walks the stream's jobs, so that descriptors and
     // addresses stay in uniform registers; one lane issues.
-    const int t = warp - 1, qt = TWO ? t : 0;  // stream, query tile
+    const int t = warp - 1;
     constexpr uint32_t idS = tc::idesc_bf16_f32(kPtRows, kPtCH);
     constexpr uint32_t idV = tc::idesc_bf16_f32_bmn(kPtRows, D);
     const uint32_t ut = __reduce_max_sync(0xffffffffu, (uint32_t)t);
@@ -584,49 +622,49 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
     int s_seg = 0, q_seen = -1;  // segment; the last one whose queries have been waited for
     bool s_on = ss.begin(sh);
     if (s_on) c = ss.c0 + (TWO ? 0 : t);
-    if (!TWO) sc = t;
+    const int ring = TWO ? 0 : (int)ut * R;  // the stream's first slot
+    auto qt = [&]() { return TWO ? t : s_seg & 1; };  // query buffer, and its phase
+    auto qph = [&]() { return (uint32_t)(TWO ? s_seg : s_seg >> 1); };
     auto next_seg = [&]() {
-      if (!TWO) sc -= c - ss.c1;  // the next segment's first chunk
       ++s_seg;
       s_on = ss.next();
       c = ss.c0 + (TWO ? 0 : t);
-      if (!TWO) sc += t;
     };
     auto wait_s = [&]() {  // the operands of the next S
       if constexpr (!TWO) {
         while (s_on && c >= ss.c1) {  // the segment's one chunk is the other stream's
           q_seen = s_seg;
-          if (!wait_warp(&sh->qfull[qt], (uint32_t)s_seg)) return;
-          if (lane == 0) tc::mbar_arrive(&sh->qfree[qt]);
+          if (!wait_warp(&sh->qfull[qt()], qph())) return;
+          if (lane == 0) tc::mbar_arrive(&sh->qfree[qt()]);
           next_seg();
         }
         if (!s_on) return;
       }
       if (q_seen < s_seg) {
         q_seen = s_seg;
-        if (!wait_warp(&sh->qfull[qt], (uint32_t)s_seg)) return;
+        if (!wait_warp(&sh->qfull[qt()], qph())) return;
       }
-      wait_warp(&sh->kfull[sc % NK], (uint32_t)(sc / NK));
+      wait_warp(&sh->kfull[ring + sc % R], (uint32_t)(sc / R));
     };
     auto issue_s = [&]() {
       if (!ok || (!TWO && !s_on)) return;
-      const int slot = sc % NK;
+      const int slot = ring + sc % R;
       tc::tc_fence_after();
-      const uint64_t k = dk + (uint64_t)(slot * TILE / 16);
+      const uint64_t k = dk + (uint64_t)(slot * TILE / 16), q = TWO ? dq : dq + (uint64_t)((s_seg & 1) * TILE / 16);
       const bool q_last = c + STEP >= ss.c1;
       if (tt_elect()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           constexpr int kBox = kPtCH * 128 / 16;  // descriptor addresses count 16 bytes
           const uint64_t off = (uint64_t)((j >> 2) * kBox + (j & 3) * 2);
-          tc::mma_bf16(tm_s, dq + off, k + off, idS, j > 0 ? 1u : 0u);
+          tc::mma_bf16(tm_s, q + off, k + off, idS, j > 0 ? 1u : 0u);
         }
         tc::mma_commit(&sh->sfull[t]);
         tc::mma_commit(&sh->kempty[slot]);
-        if (q_last) tc::mma_commit(&sh->qfree[qt]);  // the segment's query tile has been read
+        if (q_last) tc::mma_commit(&sh->qfree[qt()]);  // the segment's query tile has been read
       }
       __syncwarp();
-      sc += STEP;
+      ++sc;
       c += STEP;
       if (q_last) next_seg();
     };
@@ -634,17 +672,18 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
       wait_s();
       issue_s();
     }
-    int vc = 0, v_end = 0;  // the stream's chunks; of one tile: all chunks up to the segment's end
+    int vc = 0;
     for (bool on = sg.begin(sh); on && ok; on = sg.next()) {
       uint32_t acc0 = 0u;  // the segment's first P V starts the accumulator
-      if (!TWO) v_end += sg.c1 - sg.c0;
       for (int x = sg.c0 + (TWO ? 0 : t); x < sg.c1 && ok; x += STEP, ++vc) {
-        const int vi = TWO ? vc : v_end - (sg.c1 - x), slot = vi % NV, nk = sg.keys(x);
-        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vi / NV))) break;
+        const int slot = ring + vc % R, nk = sg.keys(x);
+        if (!wait_warp(&sh->vfull[slot], (uint32_t)(vc / R))) break;
         // waited for early, so that S follows P V in the tensor pipe without a
-        // gap; not across segments, whose query load may still take a while
+        // gap; not across segments, whose query load may still take a while, nor
+        // of one tile, where K comes late (single tokens over 1000 slots, heads of
+        // 64: 37 us, 39 with the wait; over 4096 162 and 158)
         const bool last = x + STEP >= sg.c1;
-        if (!last && s_on) wait_s();
+        if (TWO && !last && s_on) wait_s();
         if (!wait_warp(&sh->pdone[t], (uint32_t)vc)) break;
         tc::tc_fence_after();
         const uint64_t v = dv + (uint64_t)(slot * TILE / 16);
@@ -666,7 +705,7 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
         // of a wait that may pass over segments, whose V comes into the slot
         if (!TWO && tt_elect()) tc::mma_commit(&sh->vempty[slot]);
         if (s_on) {
-          if (last) wait_s();
+          if (!TWO || last) wait_s();
           issue_s();
         }
         if (TWO && tt_elect()) tc::mma_commit(&sh->vempty[slot]);
@@ -676,29 +715,40 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
   } else if (warp == 3) {
     // ---------------------------------------------------- queries, V tiles seen in part
     PtSeg<false> sg(a, tt);
-    int n = 0, vc = 0, nraw = 0, copied[2] = {0, 0};
+    int n = 0, vc = 0, v0 = 0, v1 = 0, nraw = 0, loads = 0;  // (loads: to buffers 0 and 1 in turn)
     const uint32_t qbytes = (uint32_t)(D / 64) * (uint32_t)(grp * p.tok) * 128u;
+    // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
+    auto load_q = [&](const PtSeg<false>& x, int b, int t) {
+      if (lane == 0) {
+        ++loads;
+        tc::mbar_arrive_expect_tx(&sh->qfull[b], qbytes);
+        const int tok = x.q.row0 + x.t * tt + t * p.tok;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tc::tma_load_3d(Qs + b * TILE + h * (kPtRows * 128), &p.q3, 64 * h, x.g * grp, tok, &sh->qfull[b]);
+      }
+    };
     for (bool on = sg.begin(sh); on && ok; on = sg.next(), ++n) {
+      PtSeg<false> nx(sg);
+      if constexpr (TWO) {
 #pragma unroll
-      for (int t = 0; t < (TWO ? 2 : 1); ++t) {
-        if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
-        // (tokens past the sequence's last: other rows' queries or zeros, whose results are not used)
-        if (lane == 0) {
-          ++copied[t];
-          tc::mbar_arrive_expect_tx(&sh->qfull[t], qbytes);
-          const int tok = sg.q.row0 + sg.t * tt + t * p.tok;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tc::tma_load_3d(Qs + t * TILE + h * (kPtRows * 128), &p.q3, 64 * h, sg.g * grp, tok, &sh->qfull[t]);
+        for (int t = 0; t < 2; ++t) {
+          if (n > 0 && !wait_warp(&sh->qfree[t], (uint32_t)(n - 1))) break;
+          load_q(sg, t, t);
+        }
+        if (nx.next() && lane < 2 * (D / 64))  // the next segment's queries into L2
+          tma_prefetch_3d(&p.q3, 64 * (lane >> 1), nx.g * grp, nx.q.row0 + nx.t * tt + (lane & 1) * p.tok);
+      } else {
+        if (n == 0) load_q(sg, 0, 0);
+        if (nx.next()) {  // the next segment's, in the buffer of the one before (200 short items, heads of 64: 60 us without)
+          if (n > 0 && !wait_warp(&sh->qfree[(n + 1) & 1], (uint32_t)((n - 1) >> 1))) break;
+          load_q(nx, (n + 1) & 1, 0);
         }
       }
-      PtSeg<false> nx(sg);
-      if (nx.next() && lane < (TWO ? 2 : 1) * (D / 64))  // the next segment's queries into L2
-        tma_prefetch_3d(&p.q3, 64 * (TWO ? lane >> 1 : lane), nx.g * grp,
-                        nx.q.row0 + nx.t * tt + (TWO ? lane & 1 : 0) * p.tok);
       for (int c = sg.c0; c < sg.c1 && ok; ++c, ++vc) {
         if (!sg.masked(c)) continue;
-        const int nk = sg.keys(c), slot = vc % NV;
+        const int nk = sg.keys(c), i0 = c - sg.c0;
+        const int slot = TWO ? vc % R : (i0 & 1) * R + ((i0 & 1 ? v1 : v0) + (i0 >> 1)) % R;
         if (!wait_warp(&sh->vraw[nraw & 3], (uint32_t)(nraw >> 2))) break;
         ++nraw;
         constexpr int CPR = D / 8;
@@ -731,10 +781,12 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
         if (lane == 0) tc::mbar_arrive(&sh->vfull[slot]);
       }
       if (!ok) break;
+      v0 += (sg.c1 - sg.c0 + 1) >> 1;
+      v1 += (sg.c1 - sg.c0) >> 1;
     }
     // the query copies have landed before the CTA's shared memory goes away
     for (int t = 0; t < 2; ++t)
-      if (copied[t] > 0) tc::mbar_wait(&sh->qfull[t], (uint32_t)(copied[t] - 1) & 1u, nullptr, lim_ns);
+      if (loads > t) tc::mbar_wait(&sh->qfull[t], (uint32_t)((loads - t + 1) / 2 - 1) & 1u, nullptr, lim_ns);
   } else {
     // ---------------------------------------------------- softmax, stream t
     const int t = (warp - 4) >> 2, r = tid & 127;
