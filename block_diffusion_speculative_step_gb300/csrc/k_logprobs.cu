@@ -5,6 +5,8 @@
 // read once.  Each thread keeps a running maximum m, z = sum 2^d and s = sum d
 // 2^d over d = c (x - m), c = log2(e) / T, from which
 //   log p(t) = (x_t - m) / T - ln z,   H = ln z - ln 2 * s / z.
+// ln z is log1p of z without the maximum's own 1, which stays out of the sums
+// (lp_join_sums): a token of probability 1 - p has a log probability of about -p.
 // The alternatives: the topk-th largest of 32 groups' maxima bounds the topk-th
 // largest element from below, and few elements reach it (of 32 groups 31 for
 // topk = 20, by the chances of hitting 20 of 32 groups).  They are gathered in
@@ -15,7 +17,7 @@
 // bring more candidates than the list holds: then warps insert them into
 // sorted lists of 32, one entry per lane, at worst over a second pass.
 //
-// Long calls are bound by HBM (512 rows x 151936: 60 us, 78% of the copy rate;
+// Long calls are bound by HBM (512 rows x 151936: 62 us, 76% of the copy rate;
 // a CTA's next 32 KB are in flight while it exponentiates, two CTAs an SM),
 // short ones by latency (one row: 7 us).  Bounds by sorting every thread's
 // maximum and insertion of every candidate took 68 and 10 us.
@@ -46,7 +48,9 @@ constexpr int kLpGroup = kLpThreads / 32;  // threads of a group
 
 struct LpShared {
   float m[kLpWarps], z[kLpWarps], s[kLpWarps];
-  float row[3];                    // the slice's m, z, s (read by the cluster's first CTA)
+  float own[kLpWarps];             // z of the lane that holds the maximum (z: the others')
+  int who[kLpWarps];               // that lane
+  float row[4];                    // the slice's m, z, s, z - 1 (read by the cluster's first CTA)
   float out[2];                    // the row's m, ln z (NaN: no distribution)
   uint32_t group[32];              // groups' maxima
   uint64_t best[32];               // the slice's best (read by the cluster's first CTA)
@@ -171,13 +175,22 @@ __device__ __forceinline__ void lp_add(const float4 (&x)[N], float mx, float c, 
   }
 }
 
-// A warp's sums joined, in a fixed order; lane 0's are returned in every lane.
-__device__ __forceinline__ void lp_join_sums(float c, float& m, float& z, float& s) {
+// A warp's sums joined, in a fixed order, the same in every lane.  The part
+// `own` of the lane that holds the maximum, which has the maximum's own 1 in it,
+// stays apart from the sum of everything else: beside 1 the small terms of a
+// nearly certain token would be lost, and they are its ln z.  Returns that lane.
+__device__ __forceinline__ int lp_join_sums(float c, float& m, float& z, float& s, float& own) {
   const float mw = warp_max(m);
-  lp_move(m, mw, c, z, s);
+  const int owner = __ffs(__ballot_sync(0xffffffffu, m == mw)) - 1;
+  const bool mine = (int)(threadIdx.x & 31) == owner;
+  float t = mine ? z : z + own;
+  lp_move(m, mw, c, t, s);
+  if (mine) s = fmaf(0.f, own, s);  // (NaN where own is; the maximum's own term is 0)
   m = mw;
-  z = warp_sum(z);
+  own = __shfl_sync(0xffffffffu, own, owner);
+  z = warp_sum(t);
   s = warp_sum(s);
+  return owner;
 }
 
 // HOLD: the slice stays in registers.
@@ -263,22 +276,40 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
 #pragma unroll
   for (int o = kLpGroup / 2; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
   if (tid % kLpGroup == 0) sh.group[tid / kLpGroup] = lp_key(gm);
-  lp_join_sums(c, m, z, s);
+  float own = z;
+  z = 0.f;
+  const int who = lp_join_sums(c, m, z, s, own);
   if (lane == 0) {
     sh.m[warp] = m;
     sh.z[warp] = z;
     sh.s[warp] = s;
+    sh.own[warp] = own;
+    sh.who[warp] = who;
   }
   __syncthreads();
   if (warp == 0) {
     m = lane < kLpWarps ? sh.m[lane] : -FLT_MAX;
     z = lane < kLpWarps ? sh.z[lane] : 0.f;
     s = lane < kLpWarps ? sh.s[lane] : 0.f;
-    lp_join_sums(c, m, z, s);
+    own = lane < kLpWarps ? sh.own[lane] : 0.f;
+    const int w = lp_join_sums(c, m, z, s, own);
+    float rest = own - 1.f;  // own without the maximum's 1
+    if (own > 0.5f && z + own < 1.5f) {
+      // a token holds most of the row: what that thread summed beside its 1, summed again without it
+      rest = 0.f;
+      for (int v = w * 32 + sh.who[w] + lane * kLpThreads; v < n; v += 32 * kLpThreads) {
+        const float4 x = row.load(v0 + v);
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rest += y[e] == m ? 0.f : lp_ex2(fmaxf((y[e] - m) * c, -256.f));
+      }
+      rest = warp_sum(rest);
+    }
     if (lane == 0) {
       sh.row[0] = m;
-      sh.row[1] = z;
+      sh.row[1] = z + own;
       sh.row[2] = s;
+      sh.row[3] = z + rest;
     }
   }
 
@@ -371,16 +402,23 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
   if (rank == 0) {
     if (warp == 0) {
       m = -FLT_MAX;
-      z = s = 0.f;
+      z = s = own = 0.f;
       if (lane < nc) {
         const float* other = cl.map_shared_rank(&sh.row[0], lane);
         m = other[0];
-        z = other[1];
+        own = other[1];
         s = other[2];
+        z = other[3];
       }
-      lp_join_sums(c, m, z, s);
+      const float mr = warp_max(m);
+      const bool first = lane == __ffs(__ballot_sync(0xffffffffu, m == mr)) - 1;  // its maximum's 1 is left out
+      lp_move(m, mr, c, own, s);
+      const float rest = warp_sum(first ? z : own);
+      s = warp_sum(s);
+      m = mr;
+      z = 1.f + rest;
       const bool bad = !(z > 0.5f && z < INFINITY);
-      const float lnz = bad ? NAN : logf(z);
+      const float lnz = bad ? NAN : log1pf(rest);
       if (lane == 0) {
         sh.out[0] = m;
         sh.out[1] = lnz;

@@ -231,3 +231,40 @@ def test_repeats_and_replays():
     p.logits.copy_(rand(6, 151936, 10))
     g.replay()
     p.check()
+
+
+@pytest.mark.parametrize("M,V", [(1, 50), (3, 1021), (1, 151936), (40, 151936), (200, 32000), (400, 5000)])
+@pytest.mark.parametrize("shift", [6.0, 14.0, 30.0, 60.0])
+def test_nearly_certain_tokens(M, V, shift):
+    """The most likely token's log probability is small, and right to its last
+    bits all the same: ln(1 + r), r the others' weights, each off by 2 (|y| + 4)
+    2^-24 for its argument and 2^-22 for the exponential; their sums add a
+    rounding a term, at most V / 1024 + 64 in a row in halves of a thread's
+    elements, warps and clusters; 2^-22 for the logarithm."""
+    g = torch.Generator().manual_seed(V + M)
+    x = torch.randn(M, V, generator=g)
+    at = torch.randint(0, V, (M,), generator=g)
+    x[torch.arange(M), at] += shift + math.log(V)
+    p = Scores(x.cuda(), k=1, tokens=at.tolist())
+    p.run()
+    p.check()
+    # (not by log_softmax, which rounds 1 + r at 2^-53: 2e-16 where ln(1 + r) is 5e-14)
+    rel = p.logits.double() - p.logits.double().amax(-1, keepdim=True)
+    lp = -torch.log1p(rel.exp().scatter(1, at.cuda()[:, None], 0.0).sum(-1))
+    y = 2 * (shift + math.log(V) + 12) * 1.45
+    tol = lp.abs() * (2 * (y + 4) * 2.0 ** -24 + 2.0 ** -21 + (V / 1024 + 64) * 2.0 ** -24) + 2.0 ** -126
+    for got in (p.logprob, p.top[:, 0]):
+        assert bool(((got.double() - lp).abs() <= tol).all()), float(((got.double() - lp).abs() / tol).max())
+
+
+@pytest.mark.parametrize("n", [1, 2, 3])
+def test_equal_largest_logits_of_any_size(n):
+    """One, two or three tokens share the row, the rest has no weight."""
+    for big in (0.0, 80.0, -3.4028234663852886e38):
+        x = torch.full((4, 3000), -INF, device="cuda")
+        for r in range(4):
+            x[r, [7 + r, 1500, 2999][:n]] = big
+        p = Scores(x, k=3, tokens=[7, 8, 9, 10])
+        p.run()
+        p.check()
+        assert torch.equal(p.logprob.cpu(), torch.full((4,), -math.log(n)))
