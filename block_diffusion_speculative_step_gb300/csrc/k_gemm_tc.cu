@@ -1284,6 +1284,12 @@ bool gemm_tc_supported(const GemmDesc& g) {
   return false;
 }
 
+// Sets of slots that the launches of a projection use in turn: those that one
+// fixup reads, and the next launch's, which goes ahead of that fixup.  The
+// launch after it is behind the fixup in the stream, so its stores wait (at
+// griddepcontrol.wait) until the first set has been read.
+constexpr int kPartSets = kMaxFixParts + 1;
+
 // Token rows of each launch: more than 256 rows run as launches of whole
 // sequences (<= 256 rows each).
 int launch_rows(const GemmDesc& g) {
@@ -1296,10 +1302,11 @@ size_t gemm_tc_workspace(const GemmDesc& g, int num_sms) {
   const int n_tiles = g.nseg * gemm_tiles_per_seg(g);
   const long long T = (long long)n_tiles * (g.K / 64);
   const int G = runs_for(T, num_sms), mc = launch_rows(g);
-  if (mc < 1) return 0;
-  size_t b = 0;  // every launch has its own slots: one fixup reads them all
-  for (int m0 = 0; m0 < g.M; m0 += mc) b += part_bytes(G, pick_bn(std::min(mc, g.M - m0)), n_tiles);
-  return b;
+  if (mc < 1 || g.M < 1) return 0;
+  const int parts = (g.M + mc - 1) / mc;
+  const size_t full = part_bytes(G, pick_bn(std::min(mc, g.M)), n_tiles);
+  if (parts > kPartSets) return kPartSets * full;
+  return (parts - 1) * full + part_bytes(G, pick_bn(g.M - (parts - 1) * mc), n_tiles);
 }
 
 namespace {
@@ -1332,9 +1339,9 @@ cudaError_t part_params(const GemmDesc& g, void* ws, size_t ws_bytes, uint32_t* 
 
 }  // namespace
 
-// The GEMM launches of every part first, then one fixup for the deferred
-// parts (BN >= 128), so a part's GEMM does not wait for the previous part's
-// fixup.  A row's result does not depend on the launch it is in: the
+// The GEMM launches of up to kMaxFixParts parts first, then one fixup for the
+// deferred ones (BN >= 128), so a part's GEMM does not wait for the previous
+// part's fixup.  A row's result does not depend on the launch it is in: the
 // k-partition is a function of the tiles and K only.
 cudaError_t launch_gemm_tc(const GemmDesc& g, void* ws, size_t ws_bytes, uint32_t* counters, uint32_t* status,
                            int num_sms, cudaStream_t st) {
@@ -1398,7 +1405,8 @@ cudaError_t launch_gemm_tc(const GemmDesc& g, void* ws, size_t ws_bytes, uint32_
     add_part(c1, p, p.part_b);
     return launch_fixup<256>(f, std::min(max_pieces(p.T, p.G, p.nkb), kFixBatch), st);
   }
-  size_t off = 0;
+  size_t full = 0;  // bytes of a set of slots
+  int set = 0;
   for (int m0 = 0; m0 < g.M; m0 += mc) {
     GemmDesc c = g;
     const int sq = m0 / per;  // first sequence of the launch
@@ -1417,11 +1425,13 @@ cudaError_t launch_gemm_tc(const GemmDesc& g, void* ws, size_t ws_bytes, uint32_
       }
     }
     TcParams p;
+    const size_t off = set * full;
     if (off > ws_bytes) return cudaErrorInvalidValue;
     cudaError_t e = part_params(c, static_cast<char*>(ws) + off, ws_bytes - off, counters, status, num_sms, p);
     if (e != cudaSuccess) return e;
     const int bn = pick_bn(c.M);
-    off += part_bytes(p.G, bn, p.n_tiles);
+    if (m0 == 0) full = part_bytes(p.G, bn, p.n_tiles);
+    set = (set + 1) % kPartSets;
     e = launch_params(p, st);
     if (e != cudaSuccess) return e;
     if (!p.defer) continue;
