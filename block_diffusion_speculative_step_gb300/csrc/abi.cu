@@ -113,6 +113,7 @@ struct LayerShape {
   const int32_t* prompt_start;
   const void *q_norm, *k_norm;
   bool norm() const { return q_norm || k_norm; }
+  bool reads_kv() const { return mode != DFLASH_ATTN_PROMPT || context; }  // (or writes; otherwise kv may hold anything)
 };
 
 void layer_gemms(const LayerShape& L, const dflash_layer_weights* w, GemmDesc* g4) {
@@ -718,9 +719,12 @@ static int check_layer_args_shape(const dflash_layer_args* a, const char* who) {
   DF_CHECK(a != nullptr, "%s: NULL args", who);
   int rc = check_dims(a->dims, who);
   if (rc) return rc;
-  rc = check_kv_pages(a->kv, who);
-  if (rc) return rc;
-  return check_layer_shape(layer_shape_of(a), who);
+  const LayerShape L = layer_shape_of(a);
+  if (L.reads_kv()) {
+    rc = check_kv_pages(a->kv, who);
+    if (rc) return rc;
+  }
+  return check_layer_shape(L, who);
 }
 
 int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws_bytes,
@@ -733,9 +737,9 @@ int dflash_decoder_layer_forward(const dflash_layer_args* a, void* ws, size_t ws
   LayerShape L = layer_shape_of(a);
   const bool tree = L.mode == DFLASH_ATTN_TREE, prompt = L.mode == DFLASH_ATTN_PROMPT;
   DF_CHECK(a->h && a->rope_cs, "%s: NULL pointer", who);
-  DF_CHECK((prompt && !L.context) || (a->base_pos && a->kv.k && a->kv.v), "%s: NULL pointer", who);
+  DF_CHECK(!L.reads_kv() || (a->base_pos && a->kv.k && a->kv.v), "%s: NULL pointer", who);
   DF_CHECK(aligned16(a->q_norm) && aligned16(a->k_norm), "%s: q_norm and k_norm must be 16-byte aligned", who);
-  DF_CHECK(!L.norm() || (aligned16(a->rope_cs) && aligned16(a->kv.k) && aligned16(a->kv.v)),
+  DF_CHECK(!L.norm() || (aligned16(a->rope_cs) && (!L.reads_kv() || (aligned16(a->kv.k) && aligned16(a->kv.v)))),
            "%s: head norms need a 16-byte aligned RoPE table and cache", who);
   if (prompt) {
     DF_CHECK(a->tree_pos && a->prompt_start, "%s: DFLASH_ATTN_PROMPT needs tree_pos and prompt_start", who);

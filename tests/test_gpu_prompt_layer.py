@@ -46,3 +46,26 @@ def test_many_launches_of_rows(lens):
         assert torch.equal(whole[1][r], k) and torch.equal(whole[2][r], v), r0
         assert float((whole[0][r] - h).abs().max()) < 1e-2, r0
         r0 += n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("norms", [False, True])
+def test_a_cache_descriptor_that_is_not_read(dtype, norms):
+    """Without a context kv may hold anything."""
+    w = small(dtype)
+    eng = engine(w, 15, 2, norms=norms)
+    M = 70
+    eng._prompt_buffers(M, 40)
+    start = torch.tensor([0, 30, M], dtype=torch.int32, device="cuda")
+    pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in (30, 40)]).cuda()
+    h0 = torch.randn(M, w.target.hidden, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    out = []
+    for junk in ({}, dict(k=8, v=0, pages=3, page_size=100, max_pages=-1, pool_pages=0, capacity=-7, window=5, k_exp=1)):
+        h = h0.clone()
+        a = eng.prompt_layer_args(0, 2, M, h, start, pos)
+        for k, v in junk.items():
+            setattr(a.kv, k, v)
+        D.dflash_decoder_layer_forward(a, eng.ws_ptr, eng.ws_bytes)
+        assert eng.status() == D.DFLASH_OK
+        out.append(h)
+    assert torch.equal(*out)
