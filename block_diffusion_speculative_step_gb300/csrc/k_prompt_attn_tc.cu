@@ -39,10 +39,17 @@
 // beside the softmax of its second (563, 548); two threads a row (619, 548);
 // the output by four warps of its own (553, 509: with 512 threads 128 registers
 // are left to each).
-// The reference m stays while the weights' sum suits
-// bf16 (which has fp32's exponents): it starts at 0 and takes sums of 2^-30 ..
-// 2^30, so the usual chunk needs no maximum and no rescaling of O.  Otherwise
-// the half chunk is done again with its maximum.
+// The reference m stays while the weights suit bf16 (which has fp32's
+// exponents) and the sums: it starts at 0 where a row's first half chunk sums to
+// 2^-30 at least, and stays while all of the row's weights sum to 2^30 at most,
+// so the usual chunk needs no maximum and no rescaling of O.  Otherwise the half
+// chunk is done again with a new reference: its maximum, or log2 of the row's
+// sum so far, which is no less than the maximum of what the row has seen.  Sums
+// of outputs are thus at most 2^30 max|v|, and 2^39 max|v| where the parts of all
+// CTAs are joined: values up to 2^88 do not overflow on the way, over any number
+// of keys.  (2^22 instead of 2^30, for values up to 2^96, takes new references
+// more often: 8k tokens with scores of standard deviation 1 / 3 / 4: 515 / 531 /
+// 550 us with 2^30, 515 / 546 / 1018 with 2^22.)
 //
 // The softmax is no rounding point: the weights enter their product as two
 // bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products share V's
@@ -75,6 +82,7 @@ namespace {
 constexpr int kPtCH = 128;    // keys per chunk
 constexpr int kPtRows = 128;  // query vectors per tile
 constexpr int kPtRing = 8;    // chunks whose bad rows are kept
+constexpr float kPtMost = 0x1p30f, kPtFew = 0x1p-30f;  // sums of weights that a reference suits (header)
 // Positions of a run at least: shorter ones share an item of few chunks among
 // many CTAs (seven prompts of up to 33 rows over 131 slots: 12.0 us with 1, 10.1
 // with 4, 14.4 with 6).
@@ -899,11 +907,11 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
               }
             }
           };
-          // a new reference, for a row that needs one: the largest of what it has
-          // and of n steps' scores.  (The others keep theirs: a row's result does
-          // not depend on the rows that share its warp, lanes without one included.)
-          auto refer = [&](int i0, int n, bool needs) {
-            const float m_new = fmaxf(cols_max(i0, n), m_run);
+          // a new reference, for a row that needs one: log2 of its sum l so far, or
+          // the largest of n steps' scores.  (The others keep theirs: a row's result
+          // does not depend on the rows that share its warp, lanes without one included.)
+          auto refer = [&](int i0, int n, float l, bool needs) {
+            const float m_new = fmaxf(cols_max(i0, n), m_run == -INFINITY ? m_run : m_run + tt_lg2(l));
             if (!needs) return 1.f;
             const float alpha = m_run == -INFINITY ? 0.f : tt_ex2(m_run - m_new);
             m_run = m_new;
@@ -920,7 +928,7 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
             bool again = false, over;
 #pragma unroll 1
             for (;;) {
-              const float m0 = m_run == -INFINITY ? 0.f : -m_run;
+              const float m0 = m_run == -INFINITY ? 0.f : -m_run, room = kPtMost - (l_run + sum0);
               sa = sb = tt_pair(0.f, 0.f);
               float x[W];
               tmem_ld_async(ts + HC * h, x);
@@ -935,11 +943,11 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
               float s0, s1;
               tt_unpair(tt_add2(sa, sb), s0, s1);
               sum = s0 + s1;
-              // too large for the reference; or a row's first keys, which reference 0 does not suit
-              over = sum > 0x1p30f || (m_run == -INFINITY && sum < 0x1p-30f);
+              // too much for the reference; or a row's first keys, which reference 0 does not suit
+              over = sum > room || (m_run == -INFINITY && sum < kPtFew);
               if (again || !__any_sync(0xffffffffu, over && has_row)) break;
               again = true;
-              const float alpha = refer(h * (HC / W), HC / W, over);
+              const float alpha = refer(h * (HC / W), HC / W, l_run + sum0, over);
               rescale(alpha);
               l_run *= alpha;
               if (h) {  // the half before, stored already

@@ -733,7 +733,9 @@ int dflash_qk_norm_rope(const dflash_qk_norm_rope_args* a, void* ws, size_t ws_b
  * DFLASH_ERR_INVALID_ARG in the status word and nothing is written; a base_pos
  * outside [0, max_pos] raises it and is taken as the nearest value in range.
  * The softmax runs in fp32; with bf16 the weights enter their product with the
- * values as two bf16 terms (2^-16 relative).  A call is deterministic; the
+ * values as two bf16 terms (2^-16 relative).  Outputs are summed before they
+ * are divided by the sum of the weights: values of more than 2^88 in size may
+ * overflow on the way, and of values below 2^-60 bits may be lost.  A call is deterministic; the
  * work is cut into pieces that depend on all the lengths of the launch, so a
  * sequence's last bits may differ with the batch it runs in.
  */
