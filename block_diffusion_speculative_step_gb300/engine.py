@@ -509,9 +509,9 @@ class Engine:
             D.dflash_workspace_bytes(D.DFLASH_OP_VERIFY, self.verify_args(1, self.h)))
 
     def _prompt_workspace(self, *needs):
-        """The workspace grows with the prompts, at least twofold (the smaller ones are kept)."""
+        """The workspace grows with the prompts."""
         if max(needs) > self.ws_bytes:
-            self._new_workspace(max(*needs, 2 * self.ws_bytes))
+            self._new_workspace(max(needs))
 
     def _prompt_forward(self, prompts, done):
         """One target forward over prompts (one tensor a sequence, maybe
@@ -634,9 +634,13 @@ class Engine:
         self._new_workspace(int(need))
 
     def _new_workspace(self, n: int):
-        if self.ws is not None:  # graphs captured of earlier steps use it, and its status has not been read
+        """A workspace of n bytes at least.  The one it replaces is kept: graphs
+        captured of earlier steps use it, and its status has not been read.  So
+        each is twice the one before at least, and all that are kept take no more
+        than the last."""
+        if self.ws is not None:
             self.old_ws.append((self.ws, self.ws_ptr))
-        self.ws_bytes = int(n)
+        self.ws_bytes = max(int(n), 2 * self.ws_bytes)
         self.ws = torch.zeros(self.ws_bytes + 256, dtype=torch.uint8, device=self.dev)
         self.ws_ptr = (self.ws.data_ptr() + 255) & ~255
         D.dflash_workspace_init(self.ws_ptr, self.ws_bytes)
