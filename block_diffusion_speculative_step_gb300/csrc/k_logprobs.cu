@@ -134,7 +134,9 @@ __device__ __forceinline__ void lp_move(float m, float n, float c, float& z, flo
 struct LpRow {
   const float* p;  // 16-byte aligned, `lead` elements before the row
   int lead, V, pieces;
+  uint32_t* status;
   __device__ __forceinline__ float4 load(int v) const {
+    if (!DFL_CHECK((uint32_t)v < (uint32_t)pieces, status)) return make_float4(NAN, NAN, NAN, NAN);
     if ((uint32_t)(v - 1) < (uint32_t)(pieces - 2)) return __ldg(reinterpret_cast<const float4*>(p) + v);
     const int e = 4 * v - lead;
     float x[4];
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
     row.lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) >> 2);
     row.p = base - row.lead;
     row.V = d.V;
+    row.status = d.status;
     row.pieces = (row.lead + d.V + 3) >> 2;
   }
   const float c = d.invT * 1.4426950408889634f;
@@ -245,7 +248,8 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
       um = fmaxf(um, mx);
       lp_add(x, mx, c, m, z2, s2);
       if (--left == 0 || b + 1 == blocks) {
-        sh.unit_max[u++][tid] = um;
+        if (DFL_CHECK(u < kLpUnits, d.status)) sh.unit_max[u][tid] = um;
+        ++u;
         tm = fmaxf(tm, um);
         um = -INFINITY;
         left = q;
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
     };
     // each piece of the units that reach the bound, a unit per warp at a time
     auto units = [&](auto use) {
-      for (int i = warp; i < sh.n_units; i += kLpWarps) {
+      for (int i = warp; i < sh.n_units && DFL_CHECK(i < kLpThreads * kLpUnits, d.status); i += kLpWarps) {
         const int t = sh.unit[i] / kLpUnits, b = sh.unit[i] % kLpUnits, end = min(n, (b + 1) * q * kStep);
         for (int v = b * q * kStep + t; v < end; v += 32 * kLpThreads) {
           const int at = v + lane * kLpThreads;
@@ -349,8 +353,10 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
     } else {
 #pragma unroll
       for (int b = 0; b < kLpUnits; ++b)
-        if (b * q * kStep + tid < min(n, (b + 1) * q * kStep) && lp_key(sh.unit_max[b][tid]) >= bound)
-          sh.unit[atomicAdd(&sh.n_units, 1)] = (uint16_t)(tid * kLpUnits + b);
+        if (b * q * kStep + tid < min(n, (b + 1) * q * kStep) && lp_key(sh.unit_max[b][tid]) >= bound) {
+          const int at = atomicAdd(&sh.n_units, 1);
+          if (DFL_CHECK(at < kLpThreads * kLpUnits, d.status)) sh.unit[at] = (uint16_t)(tid * kLpUnits + b);
+        }
       __syncthreads();
       units(list);
     }
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
         int r = 0;
 #pragma unroll 8
         for (int j = 0; j < cand; ++j) r += sh.list[j] > key;
-        if (r < d.topk) sh.best[r] = key;
+        if (r < d.topk && DFL_CHECK(r < 32, d.status)) sh.best[r] = key;
       }
     } else {
       uint64_t mine = 0;  // lane i: the warp's i-th best so far; 0: none
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
 #pragma unroll 8
           for (int j = 0; j < cand; ++j) r += sh.list[j] > key;
         }
-        if (r < d.topk) {
+        if (r < d.topk && DFL_CHECK(m_row < d.M && 0xFFFFFFFFu - (uint32_t)key < (uint32_t)d.V, d.status)) {
           d.top_ids[o + r] = (int)(0xFFFFFFFFu - (uint32_t)key);
           d.top_logprobs[o + r] = (lp_value((uint32_t)(key >> 32)) - mr) * d.invT - lnz;
         }

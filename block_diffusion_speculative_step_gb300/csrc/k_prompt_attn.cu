@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
   for (int i = tid; i < C::Q * (D / 4); i += kPsThreads) {
     const int r = i / (D / 4), e = i % (D / 4) * 4, qv = qv0 + r;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < nqv)
+    if (r < nqv && DFL_CHECK(sq.row0 + qv / grp < a.M, a.status))
       x = __ldg(reinterpret_cast<const float4*>(q + (sq.row0 + qv / grp) * QD + (size_t)(g * grp + qv % grp) * D + e));
     *reinterpret_cast<float4*>(Qs + r * RP + e) = x;
   }
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
     const int nk = min(kPsK, ctx ? sq.ctx - j0 : last + 1 - j0);  // keys that some row of the tile sees
     const float *kp, *vp;
     size_t pitch;
+    long long first, rows;  // the chunk's first row, those of its buffer
     if (ctx) {
       bool badp = false;
       const size_t r0 = (size_t)km.row0(s, j0, &badp) + (size_t)g * km.head_rows();
@@ -167,18 +168,22 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
       kp = static_cast<const float*>(a.kc) + r0 * D;
       vp = static_cast<const float*>(a.vc) + r0 * D;
       pitch = D;
+      first = (long long)r0;
+      rows = (long long)(a.pages ? a.pool : a.n_seqs) * a.nkv * km.head_rows();
     } else {
       const size_t r0 = (size_t)(sq.row0 + j0) * KD + (size_t)g * D;
       kp = static_cast<const float*>(a.kb) + r0;
       vp = static_cast<const float*>(a.vb) + r0;
       pitch = KD;
+      first = sq.row0 + j0;
+      rows = a.M;
     }
     __syncthreads();  // the chunk before has been used
     bool odd = false;  // a value is NaN or infinite
     for (int i = tid; i < kPsK * (D / 4); i += kPsThreads) {
       const int r = i / (D / 4), e = i % (D / 4) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (r < nk) {
+      if (r < nk && DFL_CHECK(first + r < rows, a.status)) {
         x = __ldg(reinterpret_cast<const float4*>(kp + r * pitch + e));
         y = __ldg(reinterpret_cast<const float4*>(vp + r * pitch + e));
       }
@@ -285,6 +290,7 @@ __global__ void __launch_bounds__(kPsThreads) prompt_simt_kernel(const __grid_co
     if (r >= nqv) continue;
     const int qv = qv0 + r, head = g * grp + qv % grp;
     const size_t row = (size_t)(sq.row0 + qv / grp);
+    if (!DFL_CHECK(row < (size_t)a.M && head < a.nq && z < split, a.status)) continue;
     const float f = split == 1 ? 1.f / l[i] : 1.f;  // (every row sees itself: l > 0, or NaN)
     float* part = static_cast<float*>(a.work) + ((size_t)z * a.M * a.nq + row * a.nq + head) * (D + 4);
     float* out = split == 1 ? static_cast<float*>(a.out) + row * QD + (size_t)head * D : part;

@@ -375,6 +375,7 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtItem& it, int b0
   constexpr int CG = D / CW;
   const int b1 = it.b1;
   const PromptAttnDesc& a = p.a;
+  if (!DFL_CHECK(b0 >= 0 && b1 < (int)gridDim.x && it.g >= 0 && it.g < a.nkv, a.status)) return;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int w = warp; w < (TWO ? 8 : 4) * CG; w += warps) {
@@ -382,7 +383,7 @@ __device__ __forceinline__ void pt_join(const PtTma& p, const PtItem& it, int b0
     const int rt = pt_div_grp(p, r), token = tile * p.tok + rt;
     const bool has_row = rt < p.tok && token < it.n;
     if (!__any_sync(0xffffffffu, has_row)) continue;
-    if (!has_row) continue;
+    if (!has_row || !DFL_CHECK(it.row0 >= 0 && it.row0 + token < a.M, a.status)) continue;
     const int mrow = 2 * kPtRows * D + tile * kPtRows + r;
     const size_t orow = (size_t)tile * (kPtRows * D) + ((size_t)(cg * (CW / 4)) * kPtRows + r) * 4;
     float M = -INFINITY, L = 0.f, o[CW];
@@ -548,6 +549,9 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
           row = (int)(km.row0(sg.s, c * kPtCH, &bad) + (uint32_t)sg.g * (uint32_t)km.head_rows());
           if (bad) raise_status(status, ST_RANGE);  // reads page 0 instead
         }
+        if (!DFL_CHECK((uint32_t)row < (own ? (uint32_t)a.M : (uint32_t)(a.pages ? a.pool : a.n_seqs) * a.nkv * km.head_rows()),
+                       status))
+          row = 0;
         tc::mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -1047,9 +1051,10 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
               if (sg.masked(c) && sh->odd[(cj0 + c) % kPtRing])
                 for (int i = 0; i < 4; ++i)
                   for (uint32_t b = bad_of(c, i); b; b &= b - 1) {
+                    const int vrow = sg.q.row0 + sg.key0(c) + 32 * i + __ffs(b) - 1;
+                    if (!DFL_CHECK(vrow >= 0 && vrow < a.M, status)) continue;
                     const __nv_bfloat16* v =
-                        static_cast<const __nv_bfloat16*>(a.vb) +
-                        ((size_t)(sg.q.row0 + sg.key0(c) + 32 * i + __ffs(b) - 1) * a.nkv + sg.g) * D + col;
+                        static_cast<const __nv_bfloat16*>(a.vb) + ((size_t)vrow * a.nkv + sg.g) * D + col;
 #pragma unroll
                     for (int k = 0; k < W; ++k) {
                       const float x = __bfloat162float(v[k]);
@@ -1097,7 +1102,7 @@ __global__ void __launch_bounds__(PtCfg<D, TWO>::THREADS, 1) prompt_tc_kernel(co
           __threadfence();
           tc::named_bar(1, 256);
           if (tid == 128) {
-            uint32_t* ctr = a.counters + b0;
+            uint32_t* ctr = a.counters + (DFL_CHECK(b0 >= 0 && b0 < (int)gridDim.x, status) ? b0 : blockIdx.x);
             const uint32_t before = atomicAdd(ctr, 1u);
             sh->last = before == (uint32_t)(b1 - b0);
             if (sh->last) *ctr = 0u;  // (ready for the next launch)

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kQnThreads) qk_norm_kernel(const __grid_consta
   const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + ((size_t)(live ? pos : 0) * (D / 2) + 4 * i) * 2);
   const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);  // (cos, sin) of elements 4i, 4i+1; 4i+2, 4i+3
   // where the row's keys and values go
-  size_t row = (size_t)m * a.nkv, step = 1;
+  size_t row = (size_t)m * a.nkv, step = 1, rows = (size_t)a.M * a.nkv;  // (rows: of the destination)
   bool kv_live = live;
   if (a.cache && h0 + HPG > a.nq) {
     const KvMap km{a.pages, a.cap, a.ps, a.max_pages, a.pool, a.nkv};
@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kQnThreads) qk_norm_kernel(const __grid_consta
     if (live && !bad) {
       row = km.row0(s, pos, &bad);
       step = km.head_rows();
+      rows = (size_t)(a.pages ? a.pool : a.M / a.rows) * a.nkv * step;
     }
     if (bad) {
       if (i == 0) raise_status(a.status, ST_RANGE);
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kQnThreads) qk_norm_kernel(const __grid_consta
       rope_rot(p.w, q.w, c1.z, c1.w, p.w, q.w);
     }
     if (h >= heads || !(is_q ? live : kv_live)) continue;
+    if (!DFL_CHECK(is_q ? m < a.M : row + (size_t)((h - a.nq) % a.nkv) * step < rows, a.status)) continue;
     TO* out = is_q ? static_cast<TO*>(a.q) + ((size_t)m * a.nq + h) * D
                    : static_cast<TO*>(is_v ? a.v : a.k) + (row + (size_t)((h - a.nq) % a.nkv) * step) * D;
     qn_store(out + 4 * i, p);

@@ -18,6 +18,7 @@ __device__ __forceinline__ void prompt_layer_rows(const PromptAttnDesc& a, bool 
   const long long per = (long long)a.nq * a.d * (int)sizeof(T) / 16, out = a.M - (r1 - r0);
   for (long long k = i; k < out * per; k += n) {
     const long long m = k / per < r0 ? k / per : k / per + (r1 - r0);
+    if (!DFL_CHECK(m >= 0 && m < a.M, a.status)) continue;
     reinterpret_cast<uint4*>(a.out)[m * per + k % per] = make_uint4(0, 0, 0, 0);
   }
 }
