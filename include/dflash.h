@@ -692,7 +692,9 @@ int dflash_kv_read(const dflash_kv_read_args* a, void* ws, size_t ws_bytes, dfla
  * attention of a model that normalises every query and key head:
  *   y = x / sqrt(mean(x^2) + rms_eps) * gain   (per head; no gain: y = x),
  *   (y_i, y_{i+d/2}) rotated by the position (rotate-half, dflash_rope_table),
- * in fp32, rounded once to dims.dtype; values are rounded and not turned.
+ * in fp32, rounded once to dims.dtype; values are rounded and not turned.  The
+ * squares are summed in fp32 as they are: heads of elements up to 2^59 in size,
+ * and of 2^-50 or more where rms_eps is 0, are in range.
  * Row m of the M = n_seqs * rows rows belongs to sequence m / rows and sits at
  * position base_pos[m / rows] + m % rows (packed prompts and trees: n_seqs =
  * M, rows = 1, base_pos = the rows' positions).  Keys and values go to kb /
@@ -725,19 +727,19 @@ int dflash_qk_norm_rope(const dflash_qk_norm_rope_args* a, void* ws, size_t ws_b
  * dflash_prompt_attention: per query head, for row i of sequence s
  *   out = softmax_j(scale * q . k_j) v_j  over the cache slots j < base_pos[s]
  *   and the sequence's own rows j <= i (kb / vb).
- * Sequences may be empty.  Rows that belong to no sequence (before
- * row_start[0], behind row_start[n_seqs]) are not read and their outputs are
- * left as they were.  What a row does not see may hold anything; a NaN or
- * infinity that it sees makes the outputs that it reaches NaN or infinite.  A
- * row_start outside [0, n_rows] or below the one before it raises
+ * At most 65536 sequences, which may be empty.  Rows that belong to no sequence
+ * (before row_start[0], behind row_start[n_seqs]) are not read and their
+ * outputs are left as they were.  What a row does not see may hold anything; a
+ * NaN or infinity that it sees makes the outputs that it reaches NaN or
+ * infinite.  A row_start outside [0, n_rows] or below the one before it raises
  * DFLASH_ERR_INVALID_ARG in the status word and nothing is written; a base_pos
  * outside [0, max_pos] raises it and is taken as the nearest value in range.
  * The softmax runs in fp32; with bf16 the weights enter their product with the
  * values as two bf16 terms (2^-16 relative).  Outputs are summed before they
  * are divided by the sum of the weights: values of more than 2^88 in size may
- * overflow on the way, and of values below 2^-60 bits may be lost.  A call is deterministic; the
- * work is cut into pieces that depend on all the lengths of the launch, so a
- * sequence's last bits may differ with the batch it runs in.
+ * overflow on the way, and of values below 2^-60 bits may be lost.  A call is
+ * deterministic; the work is cut into pieces that depend on all the lengths of
+ * the launch, so a sequence's last bits may differ with the batch it runs in.
  */
 typedef struct {
   dflash_dims dims;
