@@ -129,6 +129,11 @@ __device__ __forceinline__ void lp_move(float m, float n, float c, float& z, flo
   z *= f;
 }
 
+// (x - m) / T: by halves, whose difference stays in range.
+__device__ __forceinline__ float lp_over_t(float x, float m, float invT) {
+  return (0.5f * x - 0.5f * m) * (2.f * invT);
+}
+
 // A row's logits in 16-byte pieces from its first aligned address on; what lies
 // outside the row is -inf.
 struct LpRow {
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
         if (d.entropy) d.entropy[m_row] = bad ? NAN : lnz - 0.6931471805599453f * (s / z);
         if (d.tokens) {
           const int tok = d.tokens[m_row];
-          if (tok >= 0 && tok < d.V) d.logprob[m_row] = (__ldg(row.p + row.lead + tok) - m) * d.invT - lnz;
+          if (tok >= 0 && tok < d.V) d.logprob[m_row] = lp_over_t(__ldg(row.p + row.lead + tok), m, d.invT) - lnz;
           else if (tok != DFLASH_NO_TOKEN) raise_status(d.status, ST_RANGE);
         }
       }
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kLpThreads, HOLD ? 1 : 2) logprob_kernel(const
         }
         if (r < d.topk && DFL_CHECK(m_row < d.M && 0xFFFFFFFFu - (uint32_t)key < (uint32_t)d.V, d.status)) {
           d.top_ids[o + r] = (int)(0xFFFFFFFFu - (uint32_t)key);
-          d.top_logprobs[o + r] = (lp_value((uint32_t)(key >> 32)) - mr) * d.invT - lnz;
+          d.top_logprobs[o + r] = lp_over_t(lp_value((uint32_t)(key >> 32)), mr, d.invT) - lnz;
         }
       }
     }
