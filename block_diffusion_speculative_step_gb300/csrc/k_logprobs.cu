@@ -17,9 +17,9 @@
 // bring more candidates than the list holds: then warps insert them into
 // sorted lists of 32, one entry per lane, at worst over a second pass.
 //
-// Long calls are bound by HBM (512 rows x 151936: 62 us, 76% of the copy rate;
+// Long calls are bound by HBM (512 rows x 151936: 61 us, 76% of the copy rate;
 // a CTA's next 32 KB are in flight while it exponentiates, two CTAs an SM),
-// short ones by latency (one row: 7 us).  Bounds by sorting every thread's
+// short ones by latency (one row: 6 us).  Bounds by sorting every thread's
 // maximum and insertion of every candidate took 68 and 10 us.
 #include <cooperative_groups.h>
 #include <float.h>

@@ -30,11 +30,11 @@
 // the other's softmax.  Bound: the chain of a stream.  A chunk of both streams
 // takes 4.1k cycles (8k tokens, 32 / 8 heads), its products 3.0k (61 a product,
 // the tensor core's rate); the chain is softmax 1750, store and hand-over 290,
-// P V 980, the next S 520, commits and wake-ups 500.  8k tokens: 512 us, 1.07
-// PFLOP/s of the formula's, 1.6 of those executed (540 in loops of seconds, at
-// the power limit); without any softmax arithmetic 444; scores in steps of 16
-// columns instead of 32: 560.  Slower too: scores of 64 keys ahead in two
-// buffers a stream without turns (584 where this then took 558: a product 64
+// P V 980, the next S 520, commits and wake-ups 500.  8k tokens: 552 us at the
+// power limit, 1.0 PFLOP/s of the formula's, 1.5 of those executed (512 to 515 in
+// short loops, where the other figures were taken: without any softmax arithmetic
+// 444; scores in steps of 16 columns instead of 32: 560).  Slower too: scores of
+// 64 keys ahead in two buffers a stream without turns (584 where this then took 558: a product 64
 // columns wide takes almost as long as one of 128); P V of a chunk's first half
 // beside the softmax of its second (563, 548); two threads a row (619, 548);
 // the output by four warps of its own (553, 509: with 512 threads 128 registers
@@ -49,7 +49,7 @@
 // CTAs are joined: values up to 2^88 do not overflow on the way, over any number
 // of keys.  (2^22 instead of 2^30, for values up to 2^96, takes new references
 // more often: 8k tokens with scores of standard deviation 1 / 3 / 4: 515 / 531 /
-// 550 us with 2^30, 515 / 546 / 1018 with 2^22.)
+// 536 us with 2^30, 515 / 546 / 1018 with 2^22.)
 //
 // The softmax is no rounding point: the weights enter their product as two
 // bf16 operands, P = P_hi + P_lo (2^-16 relative), whose products share V's

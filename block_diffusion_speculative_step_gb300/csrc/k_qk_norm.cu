@@ -5,7 +5,7 @@
 // rotation partners d/2 further on, so the head's sum of squares is a few
 // shuffles and the rotation needs no exchange.  Every element is read once and
 // written once, which bounds the kernel: 8192 rows of 32 + 16 heads of 128, fp32
-// to bf16, 302 MB in 49 us, 92% of the copy rate.  A group takes two heads of a
+// to bf16, 302 MB in 48 us, 94% of the copy rate.  A group takes two heads of a
 // row, so that four 16-byte loads a thread are in flight and the position's
 // cosines are fetched once for both; 1 / 2 / 3 / 4 / 8 heads 58 / 49 / 49 / 50 /
 // 58 us, 256 threads a CTA instead of 128 51.
